@@ -333,6 +333,101 @@ BEAM_API beam_status beam_dense_forward_nvfp4(const beam_dense_shape* shape, con
 BEAM_API beam_status beam_moe_bias_update(const beam_moe_shape* shape, const void* ws,
                                           float* bias, float gamma, beam_stream stream);
 
+/* ---- a few tokens: 4-bit weights with group scales, and the layer in two kernels ----
+ *
+ * For 1 to BEAM_FEW_MAX_TOKENS tokens: a decode step of a few streams, or the verification of a
+ * drafted run of at most 15 tokens plus one (review page, speculative-decoding entry).  There a
+ * layer is bound by its weights' bytes, read once each, and by launches.
+ *
+ * 4-bit weights are integer codes with a BF16 scale per row and group of group_size (32, 64 or
+ * 128) consecutive elements of the row; activations stay BF16:
+ *   s = bf16(fl32(amax / 7)),  q = clamp(rne(fl32(x / s)), -8, 7),  value = s * q
+ * with amax the group's largest magnitude; a group with s = 0 has zero codes.  Products of
+ * codes and BF16 activations are exact; each group's sum, times its scale, is added in FP32.
+ *
+ * Packed storage (what the kernels stream): tiles of 16 rows; in a tile, superblocks of 128
+ * columns in order; a superblock is two 512-byte code blocks of 64 columns, then for each of its
+ * 128 / group_size groups 16 BF16 scales, scale 2g for row g of the tile and 2g + 1 for row g + 8.
+ * In a code block, 32-bit word v (0..3) of the 16 bytes at 16 (4g + c) (g 0..7, c 0..3) holds,
+ * with k = 32 (v / 2) + 8c + 4 (v % 2), each as code + 8:
+ *   row g:     column k in bits 0-3, k + 1 in 16-19, k + 2 in 8-11,  k + 3 in 24-27
+ *   row g + 8: column k in bits 4-7, k + 1 in 20-23, k + 2 in 12-15, k + 3 in 28-31
+ * Rows past the last are zero codes with zero scales.  Weights must be finite. */
+#define BEAM_FEW_MAX_TOKENS 16
+#define BEAM_INT4_MAX_K 32768
+
+/* Bytes of packed weights [groups, rows, cols] (0 for unsupported arguments: cols must be a
+ * multiple of 128).  Matrices converted with b hold 2 * rows rows. */
+BEAM_API size_t beam_int4_packed_size(int64_t groups, int32_t rows, int32_t cols,
+                                      int32_t group_size);
+
+/* Converts BF16 weights to packed 4-bit weights on `stream` (once per model).
+ *   a       BF16 [groups, rows, cols] (row-major), any rows >= 1
+ *   b       NULL, or a second BF16 [groups, rows, cols] (rows % 8 == 0): tile t of the output then
+ *           holds rows 8t .. 8t + 7 of a followed by the same rows of b.  Pass w_gate and w_up
+ *           [E, I, d] this way, w_down [E, d, I] alone.
+ *   packed  out: beam_int4_packed_size(groups, b ? 2 * rows : rows, cols, group_size) bytes
+ * Pointers 16-byte aligned, packed overlapping no input.  groups == 0 is a no-op. */
+BEAM_API beam_status beam_int4_quantize(const void* a, const void* b, int64_t groups, int32_t rows,
+                                        int32_t cols, int32_t group_size, void* packed,
+                                        beam_stream stream);
+
+typedef struct {
+  int32_t T;           /* tokens, 0..BEAM_FEW_MAX_TOKENS */
+  int32_t N;           /* output features: rows of the weight, any >= 1 */
+  int32_t K;           /* input features: a multiple of 128, at most BEAM_INT4_MAX_K */
+  int32_t group_size;  /* 32, 64 or 128 */
+} beam_int4_shape;
+
+/* out [T, N] = x [T, K] BF16 . W^T, W [N, K] packed by beam_int4_quantize; FP32 sums, rounded once
+ * to BF16, or stored in FP32 when out_fp32 is nonzero (an LM head's logits).  One launch, no
+ * workspace.  out may overlap neither input.
+ * With no workspace there is no status word: a device-side wait that ran out (see
+ * beam_moe_set_wait_limit_ns), which a healthy GPU never produces, shows as NaN in the outputs it
+ * concerns.  The kernel may begin to read `packed` while the previous beam_int4_linear or
+ * beam_dense_forward_int4 of the stream still runs; x is read and out written only after it. */
+BEAM_API beam_status beam_int4_linear(const beam_int4_shape* shape, const void* x,
+                                      const void* packed, void* out, int32_t out_fp32,
+                                      beam_stream stream);
+
+/* Workspace bytes for beam_dense_forward_int4 (0 for an unsupported shape). */
+BEAM_API size_t beam_dense_int4_workspace_size(const beam_dense_shape* shape);
+
+/* beam_dense_forward with 4-bit weights, T <= BEAM_FEW_MAX_TOKENS, I <= BEAM_INT4_MAX_K: gate_up
+ * packed from (w_gate, w_up) [1, I, d], down from w_down [1, d, I], both with group_size.  ws holds
+ * the activation only: beam_moe_sync_status does not apply to it (errors as in beam_int4_linear:
+ * NaN outputs). */
+BEAM_API beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int32_t group_size,
+                                             const void* hidden, const void* gate_up,
+                                             const void* down, void* out, void* ws,
+                                             size_t ws_bytes, beam_stream stream);
+
+/* Workspace bytes for beam_moe_forward_few and beam_moe_forward_few_int4 (0 for an unsupported
+ * shape: T <= BEAM_FEW_MAX_TOKENS and I <= 8192 besides the layer's shape rules). */
+BEAM_API size_t beam_moe_few_workspace_size(const beam_moe_shape* shape);
+
+/* beam_moe_forward for 1 to BEAM_FEW_MAX_TOKENS tokens in two launches: the same arguments and
+ * definition, with ws sized by beam_moe_few_workspace_size.  The router's sums run in FP64 and are
+ * rounded once to FP32, so topk_idx is the definition's also on near ties; expert outputs stay FP32
+ * until the combine's sum is rounded to BF16 (the activation between the expert's two products is
+ * BF16, as in beam_moe_forward).  Results do not depend on timing.  The second launch is
+ * cooperative: it needs every SM for itself and runs when they are free. */
+BEAM_API beam_status beam_moe_forward_few(const beam_moe_shape* shape, const void* hidden,
+                                          const float* router_w, const float* bias,
+                                          const void* w_gate, const void* w_up,
+                                          const void* w_down, void* out, int32_t* topk_idx,
+                                          float* topk_w, void* ws, size_t ws_bytes,
+                                          beam_stream stream);
+
+/* beam_moe_forward_few with 4-bit expert weights: gate_up packed from (w_gate, w_up) [E, I, d], down
+ * from w_down [E, d, I], both with group_size; the same workspace. */
+BEAM_API beam_status beam_moe_forward_few_int4(const beam_moe_shape* shape, int32_t group_size,
+                                               const void* hidden, const float* router_w,
+                                               const float* bias, const void* gate_up,
+                                               const void* down, void* out, int32_t* topk_idx,
+                                               float* topk_w, void* ws, size_t ws_bytes,
+                                               beam_stream stream);
+
 /* ---- expert parallelism: the layer's experts over P GPUs ----
  *
  * Cites: cookbook "Use HF Transformers", section Parallelism (ep_size = 8: each GPU holds 32

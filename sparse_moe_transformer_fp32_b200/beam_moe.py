@@ -37,8 +37,14 @@ EXPORTED = [
     "beam_moe_forward_nvfp4", "beam_moe_block_nvfp4", "beam_dense_nvfp4_workspace_size",
     "beam_dense_forward_nvfp4", "beam_moe_slot_rows", "beam_moe_ep_workspace_size",
     "beam_moe_ep_plan", "beam_moe_ep_count", "beam_moe_ep_dispatch", "beam_moe_ep_experts",
-    "beam_moe_ep_combine", "beam_moe_enable_peer_access",
+    "beam_moe_ep_combine", "beam_moe_enable_peer_access", "beam_int4_packed_size",
+    "beam_int4_quantize", "beam_int4_linear", "beam_dense_int4_workspace_size",
+    "beam_dense_forward_int4", "beam_moe_few_workspace_size", "beam_moe_forward_few",
+    "beam_moe_forward_few_int4",
 ]
+
+BEAM_FEW_MAX_TOKENS = 16
+BEAM_INT4_MAX_K = 32768
 
 
 class BeamError(RuntimeError):
@@ -63,6 +69,11 @@ class beam_moe_shape(ctypes.Structure):
 
 class beam_dense_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("I", ctypes.c_int32)]
+
+
+class beam_int4_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("group_size", ctypes.c_int32)]
 
 
 def make_shape(T, d, E, n_group, topk_group, top_k, I, routed_scaling_factor=2.5,
@@ -135,6 +146,18 @@ def lib():
     L.beam_moe_ep_experts.argtypes = [shp, i32, i32, i64, vp, vp, vp, vp, vp, vp, i64, vp, sz, vp]
     L.beam_moe_ep_combine.argtypes = [shp, i32, vp, vp, i64, vp, vp, sz, vp]
     L.beam_moe_enable_peer_access.argtypes = [i32]
+    ishp = ctypes.POINTER(beam_int4_shape)
+    L.beam_int4_packed_size.argtypes = [i64, i32, i32, i32]
+    L.beam_int4_packed_size.restype = sz
+    L.beam_int4_quantize.argtypes = [vp, vp, i64, i32, i32, i32, vp, vp]
+    L.beam_int4_linear.argtypes = [ishp, vp, vp, vp, i32, vp]
+    L.beam_dense_int4_workspace_size.argtypes = [dshp]
+    L.beam_dense_int4_workspace_size.restype = sz
+    L.beam_dense_forward_int4.argtypes = [dshp, i32, vp, vp, vp, vp, vp, sz, vp]
+    L.beam_moe_few_workspace_size.argtypes = [shp]
+    L.beam_moe_few_workspace_size.restype = sz
+    L.beam_moe_forward_few.argtypes = [shp] + [vp] * 10 + [sz, vp]
+    L.beam_moe_forward_few_int4.argtypes = [shp, i32] + [vp] * 9 + [sz, vp]
     L.beam_moe_set_wait_limit_ns.argtypes = [u64]
     L.beam_moe_get_wait_limit_ns.restype = u64
     L.beam_moe_launch_count.restype = u64
@@ -152,7 +175,9 @@ def lib():
                  "beam_moe_quantize_nvfp4", "beam_moe_forward_nvfp4", "beam_moe_block_nvfp4",
                  "beam_dense_forward_nvfp4", "beam_moe_slot_rows", "beam_moe_ep_plan",
                  "beam_moe_ep_count", "beam_moe_ep_dispatch", "beam_moe_ep_experts",
-                 "beam_moe_ep_combine", "beam_moe_enable_peer_access"):
+                 "beam_moe_ep_combine", "beam_moe_enable_peer_access", "beam_int4_quantize",
+                 "beam_int4_linear", "beam_dense_forward_int4", "beam_moe_forward_few",
+                 "beam_moe_forward_few_int4"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -380,6 +405,141 @@ def beam_moe_forward_nvfp4(shape, hidden, router_w, bias, gate_up, down, out, to
     _ptr(ws, torch.uint8, "ws")
     _check(lib().beam_moe_forward_nvfp4(ctypes.byref(shape), *args, ws.data_ptr(), ws.numel(),
                                         _stream(stream)), "beam_moe_forward_nvfp4")
+    return ws
+
+
+# ------------------------------------------------------------------ few tokens, 4-bit weights
+
+def _one_device(stream, *tensors):
+    """Launch target of a call: every tensor must be on the current CUDA device (its kernels run
+    there); returns the stream to launch on."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current CUDA device cuda:{dev} (got {t.device})")
+    return _stream(stream)
+
+
+def int4_shape(T, N, K, group_size=128) -> beam_int4_shape:
+    return beam_int4_shape(T, N, K, group_size)
+
+
+def beam_int4_packed_size(groups, rows, cols, group_size=128) -> int:
+    return int(lib().beam_int4_packed_size(groups, rows, cols, group_size))
+
+
+def beam_int4_quantize(a, b=None, group_size=128, out=None, stream=None):
+    """Packed 4-bit weights of BF16 weights a [groups, rows, cols] (with b of the same shape: a and b
+    interleaved in 8-row chunks, 2 * rows rows per group): uint8 [groups, bytes]."""
+    if a.dim() != 3:
+        raise ValueError("a must be [groups, rows, cols]")
+    groups, rows, cols = a.shape
+    n = beam_int4_packed_size(1, 2 * rows if b is not None else rows, cols, group_size)
+    if n == 0:
+        raise BeamError(BEAM_ERR_UNSUPPORTED, "beam_int4_packed_size")
+    if out is None:
+        out = torch.empty((groups, n), dtype=torch.uint8, device=a.device)
+    args = [_ptr(a, torch.bfloat16, "a", tuple(a.shape)),
+            _ptr(b, torch.bfloat16, "b", tuple(a.shape), optional=True),
+            groups, rows, cols, group_size, _ptr(out, torch.uint8, "out", (groups, n))]
+    _check(lib().beam_int4_quantize(*args, _one_device(stream, a, b, out)), "beam_int4_quantize")
+    return out
+
+
+def _packed(t, name, groups, rows, cols, group_size):
+    """Pointer of packed weights, whose size must be that of [groups, rows, cols]."""
+    p = _ptr(t, torch.uint8, name)
+    if t.numel() != beam_int4_packed_size(groups, rows, cols, group_size):
+        raise ValueError(f"{name} must hold {groups} x {rows} x {cols} weights in groups of {group_size} "
+                         f"(got {t.numel()} bytes)")
+    return p
+
+
+def beam_int4_linear(shape, x, packed, out, stream=None):
+    """out [T, N] (bfloat16 or float32) = x [T, K] BF16 times packed 4-bit weights [N, K]."""
+    T, N, K = shape.T, shape.N, shape.K
+    fp32 = isinstance(out, torch.Tensor) and out.dtype == torch.float32
+    args = [_ptr(x, torch.bfloat16, "x", (T, K)),
+            _packed(packed, "packed", 1, N, K, shape.group_size),
+            _ptr(out, torch.float32 if fp32 else torch.bfloat16, "out", (T, N)), 1 if fp32 else 0]
+    _check(lib().beam_int4_linear(ctypes.byref(shape), *args, _one_device(stream, x, packed, out)),
+           "beam_int4_linear")
+
+
+def dense_int4_workspace(shape: beam_dense_shape, device="cuda") -> torch.Tensor:
+    n = int(lib().beam_dense_int4_workspace_size(ctypes.byref(shape)))
+    if n == 0:
+        raise BeamError(BEAM_ERR_UNSUPPORTED, "beam_dense_int4_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def beam_dense_forward_int4(shape, group_size, hidden, gate_up, down, out, ws=None, stream=None):
+    """beam_dense_forward for at most 16 tokens with 4-bit weights: gate_up =
+    beam_int4_quantize(w_gate[None], w_up[None]), down = beam_int4_quantize(w_down[None])."""
+    T, d, I = shape.T, shape.d, shape.I
+    args = [_ptr(hidden, torch.bfloat16, "hidden", (T, d)),
+            _packed(gate_up, "gate_up", 1, 2 * I, d, group_size),
+            _packed(down, "down", 1, d, I, group_size),
+            _ptr(out, torch.bfloat16, "out", (T, d))]
+    if ws is None:
+        ws = dense_int4_workspace(shape, hidden.device)
+    _ptr(ws, torch.uint8, "ws")
+    _check(lib().beam_dense_forward_int4(ctypes.byref(shape), group_size, *args, ws.data_ptr(),
+                                         ws.numel(),
+                                         _one_device(stream, hidden, gate_up, down, out, ws)),
+           "beam_dense_forward_int4")
+    return ws
+
+
+def few_workspace(shape: beam_moe_shape, device="cuda") -> torch.Tensor:
+    """Workspace of beam_moe_forward_few and beam_moe_forward_few_int4."""
+    n = int(lib().beam_moe_few_workspace_size(ctypes.byref(shape)))
+    if n == 0:
+        raise BeamError(BEAM_ERR_UNSUPPORTED, "beam_moe_few_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def beam_moe_forward_few(shape, hidden, router_w, bias, w_gate, w_up, w_down, out, topk_idx=None,
+                         topk_w=None, ws=None, stream=None):
+    """beam_moe_forward for at most 16 tokens, in two launches."""
+    T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
+    args = [_ptr(hidden, torch.bfloat16, "hidden", (T, d)),
+            _ptr(router_w, torch.float32, "router_w", (E, d)),
+            _ptr(bias, torch.float32, "bias", (E,)),
+            _ptr(w_gate, torch.bfloat16, "w_gate", (E, I, d)),
+            _ptr(w_up, torch.bfloat16, "w_up", (E, I, d)),
+            _ptr(w_down, torch.bfloat16, "w_down", (E, d, I)),
+            _ptr(out, torch.bfloat16, "out", (T, d)),
+            _ptr(topk_idx, torch.int32, "topk_idx", (T, k), optional=True),
+            _ptr(topk_w, torch.float32, "topk_w", (T, k), optional=True)]
+    if ws is None:
+        ws = few_workspace(shape, hidden.device)
+    _ptr(ws, torch.uint8, "ws")
+    st = _one_device(stream, hidden, router_w, bias, w_gate, w_up, w_down, out, topk_idx, topk_w, ws)
+    _check(lib().beam_moe_forward_few(ctypes.byref(shape), *args, ws.data_ptr(), ws.numel(), st),
+           "beam_moe_forward_few")
+    return ws
+
+
+def beam_moe_forward_few_int4(shape, group_size, hidden, router_w, bias, gate_up, down, out,
+                              topk_idx=None, topk_w=None, ws=None, stream=None):
+    """beam_moe_forward_few with 4-bit experts: gate_up = beam_int4_quantize(w_gate, w_up, group_size),
+    down = beam_int4_quantize(w_down, group_size=group_size)."""
+    T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
+    args = [_ptr(hidden, torch.bfloat16, "hidden", (T, d)),
+            _ptr(router_w, torch.float32, "router_w", (E, d)),
+            _ptr(bias, torch.float32, "bias", (E,)),
+            _packed(gate_up, "gate_up", E, 2 * I, d, group_size),
+            _packed(down, "down", E, d, I, group_size),
+            _ptr(out, torch.bfloat16, "out", (T, d)),
+            _ptr(topk_idx, torch.int32, "topk_idx", (T, k), optional=True),
+            _ptr(topk_w, torch.float32, "topk_w", (T, k), optional=True)]
+    if ws is None:
+        ws = few_workspace(shape, hidden.device)
+    _ptr(ws, torch.uint8, "ws")
+    st = _one_device(stream, hidden, router_w, bias, gate_up, down, out, topk_idx, topk_w, ws)
+    _check(lib().beam_moe_forward_few_int4(ctypes.byref(shape), group_size, *args, ws.data_ptr(),
+                                           ws.numel(), st), "beam_moe_forward_few_int4")
     return ws
 
 

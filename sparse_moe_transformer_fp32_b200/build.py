@@ -20,9 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbeam_moe.so")
 SOURCES = ["beam_moe_api.cu", "router.cu", "dispatch.cu", "expert_gemm.cu", "expert_gemm_2sm.cu",
-           "combine.cu", "nvfp4.cu", "ep.cu"]
+           "combine.cu", "nvfp4.cu", "ep.cu", "int4.cu", "few.cu"]
 HEADERS = [os.path.join(CSRC, "beam_moe_internal.cuh"), os.path.join(CSRC, "beam_moe_nvfp4.cuh"),
            os.path.join(CSRC, "beam_moe_div.cuh"), os.path.join(CSRC, "beam_moe_router.cuh"),
+           os.path.join(CSRC, "beam_moe_few.cuh"),
            os.path.join(INCLUDE, "beam_moe.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -4,6 +4,7 @@
 #include "beam_moe_internal.cuh"
 #include "beam_moe_router.cuh"
 #include "beam_moe_nvfp4.cuh"
+#include "beam_moe_few.cuh"
 
 #include <cudaTypedefs.h>
 
@@ -45,13 +46,17 @@ enum KernelId {
   kKEpPush,
   kKEpLocalCounts,
   kKEpCombine,
+  kKQuantizeInt4,
+  kKInt4Linear,
+  kKFewRouter,
+  kKFewLayer,
   kNumKernels
 };
 const char* const kKernelNames[kNumKernels] = {
     "router_gemm", "router_select", "dispatch_scan", "permute", "expert_gemm_gate_up",
     "expert_gemm_down", "combine", "combine_block", "prenorm", "router_transpose", "dense_tiles",
     "bias_update", "quantize_e4m3", "quantize_nvfp4", "ep_count", "ep_offsets", "ep_push",
-    "ep_local_counts", "ep_combine"};
+    "ep_local_counts", "ep_combine", "quantize_int4", "int4_linear", "few_router", "few_layer"};
 
 struct Profiler {
   std::mutex mu;
@@ -337,6 +342,10 @@ beam_status device_info(DeviceInfo** out) {
     e = prepare_gemm_2sm_kernels();
     if (e != cudaSuccess) return cuda_fail(e);
     e = prepare_gemm_nvfp4_kernels();
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = prepare_int4_kernels();
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = prepare_few_kernels();
     if (e != cudaSuccess) return cuda_fail(e);
     d.pair_grid = max_pair_grid(d.sms);
     d.prepared = true;
@@ -1152,9 +1161,257 @@ beam_status check_ep_ws(const EpLayout& L, void* ws, size_t ws_bytes) {
   return BEAM_OK;
 }
 
+// ------------------------------------------------------------------ few tokens, 4-bit weights
+
+bool int4_group_ok(int32_t group_size, int64_t cols) {
+  return (group_size == 32 || group_size == 64 || group_size == 128) && cols > 0 &&
+         cols % kI4Unit == 0;
+}
+
+// Bytes of packed 4-bit weights [rows, cols]: whole 16-row tiles.
+size_t int4_bytes(int64_t rows, int64_t cols, int32_t group_size) {
+  return static_cast<size_t>(ceil_div(rows, 16)) * (cols / kI4Unit) * i4_unit_bytes(group_size);
+}
+
+bool ranges_overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
+
+beam_status unsupported(const char* why) {
+  std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "%s", why);
+  return BEAM_ERR_UNSUPPORTED;
+}
+
+beam_status check_int4_linear(const beam_int4_shape* s) {
+  if (!s) return BEAM_ERR_INVALID_ARG;
+  if (s->T < 0 || s->N <= 0 || s->K <= 0) return BEAM_ERR_INVALID_ARG;
+  if (!int4_group_ok(s->group_size, s->K))
+    return unsupported("4-bit weights: group_size must be 32, 64 or 128 and K a multiple of 128");
+  if (s->T > kFewMaxTokens) return unsupported("4-bit products: at most 16 tokens");
+  if (s->K > BEAM_INT4_MAX_K) return unsupported("4-bit products: K above BEAM_INT4_MAX_K");
+  return BEAM_OK;
+}
+
+beam_status run_int4_linear(const DeviceInfo& dev, const beam_int4_shape& s, const void* x,
+                            const void* w, void* out, Int4Out kind, cudaStream_t st) {
+  Int4LinearArgs la{};
+  la.x = static_cast<const __nv_bfloat16*>(x);
+  la.w = static_cast<const uint8_t*>(w);
+  la.out = out;
+  la.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  la.T = s.T;
+  la.N = s.N;
+  la.K = s.K;
+  la.tiles = static_cast<int>(ceil_div(s.N, 16));
+  la.out_kind = kind;
+  BEAM_LAUNCH(kKInt4Linear, st, launch_int4_linear(la, s.group_size, dev.sms, st));
+  return BEAM_OK;
+}
+
+beam_status check_dense_int4(const beam_dense_shape* s, int32_t group_size) {
+  const beam_status b = check_dense_shape(s);
+  if (b != BEAM_OK) return b;
+  if (!int4_group_ok(group_size, s->d))
+    return unsupported("4-bit weights: group_size must be 32, 64 or 128");
+  if (s->T > kFewMaxTokens) return unsupported("4-bit products: at most 16 tokens");
+  if (s->I > BEAM_INT4_MAX_K) return unsupported("4-bit products: I above BEAM_INT4_MAX_K");
+  return BEAM_OK;
+}
+
+struct FewLayout {
+  size_t ctl, sc, act, y, total;
+  int ctl_words;
+};
+
+beam_status check_few_shape(const beam_moe_shape* s) {
+  const beam_status b = check_shape(s);
+  if (b != BEAM_OK) return b;
+  if (s->T > kFewMaxTokens) return unsupported("few-token layer: at most 16 tokens");
+  if (s->I > kFewMaxK) return unsupported("few-token layer: I above 8192");
+  return BEAM_OK;
+}
+
+// Status words first, as in every workspace, then the counters (cleared together).
+FewLayout plan_few(const beam_moe_shape& s) {
+  FewLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = o;
+    o = align_up(o + (bytes ? bytes : 1), 1024);
+    return r;
+  };
+  const size_t R = static_cast<size_t>(s.T) * s.top_k;
+  L.ctl_words = 4 + kFewMaxSlots + s.d / 16;
+  L.ctl = take(sizeof(uint32_t) * L.ctl_words);
+  L.sc = take(sizeof(float2) * s.T * s.E);
+  L.act = take(sizeof(__nv_bfloat16) * R * s.I);
+  L.y = take(sizeof(float) * R * s.d);
+  L.total = o;
+  return L;
+}
+
+// BF16 (group_size 0: w_gate, w_up, w_down) and 4-bit (w_gate: packed gate|up) forms.
+beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void* hidden,
+                     const float* router_w, const float* bias, const void* w_gate,
+                     const void* w_up, const void* w_down, void* out, int32_t* topk_idx,
+                     float* topk_w, void* ws, size_t ws_bytes, beam_stream stream) {
+  beam_status b = check_few_shape(shape);
+  if (b != BEAM_OK) return b;
+  if (shape->T == 0) return BEAM_OK;  // nothing to read or write
+  if (any_misaligned({hidden, router_w, w_gate, w_down, out}) || (!group_size && any_misaligned({w_up})) ||
+      !bias || (topk_idx && !aligned16(topk_idx)) || (topk_w && !aligned16(topk_w)))
+    return BEAM_ERR_INVALID_ARG;
+  const FewLayout L = plan_few(*shape);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < L.total)
+    return BEAM_ERR_WORKSPACE;
+  DeviceInfo* dev;
+  if ((b = device_info(&dev)) != BEAM_OK) return b;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  FewRouterArgs ra{};
+  ra.h = static_cast<const __nv_bfloat16*>(hidden);
+  ra.W = router_w;
+  ra.bias = bias;
+  ra.sc = at<float2>(ws, L.sc);
+  ra.ctl = at<uint32_t>(ws, L.ctl);
+  ra.ctl_words = L.ctl_words;
+  ra.T = shape->T;
+  ra.d = shape->d;
+  ra.E = shape->E;
+  BEAM_LAUNCH(kKFewRouter, st, launch_few_router(ra, st));
+  FewLayerArgs la{};
+  la.h = ra.h;
+  la.sc = ra.sc;
+  la.w_gate = w_gate;
+  la.w_up = w_up;
+  la.w_down = w_down;
+  la.act = at<__nv_bfloat16>(ws, L.act);
+  la.y = at<float>(ws, L.y);
+  la.out = static_cast<__nv_bfloat16*>(out);
+  la.idx = topk_idx;
+  la.wts = topk_w;
+  la.status = ra.ctl;
+  la.ready = ra.ctl + 4;
+  la.done = ra.ctl + 4 + kFewMaxSlots;
+  la.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  la.T = shape->T;
+  la.d = shape->d;
+  la.E = shape->E;
+  la.G = shape->n_group;
+  la.Gk = shape->topk_group;
+  la.k = shape->top_k;
+  la.I = shape->I;
+  la.scale = shape->routed_scaling_factor;
+  la.norm = shape->norm_topk_prob ? 1 : 0;
+  BEAM_LAUNCH(kKFewLayer, st, launch_few_layer(la, group_size, dev->sms, st));
+  return BEAM_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t beam_int4_packed_size(int64_t groups, int32_t rows, int32_t cols, int32_t group_size) {
+  if (groups < 0 || rows <= 0 || !int4_group_ok(group_size, cols)) return 0;
+  return static_cast<size_t>(groups) * int4_bytes(rows, cols, group_size);
+}
+
+beam_status beam_int4_quantize(const void* a, const void* b, int64_t groups, int32_t rows,
+                               int32_t cols, int32_t group_size, void* packed,
+                               beam_stream stream) {
+  if (groups < 0 || rows <= 0 || cols <= 0) return BEAM_ERR_INVALID_ARG;
+  if (!int4_group_ok(group_size, cols))
+    return unsupported("4-bit weights: group_size must be 32, 64 or 128 and cols a multiple of 128");
+  if (b && rows % 8 != 0)
+    return unsupported("4-bit weights: interleaving needs rows to be a multiple of 8");
+  if (b && rows > (1 << 30)) return BEAM_ERR_UNSUPPORTED;
+  if (groups == 0) return BEAM_OK;
+  if (any_misaligned({a, packed}) || (b && !aligned16(b))) return BEAM_ERR_INVALID_ARG;
+  const uint64_t in_bytes = static_cast<uint64_t>(groups) * rows * cols * 2;
+  const int32_t out_rows = b ? 2 * rows : rows;
+  const uint64_t out_bytes = static_cast<uint64_t>(groups) * int4_bytes(out_rows, cols, group_size);
+  if (ranges_overlap(packed, out_bytes, a, in_bytes) || ranges_overlap(packed, out_bytes, b, in_bytes))
+    return BEAM_ERR_INVALID_ARG;
+  Int4QuantArgs qa{};
+  qa.a = static_cast<const __nv_bfloat16*>(a);
+  qa.b = static_cast<const __nv_bfloat16*>(b);
+  qa.packed = static_cast<uint8_t*>(packed);
+  qa.rows = rows;
+  qa.cols = cols;
+  qa.tiles = static_cast<int>(ceil_div(out_rows, 16));
+  qa.units = groups * qa.tiles * (cols / kI4Unit);
+  qa.group = group_size;
+  if (ceil_div(qa.units, 8) > 0x7fffffff) return BEAM_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  BEAM_LAUNCH(kKQuantizeInt4, st, launch_int4_quantize(qa, st));
+  return BEAM_OK;
+}
+
+beam_status beam_int4_linear(const beam_int4_shape* shape, const void* x, const void* packed,
+                             void* out, int32_t out_fp32, beam_stream stream) {
+  beam_status b = check_int4_linear(shape);
+  if (b != BEAM_OK) return b;
+  if (shape->T == 0) return BEAM_OK;  // nothing to read or write
+  if (any_misaligned({x, packed, out})) return BEAM_ERR_INVALID_ARG;
+  const uint64_t out_bytes = static_cast<uint64_t>(shape->T) * shape->N * (out_fp32 ? 4 : 2);
+  if (ranges_overlap(out, out_bytes, x, static_cast<uint64_t>(shape->T) * shape->K * 2) ||
+      ranges_overlap(out, out_bytes, packed, int4_bytes(shape->N, shape->K, shape->group_size)))
+    return BEAM_ERR_INVALID_ARG;
+  DeviceInfo* dev;
+  if ((b = device_info(&dev)) != BEAM_OK) return b;
+  return run_int4_linear(*dev, *shape, x, packed, out, out_fp32 ? kI4OutF32 : kI4OutBf16,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t beam_dense_int4_workspace_size(const beam_dense_shape* shape) {
+  if (check_dense_int4(shape, 128) != BEAM_OK) return 0;
+  return align_up(sizeof(__nv_bfloat16) * static_cast<size_t>(shape->T ? shape->T : 1) * shape->I, 1024);
+}
+
+beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int32_t group_size,
+                                    const void* hidden, const void* gate_up, const void* down,
+                                    void* out, void* ws, size_t ws_bytes, beam_stream stream) {
+  beam_status b = check_dense_int4(shape, group_size);
+  if (b != BEAM_OK) return b;
+  if (shape->T == 0) return BEAM_OK;  // nothing to read or write
+  if (any_misaligned({hidden, gate_up, down, out})) return BEAM_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
+      ws_bytes < beam_dense_int4_workspace_size(shape))
+    return BEAM_ERR_WORKSPACE;
+  DeviceInfo* dev;
+  if ((b = device_info(&dev)) != BEAM_OK) return b;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const beam_int4_shape up{shape->T, 2 * shape->I, shape->d, group_size};
+  const beam_int4_shape dn{shape->T, shape->d, shape->I, group_size};
+  if ((b = run_int4_linear(*dev, up, hidden, gate_up, ws, kI4OutSwiglu, st)) != BEAM_OK) return b;
+  return run_int4_linear(*dev, dn, ws, down, out, kI4OutBf16, st);
+}
+
+size_t beam_moe_few_workspace_size(const beam_moe_shape* shape) {
+  if (check_few_shape(shape) != BEAM_OK) return 0;
+  return plan_few(*shape).total;
+}
+
+beam_status beam_moe_forward_few(const beam_moe_shape* shape, const void* hidden,
+                                 const float* router_w, const float* bias, const void* w_gate,
+                                 const void* w_up, const void* w_down, void* out,
+                                 int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                                 beam_stream stream) {
+  return few_impl(shape, 0, hidden, router_w, bias, w_gate, w_up, w_down, out, topk_idx, topk_w, ws,
+                  ws_bytes, stream);
+}
+
+beam_status beam_moe_forward_few_int4(const beam_moe_shape* shape, int32_t group_size,
+                                      const void* hidden, const float* router_w, const float* bias,
+                                      const void* gate_up, const void* down, void* out,
+                                      int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                                      beam_stream stream) {
+  if (!shape) return BEAM_ERR_INVALID_ARG;
+  if (!int4_group_ok(group_size, 128))
+    return unsupported("4-bit weights: group_size must be 32, 64 or 128");
+  return few_impl(shape, group_size, hidden, router_w, bias, gate_up, nullptr, down, out, topk_idx,
+                  topk_w, ws, ws_bytes, stream);
+}
 
 int beam_moe_abi_version(void) { return 1; }
 

@@ -1,0 +1,612 @@
+// The whole MoE layer for 1 to 16 tokens in two kernels: router scores, then everything else.
+#include "beam_moe_few.cuh"
+
+#include <math_constants.h>
+
+namespace beam {
+namespace {
+
+// ------------------------------------------------------------------ router scores
+
+// logits = h W_r^T, s = sigmoid(logit), sb = s + bias.  The sums run in FP64 and are rounded to
+// FP32 once, and so is the sigmoid: with a few tokens the FP64 units are far from busy (one FMA
+// per router weight and token: 21 M at T = 16, under 2 us) and the scores then equal the exactly
+// rounded ones, so that near ties fall as the definition has them.  Two experts per CTA: 128 CTAs
+// for 256 experts, each reading 2 d FP32 weights; latency-bound at 5.2 MB in all.
+//
+// Block 0 also clears the control words that the layer kernel counts in.
+constexpr int kRtThreads = 256, kRtExperts = 2;
+
+template <int TM>
+__global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterArgs a) {
+  __shared__ double part[kRtThreads / 32][kRtExperts * TM];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.ctl_words; i += kRtThreads) a.ctl[i] = 0u;
+  const int e0 = blockIdx.x * kRtExperts;
+  double acc[kRtExperts][TM];
+#pragma unroll
+  for (int j = 0; j < kRtExperts; ++j)
+#pragma unroll
+    for (int t = 0; t < TM; ++t) acc[j][t] = 0.0;
+#pragma unroll 2
+  for (int k = threadIdx.x * 4; k < a.d; k += kRtThreads * 4) {
+    float4 w[kRtExperts];
+#pragma unroll
+    for (int j = 0; j < kRtExperts; ++j)
+      w[j] = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e0 + j) * a.d + k));
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      if (t < a.T) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.h + static_cast<size_t>(t) * a.d + k));
+        const double h0 = bf16_lo(v.x), h1 = bf16_hi(v.x), h2 = bf16_lo(v.y), h3 = bf16_hi(v.y);
+#pragma unroll
+        for (int j = 0; j < kRtExperts; ++j) {
+          acc[j][t] = fma(static_cast<double>(w[j].x), h0, acc[j][t]);
+          acc[j][t] = fma(static_cast<double>(w[j].y), h1, acc[j][t]);
+          acc[j][t] = fma(static_cast<double>(w[j].z), h2, acc[j][t]);
+          acc[j][t] = fma(static_cast<double>(w[j].w), h3, acc[j][t]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRtExperts; ++j)
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      double v = acc[j][t];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) part[warp][j * TM + t] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x < kRtExperts * TM) {
+    const int j = threadIdx.x / TM, t = threadIdx.x % TM;
+    if (t < a.T) {
+      double v = 0.0;
+#pragma unroll
+      for (int w = 0; w < kRtThreads / 32; ++w) v += part[w][threadIdx.x];
+      const float logit = static_cast<float>(v);
+      const float s = static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logit))));
+      a.sc[static_cast<size_t>(t) * a.E + e0 + j] = make_float2(s, s + a.bias[e0 + j]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the layer
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Order-preserving map of a score to unsigned; NaN above everything, nothing maps to 0.
+__device__ __forceinline__ uint32_t score_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  if (v != v) return 0xffffffffu;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..24
+
+struct FewShared {
+  uint64_t full_bar[kFewMaxStages], empty_bar[kFewMaxStages];
+  uint64_t red_full[kFewRed], red_empty[kFewRed];
+  float wts[kFewMaxSlots];              // routing weight of slot t * k + j
+  uint32_t mask[kMaxE];                 // tokens of each expert
+  uint8_t chosen[kFewMaxTokens][kMaxTopK];  // chosen experts of each token, ascending
+  uint8_t entry_e[kFewMaxSlots];        // expert of each entry
+  uint8_t entry_n[kFewMaxSlots];        // its tokens, 1..8
+  uint8_t entry_slot[kFewMaxSlots][kFewCols];  // their slots
+  uint16_t last[kMaxD / 16];            // output tiles that this CTA completes
+  int n_entries, n_last, abort_flag;
+};
+
+// Selection of token `t` by one warp from its E (score, biased score) pairs in `sc`:
+// the Gk groups with the largest sums of their two best biased scores, the k best experts in
+// them, ties to the lower index; ascending experts and normalised weights out.
+__device__ void few_select(const FewLayerArgs& a, const float2* sc, FewShared& sh, int t, int lane) {
+  const int P = a.E / a.G;
+  uint32_t gkey = 0;
+  if (lane < a.G) {
+    float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
+    bool nan = false;
+    for (int j = 0; j < P; ++j) {
+      int jj = j + lane;  // start at different banks
+      jj -= jj >= P ? (jj / P) * P : 0;
+      const float v = sc[lane * P + jj].y;
+      nan |= v != v;
+      if (v > m1) {
+        m2 = m1;
+        m1 = v;
+      } else if (v > m2) {
+        m2 = v;
+      }
+    }
+    gkey = nan ? 0xffffffffu : score_key(P >= 2 ? m1 + m2 : m1);
+  }
+  int grank = 0;
+  for (int g = 0; g < a.G; ++g) {
+    const uint32_t o = __shfl_sync(0xffffffffu, gkey, g);
+    if (o > gkey || (o == gkey && g < lane)) ++grank;
+  }
+  const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.G && grank < a.Gk);
+  // experts lane, lane + 32, ...: ties between lanes fall to the lower expert below
+  uint32_t key[kMaxE / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxE / 32; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < a.E && ((kept >> (e / P)) & 1u) ? score_key(sc[e].y) : 0u;
+  }
+  uint32_t chosen = 0;  // bit i: expert lane + 32 i
+  for (int r = 0; r < a.k; ++r) {
+    uint32_t best = 0;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        bi = i;
+      }
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t cand = best == m ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffffffu;
+    const uint32_t win = __reduce_min_sync(0xffffffffu, cand);
+    if (cand == win) {
+      chosen |= 1u << bi;
+#pragma unroll
+      for (int i = 0; i < kMaxE / 32; ++i)
+        if (i == bi) key[i] = 0u;
+    }
+  }
+  // ascending expert ids, and the sum of the chosen scores in that order
+  int at = 0;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxE / 32; ++i) {
+    uint32_t b = __ballot_sync(0xffffffffu, (chosen >> i) & 1u);
+    while (b) {
+      const int e = (__ffs(b) - 1) + 32 * i;
+      b &= b - 1;
+      sum += sc[e].x;
+      if (lane == 0) {
+        sh.chosen[t][at] = static_cast<uint8_t>(e);
+        atomicOr(&sh.mask[e], 1u << t);
+      }
+      ++at;
+    }
+  }
+  __syncwarp();
+  if (lane < a.k) {
+    const int e = sh.chosen[t][lane];
+    const float s = sc[e].x;
+    const float w = a.norm ? a.scale * s / sum : a.scale * s;
+    sh.wts[t * a.k + lane] = w;
+    if (blockIdx.x == 0) {
+      if (a.idx) a.idx[t * a.k + lane] = e;
+      if (a.wts) a.wts[t * a.k + lane] = w;
+    }
+  }
+}
+
+// Lists the touched experts ascending, 8 tokens at most to an entry (a ninth token of an expert
+// opens a second entry that reads its weights again: with at most 16 tokens that takes a
+// routing where more than half of them agree).  Run by one warp.
+__device__ void few_entries(const FewLayerArgs& a, FewShared& sh, int lane) {
+  int base = 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    uint32_t m = e < a.E ? sh.mask[e] : 0u;
+    const int need = (__popc(m) + kFewCols - 1) / kFewCols;
+    int incl = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int at = base + incl - need;
+    for (int p = 0; p < need; ++p, ++at) {
+      int n = 0;
+      while (m && n < kFewCols) {
+        const int t = __ffs(m) - 1;
+        m &= m - 1;
+        int j = 0;
+        while (sh.chosen[t][j] != e) ++j;
+        sh.entry_slot[at][n++] = static_cast<uint8_t>(t * a.k + j);
+      }
+      sh.entry_e[at] = static_cast<uint8_t>(e);
+      sh.entry_n[at] = static_cast<uint8_t>(n);
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) sh.n_entries = base;
+}
+
+// Everything after the router scores, in one cooperative persistent kernel:
+//   selection        every CTA for itself (E scores per token; no exchange needed)
+//   gate|up          items (entry, 8 intermediate rows): a 16-row tile holds 8 gate rows and the
+//                    same 8 up rows, so one lane ends up with both and applies SwiGLU; BF16
+//                    activations, the down product's MMA operand, as the layer defines them
+//   down             items (entry, 16 output rows); an item needs its entry's activations
+//                    complete, which a counter per entry tells; FP32 partial outputs per slot
+//   combine          per output tile by the CTA that finishes its last item: each token's k
+//                    slots in ascending expert order, FP32, rounded to BF16 once
+// Each CTA takes one contiguous run of items of either phase, cut so that both runs together are
+// the same number of weight bytes for every CTA; its producer goes from the first into the second
+// without waiting for anything but ring space, so the weights keep streaming while activations
+// cross the GPU.  GROUP = 0: BF16 weights.  HBM-bound on the touched experts' bytes.
+template <int GROUP>
+__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLayerArgs a) {
+  constexpr bool kI4 = GROUP != 0;
+  constexpr int kUnit = kI4 ? kI4Unit : kBf16Unit;                       // K elements
+  constexpr int kUnitBytes = kI4 ? i4_unit_bytes(kI4 ? GROUP : 128) : 0;  // packed bytes
+  constexpr int kRuns = kFewMaxK / kFewWarps / 32;                       // runs of 32 per warp
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ FewShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t red = ring + a.stages * a.slot_bytes;
+  volatile int* abort_flag = &sh.abort_flag;
+
+  for (int e = threadIdx.x; e < kMaxE; e += kFewThreads) sh.mask[e] = 0u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(smem_u32(&sh.full_bar[i]), 1);
+      mbar_init(smem_u32(&sh.empty_bar[i]), kFewWarps);
+    }
+    for (int i = 0; i < kFewRed; ++i) {
+      mbar_init(smem_u32(&sh.red_full[i]), kFewWarps);
+      mbar_init(smem_u32(&sh.red_empty[i]), 1);
+    }
+    sh.abort_flag = 0;
+    sh.n_last = 0;
+    fence_mbarrier_init();
+  }
+  // the tokens' scores, in the ring's space until the weights need it
+  float2* sc = reinterpret_cast<float2*>(smem);
+  for (int i = threadIdx.x; i < a.T * a.E; i += kFewThreads) sc[i] = a.sc[i];
+  __syncthreads();
+  if (warp < a.T) few_select(a, sc + warp * a.E, sh, warp, lane);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic reads before bulk writes
+  __syncthreads();
+  if (warp == 0) few_entries(a, sh, lane);
+  __syncthreads();
+
+  // ---- this CTA's items
+  const int n_gu = a.I / 8, n_dn = a.d / 16;
+  const int64_t N1 = static_cast<int64_t>(sh.n_entries) * n_gu;
+  const int64_t N2 = static_cast<int64_t>(sh.n_entries) * n_dn;
+  const int64_t grid = gridDim.x;
+  auto first1 = [&](int64_t b) { return b * N1 / grid; };
+  // Down items start where the CTAs before b have b / grid of all bytes (an item's are 16 K;
+  // gate|up: K = d, down: K = I).  That is monotone in b as long as a CTA's down bytes cover the
+  // one gate|up item by which the first runs differ; below that, an even cut.
+  auto first2 = [&](int64_t b) {
+    if (N2 * a.I < grid * a.d) return b * N2 / grid;
+    const int64_t v = (b * (N1 * a.d + N2 * a.I) / grid - first1(b) * a.d) / a.I;
+    return b == grid || v > N2 ? N2 : v;
+  };
+  const int i1 = static_cast<int>(first1(blockIdx.x)), j1 = static_cast<int>(first1(blockIdx.x + 1));
+  const int i2 = static_cast<int>(first2(blockIdx.x)), j2 = static_cast<int>(first2(blockIdx.x + 1));
+
+  if (warp == kFewWarps) {
+    // ---- producer
+    int slot = 0;
+    uint32_t par = 1, issued = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const KSplit ks = ph ? a.k2 : a.k1;
+      const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
+      const int cw = 1 << ks.log_cw;
+      int entry = (ph ? i2 : i1) / per, tile = (ph ? i2 : i1) % per;
+#pragma unroll 1
+      for (int it = ph ? i2 : i1; it < (ph ? j2 : j1) && ok; ++it) {
+        const int e = sh.entry_e[entry];
+        const uint8_t* src;
+        if (kI4) {
+          src = static_cast<const uint8_t*>(ph ? a.w_down : a.w_gate) +
+                (static_cast<size_t>(e) * per + tile) * ks.n * kUnitBytes;
+        } else {  // lane r < 16 copies row r of the tile
+          const int r = lane & 15;
+          const void* m = ph ? a.w_down : (r < 8 ? a.w_gate : a.w_up);
+          const size_t row = ph ? static_cast<size_t>(e) * a.d + tile * 16 + r
+                                : static_cast<size_t>(e) * a.I + tile * 8 + (r & 7);
+          src = static_cast<const uint8_t*>(m) + row * K * 2;
+        }
+        for (int w = 0; w < kFewWarps; w += cw) {
+          ok = mbar_wait_warp(smem_u32(&sh.empty_bar[slot]), par, abort_flag, a.wait_limit_ns,
+                              a.status, kWhereFew);
+          if (!ok) break;
+          const int s = ks.start(w), n = ks.start(w + cw) - s;
+          const uint32_t bar = smem_u32(&sh.full_bar[slot]);
+          const uint32_t dst = ring + slot * a.slot_bytes;
+          if (lane == 0) mbar_arrive_expect_tx(bar, kI4 ? n * kUnitBytes : 16 * n * 64);
+          __syncwarp();
+          if (kI4) {
+            if (lane == 0)
+              bulk_load(dst, src + static_cast<size_t>(s) * kUnitBytes, n * kUnitBytes, bar);
+          } else if (lane < 16 && n > 0) {
+            bulk_load(dst + lane * bf16_row_stride(n), src + static_cast<size_t>(s) * 64, n * 64, bar);
+          }
+          ++issued;
+          if (++slot == a.stages) {
+            slot = 0;
+            par ^= 1;
+          }
+        }
+        if (++tile == per) {
+          tile = 0;
+          ++entry;
+        }
+      }
+    }
+    if (!ok) {  // copies in flight must land before this CTA's shared memory is given up
+      volatile int never = 0;
+      const uint32_t back = issued < static_cast<uint32_t>(a.stages) ? issued : a.stages;
+      for (uint32_t i = issued - back; i < issued; ++i)
+        mbar_wait_bounded(smem_u32(&sh.full_bar[i % a.stages]), (i / a.stages) & 1, &never,
+                          2000000000ull, nullptr, 0);
+    }
+  } else if (warp < kFewWarps) {
+    // ---- consumers
+    uint32_t b[1][kRuns * 4];
+    int slot = 0, rb = 0;
+    uint32_t par = 0, rpar = 1;
+    bool ok = true;
+#pragma unroll 1
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const KSplit ks = ph ? a.k2 : a.k1;
+      const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
+      const int first = ph ? i2 : i1, last = ph ? j2 : j1;
+      const int units = ks.count(warp), mine = warp >> ks.log_cw, chunks = ks.chunks();
+      const int cstart = ks.start(mine << ks.log_cw);
+      const int cunits = ks.start((mine + 1) << ks.log_cw) - cstart;
+      const int uoff = ks.start(warp) - cstart;
+      const uint32_t off = kI4 ? uoff * kUnitBytes : uoff * 64;
+      const int stride = bf16_row_stride(cunits);
+      const int k0 = ks.start(warp) * kUnit;
+      int entry = first / per, tile = first % per, loaded = -1;
+#pragma unroll 1
+      for (int it = first; it < last; ++it) {
+        if (entry != loaded) {  // token fragments of the entry
+          loaded = entry;
+          if (ph) {
+            // activations of the entry complete?
+            ok = true;
+            if (lane == 0) {
+              const uint32_t want = n_gu;
+              uint64_t t0 = 0;
+              while (ld_acquire(a.ready + entry) < want) {
+                const uint64_t now = globaltimer_ns();
+                if (!t0) t0 = now;
+                if (*abort_flag || ld_acquire(a.status)) {  // here or in another CTA
+                  *abort_flag = 1;
+                  ok = false;
+                  break;
+                }
+                if (now - t0 >= a.wait_limit_ns) {
+                  *abort_flag = 1;
+                  record_status(a.status, kDevTimeout, kWhereFew + 1);
+                  ok = false;
+                  break;
+                }
+                __nanosleep(40);
+              }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          const int col = lane >> 2;
+          const __nv_bfloat16* row = nullptr;
+          if (col < sh.entry_n[entry]) {
+            const int s = sh.entry_slot[entry][col];
+            row = ph ? a.act + static_cast<size_t>(s) * K + k0
+                     : a.h + static_cast<size_t>(s / a.k) * K + k0;
+          }
+          load_tokens<kRuns, true>(b[0], row, units * (kUnit / 32), lane & 3);
+        }
+        float acc[1][4] = {};
+        // every warp passes every chunk in order: a phase may only be waited for by who has seen
+        // the slot's phase before
+#pragma unroll 1
+        for (int ch = 0; ch < chunks; ++ch) {
+          ok = mbar_wait_warp(smem_u32(&sh.full_bar[slot]), par, abort_flag, a.wait_limit_ns, a.status,
+                              kWhereFew + 2);
+          if (!ok) break;
+          if (ch == mine) {
+            const uint32_t base = ring + slot * a.slot_bytes + off;
+            if constexpr (kI4)
+              i4_slice<1, kRuns / 4, kI4 ? GROUP : 128>(acc, b, base, units, lane);
+            else
+              bf16_slice<kRuns>(acc[0], b[0], base, stride, units, lane);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.empty_bar[slot]));
+          if (++slot == a.stages) {
+            slot = 0;
+            par ^= 1;
+          }
+        }
+        if (!ok) break;
+        ok = mbar_wait_warp(smem_u32(&sh.red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
+                            kWhereFew + 3);
+        if (!ok) break;
+        if (units > 0)
+          sts128(red + (rb * kFewWarps + warp) * 512 + lane * 16,
+                 make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.red_full[rb]));
+        if (++rb == kFewRed) {
+          rb = 0;
+          rpar ^= 1;
+        }
+        if (++tile == per) {
+          tile = 0;
+          ++entry;
+        }
+      }
+    }
+  } else {
+    // ---- finishing warp
+    const int g = lane >> 2, c = lane & 3;
+    int rb = 0;
+    uint32_t rpar = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const KSplit ks = ph ? a.k2 : a.k1;
+      const int per = ph ? n_dn : n_gu;
+      const int first = ph ? i2 : i1, last = ph ? j2 : j1;
+      const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
+      int entry = first / per, tile = first % per, run = 0;
+#pragma unroll 1
+      for (int it = first; it < last; ++it) {
+        ok = mbar_wait_warp(smem_u32(&sh.red_full[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
+                            kWhereFew + 4);
+        if (!ok) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < active; ++w) {
+          const uint4 p = lds128(red + (rb * kFewWarps + w) * 512 + lane * 16);
+          v.x += __uint_as_float(p.x);
+          v.y += __uint_as_float(p.y);
+          v.z += __uint_as_float(p.z);
+          v.w += __uint_as_float(p.w);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.red_empty[rb]));
+        if (++rb == kFewRed) {
+          rb = 0;
+          rpar ^= 1;
+        }
+        const int n = sh.entry_n[entry];
+        const float lo[2] = {v.x, v.y}, hi[2] = {v.z, v.w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = c * 2 + h;
+          if (col < n) {
+            const size_t s = sh.entry_slot[entry][col];
+            if (ph == 0) {
+              a.act[s * a.I + tile * 8 + g] = __float2bfloat16_rn(swiglu(lo[h], hi[h]));
+            } else {
+              float* y = a.y + s * a.d + tile * 16 + g;
+              __stcg(y, lo[h]);
+              __stcg(y + 8, hi[h]);
+            }
+          }
+        }
+        ++run;
+        if (++tile == per || it + 1 == last) {
+          if (ph == 0) {  // publish the activations of this run of the entry's tiles
+            __syncwarp();
+            if (lane == 0) {
+              __threadfence();
+              atomicAdd(a.ready + entry, static_cast<uint32_t>(run));
+            }
+          }
+          run = 0;
+          if (tile == per) {
+            tile = 0;
+            ++entry;
+          }
+        }
+      }
+    }
+  }
+
+  // ---- combine: the output tiles whose last item this CTA finished
+  __syncthreads();
+  if (sh.abort_flag) return;
+  const uint32_t items = static_cast<uint32_t>(sh.n_entries);
+  for (int it = i2 + static_cast<int>(threadIdx.x); it < j2; it += kFewThreads) {
+    const int tile = it % n_dn;
+    __threadfence();
+    if (atomicAdd(a.done + tile, 1u) == items - 1u)
+      sh.last[atomicAdd(&sh.n_last, 1)] = static_cast<uint16_t>(tile);
+  }
+  __syncthreads();
+  const int work = sh.n_last * a.T * 16;
+  if (work == 0) return;
+  __threadfence();
+  for (int u = threadIdx.x; u < work; u += kFewThreads) {
+    const int cc = u & 15, t = (u >> 4) % a.T, tile = sh.last[(u >> 4) / a.T];
+    const float* y = a.y + static_cast<size_t>(t) * a.k * a.d + tile * 16 + cc;
+    float v[kMaxTopK];
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)
+      if (j < a.k) v[j] = __ldcg(y + static_cast<size_t>(j) * a.d);
+    float o = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)
+      if (j < a.k) o = fmaf(sh.wts[t * a.k + j], v[j], o);
+    a.out[static_cast<size_t>(t) * a.d + tile * 16 + cc] = __float2bfloat16_rn(o);
+  }
+}
+
+using LayerKernel = void (*)(FewLayerArgs);
+LayerKernel layer_kernel(int group) {
+  return group == 0    ? few_layer_kernel<0>
+         : group == 32 ? few_layer_kernel<32>
+         : group == 64 ? few_layer_kernel<64>
+                       : few_layer_kernel<128>;
+}
+
+constexpr size_t kFewDynamicSmem = kFewSmemMax - 6144;  // the rest: FewShared
+static_assert(sizeof(FewShared) <= 6144, "FewShared must fit beside the ring");
+// the scores of 16 tokens fit in the ring
+static_assert(kFewMaxTokens * kMaxE * 8 <= 2 * kFewSlotBytes, "scores must fit in the ring");
+
+}  // namespace
+
+cudaError_t launch_few_router(const FewRouterArgs& a, cudaStream_t s) {
+  const dim3 grid(a.E / kRtExperts);
+  if (a.T <= 1)
+    few_router_kernel<1><<<grid, kRtThreads, 0, s>>>(a);
+  else if (a.T <= 2)
+    few_router_kernel<2><<<grid, kRtThreads, 0, s>>>(a);
+  else if (a.T <= 4)
+    few_router_kernel<4><<<grid, kRtThreads, 0, s>>>(a);
+  else if (a.T <= 8)
+    few_router_kernel<8><<<grid, kRtThreads, 0, s>>>(a);
+  else
+    few_router_kernel<16><<<grid, kRtThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
+  const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
+  a.k1 = make_ksplit(a.d / unit, kFewSlotBytes, unit_bytes);
+  a.k2 = make_ksplit(a.I / unit, kFewSlotBytes, unit_bytes);
+  const size_t red = static_cast<size_t>(kFewRed) * kFewWarps * 512;
+  a.slot_bytes = kFewSlotBytes;
+  a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);
+  if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
+  // no more CTAs than gate|up items can exist
+  const int64_t most = static_cast<int64_t>(a.T) * a.k * (a.I / 8);
+  const int grid = most < sms ? static_cast<int>(most) : sms;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = a.stages * static_cast<size_t>(a.slot_bytes) + red;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, layer_kernel(group), a);
+}
+
+cudaError_t prepare_few_kernels() {
+  for (int group : {0, 32, 64, 128}) {
+    const cudaError_t e = cudaFuncSetAttribute(layer_kernel(group),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kFewDynamicSmem));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace beam

@@ -1,0 +1,511 @@
+// 4-bit weights with group scales: conversion of BF16 weights, and y = x W^T for 1 to 16 tokens.
+#include "beam_moe_few.cuh"
+
+#include <cstring>
+
+namespace beam {
+namespace {
+
+// ------------------------------------------------------------------ conversion
+
+// One warp per superblock (16 output rows x 128 K elements).  s = bf16(amax / 7),
+// q = clamp(rne(x / s), -8, 7): lane (g, c) = (lane / 4, lane % 4) reads exactly the elements whose
+// codes its 16-byte words hold, so no code moves between lanes; a group's maximum is combined
+// over the four lanes that share its rows.  HBM-bound: 2 bytes read and about half a byte written
+// per weight, once per model.
+__global__ void __launch_bounds__(256) int4_quantize_kernel(const Int4QuantArgs a) {
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (unit >= a.units) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int sbs = a.cols / kI4Unit;
+  const int sb = static_cast<int>(unit % sbs);
+  const int64_t tile_all = unit / sbs;
+  const int tile = static_cast<int>(tile_all % a.tiles);
+  const int64_t grp = tile_all / a.tiles;
+  // rows of the lane's two fragment rows: 8 of a and 8 of b, or 16 consecutive ones of a
+  const __nv_bfloat16* src[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = a.b ? tile * 8 + g : tile * 16 + h * 8 + g;
+    const __nv_bfloat16* m = a.b && h ? a.b : a.a;
+    src[h] = r < a.rows ? m + (static_cast<size_t>(grp) * a.rows + r) * a.cols +
+                              static_cast<size_t>(sb) * kI4Unit + c * 8
+                        : nullptr;
+  }
+  uint4 v[2][4];  // [row half][run of 32]
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[h][j] = src[h] ? __ldg(reinterpret_cast<const uint4*>(src[h] + j * 32))
+                       : make_uint4(0u, 0u, 0u, 0u);
+  float amax[2][4];  // per run of 32
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      amax[h][j] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    }
+  const int runs = a.group / 32;  // runs of 32 per group: 1, 2 or 4
+  if (runs >= 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      amax[h][0] = amax[h][1] = fmaxf(amax[h][0], amax[h][1]);
+      amax[h][2] = amax[h][3] = fmaxf(amax[h][2], amax[h][3]);
+      if (runs == 4) amax[h][0] = amax[h][1] = amax[h][2] = amax[h][3] = fmaxf(amax[h][0], amax[h][2]);
+    }
+  }
+  uint8_t* dst = a.packed + static_cast<size_t>(unit) * i4_unit_bytes(a.group);
+  uint32_t word[8] = {};
+  uint32_t scale_bits[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat16 s0 = __float2bfloat16_rn(__fdiv_rn(amax[0][j], 7.f));
+    const __nv_bfloat16 s1 = __float2bfloat16_rn(__fdiv_rn(amax[1][j], 7.f));
+    scale_bits[j] = static_cast<uint32_t>(__bfloat16_as_ushort(s0)) |
+                    (static_cast<uint32_t>(__bfloat16_as_ushort(s1)) << 16);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float s = __bfloat162float(h ? s1 : s0);
+      const uint32_t w[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // element k = 32 j + 8 c + i
+        const float x = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+        float q = s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
+        q = fminf(fmaxf(q, -8.f), 7.f);
+        const uint32_t n = static_cast<uint32_t>(static_cast<int>(q) + 8) & 15u;
+        // word 2 j + i / 4; element pair (i % 4) / 2 of row half h is nibble h + 2 ((i % 4) / 2),
+        // its second element four nibbles up
+        word[j * 2 + (i >> 2)] |= n << (4 * (h + 2 * ((i & 3) >> 1) + 4 * (i & 1)));
+      }
+    }
+  }
+  reinterpret_cast<uint4*>(dst)[lane] = make_uint4(word[0], word[1], word[2], word[3]);
+  reinterpret_cast<uint4*>(dst + 512)[lane] = make_uint4(word[4], word[5], word[6], word[7]);
+  if (c == 0) {
+    uint32_t* sc = reinterpret_cast<uint32_t*>(dst + 1024);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j % runs == 0) sc[(j / runs) * 8 + g] = scale_bits[j];
+  }
+}
+
+// ------------------------------------------------------------------ linear product
+
+constexpr int kLinRecv = 2;        // receive buffers of a tile's other K ranges
+constexpr int kLinMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void remote_store(uint32_t a, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait of a warp for another CTA of the cluster.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             uint64_t limit_ns) {
+  bool ok = mbar_try_wait_cluster(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!(ok = mbar_try_wait_cluster(bar, parity))) {
+      if (*abort_flag) break;
+      if (globaltimer_ns() - t0 > limit_ns) {
+        *abort_flag = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// y = x W^T, T <= 8 NT tokens.  A tile is 16 rows of W; a cluster of C CTAs shares a tile, each
+// taking a K range, and the CTA whose turn it is (tile index mod C) receives the others' partial
+// tiles in its shared memory and adds them in rank order.  C > 1 is for matrices with few tiles
+// (the spread over 148 SMs would be uneven) and for K ranges whose token fragments do not fit in
+// registers.  HBM-bound on N K (1/2 + 2 / group) bytes.
+//
+// Launched with programmatic stream serialisation: the producer starts on the weights while the
+// previous kernel of the stream drains; tokens are read, and outputs written, after
+// griddepcontrol.wait.  (Weights written by the previous kernel are safe: only kernels of this
+// kind let their successor start early, and they write no weights.)
+template <int NT, int GROUP>
+__global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4LinearArgs a) {
+  constexpr int kUnits = NT == 1 ? 4 : 2;  // superblocks per warp: 64 registers of fragments
+  constexpr int kUnitBytes = i4_unit_bytes(GROUP);
+  constexpr int kRedBytes = 512 * NT;      // one partial tile
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full_bar[kFewMaxStages], empty_bar[kFewMaxStages];
+  __shared__ __align__(8) uint64_t red_full[kFewRed], red_empty[kFewRed];
+  __shared__ __align__(8) uint64_t recv_full[kLinRecv], recv_free[kLinMaxCluster][kLinRecv];
+  __shared__ int abort_sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t C = a.cluster, rank = C > 1 ? cluster_rank() : 0;
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t red = ring + a.stages * a.slot_bytes;
+  const uint32_t recv = red + kFewRed * kFewWarps * kRedBytes;
+  volatile int* abort_flag = &abort_sh;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(smem_u32(&full_bar[i]), 1);
+      mbar_init(smem_u32(&empty_bar[i]), kFewWarps);
+    }
+    for (int i = 0; i < kFewRed; ++i) {
+      mbar_init(smem_u32(&red_full[i]), kFewWarps);
+      mbar_init(smem_u32(&red_empty[i]), 1);
+    }
+    for (int i = 0; i < kLinRecv; ++i) {
+      mbar_init(smem_u32(&recv_full[i]), C > 1 ? C - 1 : 1);
+      for (int r = 0; r < kLinMaxCluster; ++r) mbar_init(smem_u32(&recv_free[r][i]), 1);
+    }
+    abort_sh = 0;
+    fence_mbarrier_init();
+  }
+  pdl_launch();
+  if (C > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+
+  const int nclus = gridDim.x / C, q = blockIdx.x / C;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(q) * a.tiles / nclus);
+  const int tile1 = static_cast<int>(static_cast<int64_t>(q + 1) * a.tiles / nclus);
+  const int units_all = a.K / kI4Unit;
+  const int u0 = rank * units_all / C, u1 = (rank + 1) * units_all / C;
+  // the chunk size is chosen on the host for the largest K range
+  KSplit ks{u1 - u0, a.log_cw};
+  const int cw = 1 << a.log_cw;
+
+  if (warp == kFewWarps) {
+    // ---- producer
+    int slot = 0;
+    uint32_t par = 1, issued = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < tile1 && ok; ++tile) {
+      const uint8_t* src = a.w + (static_cast<size_t>(tile) * units_all + u0) * kUnitBytes;
+      for (int w = 0; w < kFewWarps; w += cw) {
+        ok = mbar_wait_warp(smem_u32(&empty_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
+        if (!ok) break;
+        if (lane == 0) {
+          const int s = ks.start(w), n = ks.start(w + cw) - s;
+          const uint32_t bar = smem_u32(&full_bar[slot]);
+          mbar_arrive_expect_tx(bar, n * kUnitBytes);
+          bulk_load(ring + slot * a.slot_bytes, src + static_cast<size_t>(s) * kUnitBytes,
+                    n * kUnitBytes, bar);
+        }
+        ++issued;
+        if (++slot == a.stages) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
+    }
+    if (!ok) {  // copies in flight must land before this CTA's shared memory is given up
+      volatile int never = 0;
+      const uint32_t back = issued < static_cast<uint32_t>(a.stages) ? issued : a.stages;
+      for (uint32_t i = issued - back; i < issued; ++i)
+        mbar_wait_bounded(smem_u32(&full_bar[i % a.stages]), (i / a.stages) & 1, &never,
+                          2000000000ull, nullptr, 0);
+    }
+  } else if (warp < kFewWarps) {
+    // ---- consumers
+    const int units = ks.count(warp), mine = warp >> a.log_cw, chunks = ks.chunks();
+    const uint32_t off = (ks.start(warp) - ks.start(mine << a.log_cw)) * kUnitBytes;
+    uint32_t b[NT][kUnits * 16];
+    pdl_wait();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int t = nt * kFewCols + (lane >> 2);
+      load_tokens<kUnits * 4, true>(
+          b[nt],
+          t < a.T ? a.x + static_cast<size_t>(t) * a.K + static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit
+                  : nullptr,
+          units * 4, lane & 3);
+    }
+    int slot = 0, rb = 0;
+    uint32_t par = 0, rpar = 1;
+    bool ok = true;
+    for (int tile = tile0; tile < tile1; ++tile) {
+      float acc[NT][4] = {};
+      // every warp passes every chunk in order: a phase may only be waited for by who has seen the
+      // slot's phase before
+#pragma unroll 1
+      for (int ch = 0; ch < chunks; ++ch) {
+        ok = mbar_wait_warp(smem_u32(&full_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
+        if (!ok) break;
+        if (ch == mine) i4_slice<NT, kUnits, GROUP>(acc, b, ring + slot * a.slot_bytes + off, units, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[slot]));
+        if (++slot == a.stages) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (!mbar_wait_warp(smem_u32(&red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0)) break;
+      if (units > 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          sts128(red + (rb * kFewWarps + warp) * kRedBytes + nt * 512 + lane * 16,
+                 make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&red_full[rb]));
+      if (++rb == kFewRed) {
+        rb = 0;
+        rpar ^= 1;
+      }
+    }
+  } else {
+    // ---- finishing warp
+    const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
+    const int g = lane >> 2, c = lane & 3;
+    int rb = 0;
+    uint32_t rpar = 0;
+    bool ok = true;
+    pdl_wait();
+    for (int i = 0; i < tile1 - tile0; ++i) {
+      float4 v[NT];
+      if (ok) ok = mbar_wait_warp(smem_u32(&red_full[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0);
+      if (ok) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) v[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < active; ++w) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint4 p = lds128(red + (rb * kFewWarps + w) * kRedBytes + nt * 512 + lane * 16);
+            v[nt].x += __uint_as_float(p.x);
+            v[nt].y += __uint_as_float(p.y);
+            v[nt].z += __uint_as_float(p.z);
+            v[nt].w += __uint_as_float(p.w);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&red_empty[rb]));
+        if (++rb == kFewRed) {
+          rb = 0;
+          rpar ^= 1;
+        }
+      }
+      const uint32_t owner = C > 1 ? i % C : 0;
+      if (C > 1 && ok) {
+        const int n = i / C, slot = n & 1;  // the owner's n-th tile
+        if (owner != rank) {
+          if (n >= kLinRecv)
+            ok = wait_cluster(smem_u32(&recv_free[owner][slot]), ((n >> 1) - 1) & 1, abort_flag,
+                              a.wait_limit_ns);
+          if (ok) {
+            const uint32_t src = rank < owner ? rank : rank - 1;
+            const uint32_t dst =
+                map_rank(recv + (slot * (C - 1) + src) * kRedBytes + lane * 16, owner);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) remote_store(dst + nt * 512, v[nt]);
+            __syncwarp();
+            if (lane == 0) remote_arrive(map_rank(smem_u32(&recv_full[slot]), owner));
+          }
+        } else {
+          ok = wait_cluster(smem_u32(&recv_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns);
+          if (ok) {
+            float4 own[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              own[nt] = v[nt];
+              v[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            for (uint32_t r = 0; r < C; ++r) {
+              const uint32_t src = r < rank ? r : r - 1;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float4 p = own[nt];
+                if (r != rank) {
+                  const uint4 u = lds128(recv + (slot * (C - 1) + src) * kRedBytes + nt * 512 + lane * 16);
+                  p = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                  __uint_as_float(u.w));
+                }
+                v[nt].x += p.x;
+                v[nt].y += p.y;
+                v[nt].z += p.z;
+                v[nt].w += p.w;
+              }
+            }
+            __syncwarp();
+            if (lane < static_cast<int>(C) && lane != static_cast<int>(rank))
+              remote_arrive(map_rank(smem_u32(&recv_free[rank][slot]), lane));
+          }
+        }
+      }
+      if (owner != rank) continue;
+      if (!ok) {  // a wait ran out: the tile's outputs say so
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float nan = __uint_as_float(0x7fc00000u);
+          v[nt] = make_float4(nan, nan, nan, nan);
+        }
+      }
+      const int tile = tile0 + i;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float lo[2] = {v[nt].x, v[nt].y}, hi[2] = {v[nt].z, v[nt].w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = nt * kFewCols + c * 2 + h;
+          if (t >= a.T) continue;
+          if (a.out_kind == kI4OutSwiglu) {  // row g: gate, row g + 8: up
+            const int n = tile * 8 + g;
+            if (n < a.N / 2)
+              static_cast<__nv_bfloat16*>(a.out)[static_cast<size_t>(t) * (a.N / 2) + n] =
+                  __float2bfloat16_rn(swiglu(lo[h], hi[h]));
+          } else {
+            const int n = tile * 16 + g;
+            const size_t o = static_cast<size_t>(t) * a.N + n;
+            if (a.out_kind == kI4OutF32) {
+              if (n < a.N) static_cast<float*>(a.out)[o] = lo[h];
+              if (n + 8 < a.N) static_cast<float*>(a.out)[o + 8] = hi[h];
+            } else {
+              if (n < a.N) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(lo[h]);
+              if (n + 8 < a.N) static_cast<__nv_bfloat16*>(a.out)[o + 8] = __float2bfloat16_rn(hi[h]);
+            }
+          }
+        }
+      }
+    }
+  }
+  if (C > 1) {  // no CTA leaves while another may still write its shared memory
+    __syncwarp();
+    cluster_sync_all();
+  }
+}
+
+using LinearKernel = void (*)(Int4LinearArgs);
+LinearKernel linear_kernel(int nt, int group) {
+  if (nt == 1)
+    return group == 32 ? int4_linear_kernel<1, 32> : group == 64 ? int4_linear_kernel<1, 64>
+                                                                 : int4_linear_kernel<1, 128>;
+  return group == 32 ? int4_linear_kernel<2, 32> : group == 64 ? int4_linear_kernel<2, 64>
+                                                               : int4_linear_kernel<2, 128>;
+}
+
+// Co-resident clusters of C CTAs on this device, by log2 C (filled by prepare_int4_kernels; one
+// kind of device per process).
+int g_max_clusters[4] = {0, 0, 0, 0};
+
+cudaLaunchConfig_t linear_config(int grid, size_t smem, cudaStream_t s, int cluster,
+                                 cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cfg;
+}
+
+constexpr size_t kLinDynamicSmem = kFewSmemMax - 1024;  // the rest: barriers
+
+}  // namespace
+
+cudaError_t launch_int4_quantize(const Int4QuantArgs& a, cudaStream_t s) {
+  const int64_t blocks = (a.units + 7) / 8;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  int4_quantize_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_t s) {
+  const int nt = a.T > kFewCols ? 2 : 1;
+  const int units = a.K / kI4Unit, unit_bytes = i4_unit_bytes(group);
+  const int max_units = kFewWarps * (nt == 1 ? 4 : 2);  // K range of a CTA
+  // The cluster size that finishes soonest: the largest share of bytes of one CTA at its share of
+  // the HBM rate, and about 1 us for the exchange between the CTAs of a cluster.
+  int best = 0, best_clus = 0;
+  double best_t = 0.;
+  for (int lc = 0; lc < 4; ++lc) {
+    const int C = 1 << lc;
+    const int per = (units + C - 1) / C;
+    if (per > max_units || C > units) continue;
+    int clus = lc == 0 ? sms : g_max_clusters[lc];
+    if (clus > a.tiles) clus = a.tiles;
+    if (clus <= 0) continue;
+    const double t = static_cast<double>((a.tiles + clus - 1) / clus) * per * unit_bytes / 44.0 +
+                     (C > 1 ? 1000.0 : 0.0);
+    if (!best || t < best_t) {
+      best = C;
+      best_clus = clus;
+      best_t = t;
+    }
+  }
+  if (!best) return cudaErrorInvalidConfiguration;
+  a.cluster = best;
+  const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * nt +
+                      static_cast<size_t>(kLinRecv) * (best - 1) * 512 * nt;
+  const int per = (units + best - 1) / best;
+  a.log_cw = make_ksplit(per, kFewSlotBytes, unit_bytes).log_cw;
+  a.slot_bytes = kFewSlotBytes;
+  a.stages = static_cast<int>((kLinDynamicSmem - rest) / a.slot_bytes);
+  if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg =
+      linear_config(best * best_clus, a.stages * static_cast<size_t>(a.slot_bytes) + rest, s, best, attr);
+  return cudaLaunchKernelEx(&cfg, linear_kernel(nt, group), a);
+}
+
+cudaError_t prepare_int4_kernels() {
+  for (int nt = 1; nt <= 2; ++nt)
+    for (int group : {32, 64, 128}) {
+      const cudaError_t e = cudaFuncSetAttribute(linear_kernel(nt, group),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(kLinDynamicSmem));
+      if (e != cudaSuccess) return e;
+    }
+  for (int lc = 1; lc < 4; ++lc) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = linear_config(1 << lc, kLinDynamicSmem, nullptr, 1 << lc, attr);
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, linear_kernel(1, 128), &cfg);
+    if (e != cudaSuccess) return e;
+    g_max_clusters[lc] = n;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace beam

@@ -1,0 +1,317 @@
+"""The MoE layer for a few tokens (BF16 and 4-bit experts) against plain 64-bit forms
+(tests/int4_ref.py, whose error bounds are the tolerances) and the oracle's routing."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from sparse_moe_transformer_fp32_b200 import beam_moe as bm
+from sparse_moe_transformer_fp32_b200 import workloads as W
+from tests import int4_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+
+
+def normal(seed, *shape, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.empty(shape, device="cuda", dtype=dtype).normal_(0.0, std, generator=g)
+
+
+class Layer:
+    def __init__(self, d, E, G, Gk, k, I, group=0, seed=0, bias=None, norm=True, scale=2.5):
+        self.cfg = (d, E, G, Gk, k, I)
+        self.group, self.norm, self.scale = group, norm, scale
+        self.router_w = normal(seed + 1, E, d, std=0.7 * d ** -0.5, dtype=torch.float32)
+        self.bias = normal(seed + 2, E, std=0.05, dtype=torch.float32) if bias is None else bias
+        self.gate = normal(seed + 3, E, I, d, std=d ** -0.5)
+        self.up = normal(seed + 4, E, I, d, std=d ** -0.5)
+        self.down = normal(seed + 5, E, d, I, std=I ** -0.5)
+        if group:
+            self.gu = bm.beam_int4_quantize(self.gate, self.up, group_size=group)
+            self.dn = bm.beam_int4_quantize(self.down, group_size=group)
+
+    def shape(self, T):
+        d, E, G, Gk, k, I = self.cfg
+        return bm.make_shape(T, d, E, G, Gk, k, I, self.scale, self.norm)
+
+    def call(self, h, out, idx=None, w=None, ws=None, stream=None):
+        s = self.shape(h.shape[0])
+        if self.group:
+            return bm.beam_moe_forward_few_int4(s, self.group, h, self.router_w, self.bias, self.gu,
+                                                self.dn, out, idx, w, ws=ws, stream=stream)
+        return bm.beam_moe_forward_few(s, h, self.router_w, self.bias, self.gate, self.up, self.down,
+                                       out, idx, w, ws=ws, stream=stream)
+
+    def run(self, h, ws=None):
+        T, (d, E, G, Gk, k, I) = h.shape[0], self.cfg
+        # rows before and behind the outputs stay as they were
+        flat = torch.full((T + 2, d), 7.0, device="cuda", dtype=torch.bfloat16)
+        out = flat[1:T + 1]
+        idx = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+        w = torch.full((T, k), -1.0, device="cuda")
+        ws = self.call(h, out, idx, w, ws)
+        assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
+        assert (flat[0] == 7).all() and (flat[T + 1] == 7).all()
+        return out, idx, w, ws
+
+    def check(self, h, out, idx, w):
+        d, E, G, Gk, k, I = self.cfg
+        ridx, rw = R.route_ref(h, self.router_w, self.bias, G, Gk, k, self.scale, self.norm)
+        assert torch.equal(idx.cpu().long(), ridx)
+        # score (rounded twice to FP32), k - 1 additions, product and quotient
+        assert ((w.cpu().double() - rw).abs() <= (k + 6) * R.U32 * rw).all()
+        ref, bound = R.layer_ref(h, ridx, rw, self.gate, self.up, self.down, self.group)
+        return R.assert_within(out, ref, bound, f"T={h.shape[0]} {self.cfg} g={self.group}")
+
+
+SHAPES = [  # T, d, E, G, Gk, k, I
+    (1, 256, 16, 4, 2, 4, 128),
+    (7, 256, 16, 4, 2, 4, 128),
+    (16, 256, 4, 1, 1, 1, 128),
+    (5, 512, 32, 8, 8, 8, 384),
+    (3, 768, 64, 2, 1, 3, 640),
+    (16, 1280, 128, 4, 3, 5, 256),
+    (2, 2560, 40, 8, 5, 7, 1408),
+    (9, 4096, 8, 2, 2, 2, 2048),
+    (4, 5120, 16, 4, 2, 8, 2560),
+    (2, 8192, 4, 1, 1, 2, 8192),
+    (6, 256, 256, 32, 3, 8, 128),
+]
+
+
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("T,d,E,G,Gk,k,I", SHAPES)
+def test_layer_matches_64_bits(T, d, E, G, Gk, k, I, group):
+    m = Layer(d, E, G, Gk, k, I, group)
+    h = normal(99, T, d)
+    out, idx, w, _ = m.run(h)
+    m.check(h, out, idx, w)
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("T", range(1, 17))
+def test_every_token_count(T, group):
+    m = Layer(512, 16, 4, 2, 4, 384, group, seed=T)
+    h = normal(99 + T, T, 512)
+    out, idx, w, _ = m.run(h)
+    m.check(h, out, idx, w)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("T", [8, 9, 16])
+def test_all_tokens_on_the_same_experts(T, group):
+    """More than eight tokens on an expert open a second entry for it."""
+    bias = torch.zeros(32, device="cuda")
+    bias[[3, 4, 9, 30]] = 5.0
+    m = Layer(512, 32, 4, 4, 4, 256, group, bias=bias)
+    h = normal(3, T, 512)
+    out, idx, w, _ = m.run(h)
+    assert (idx.cpu() == torch.tensor([3, 4, 9, 30])).all()
+    m.check(h, out, idx, w)
+    # identical tokens give identical rows
+    h[1:] = h[0]
+    out, idx, w, _ = m.run(h)
+    assert (out == out[0]).all()
+
+
+def test_ties_go_to_the_lower_index():
+    m = Layer(256, 32, 4, 2, 4, 128)
+    m.router_w.zero_()
+    m.bias.zero_()
+    h = normal(3, 5, 256)
+    out, idx, w, _ = m.run(h)
+    assert (idx.cpu() == torch.arange(4)).all()
+    assert (w == 2.5 / 4).all()
+    m.check(h, out, idx, w)
+    # equal groups and equal experts across lanes of 32
+    m = Layer(256, 256, 8, 4, 8, 128)
+    m.router_w.zero_()
+    m.bias.zero_()
+    m.bias[[5, 37, 69, 101, 133, 165, 197, 229]] = 1.0  # one per group: groups tie, lowest four stay
+    out, idx, w, _ = m.run(h)
+    assert idx[0].tolist() == [0, 1, 2, 3, 5, 37, 69, 101]
+    m.check(h, out, idx, w)
+
+
+def test_near_ties_follow_the_definition():
+    """Router rows that differ in their last bits: FP32 sums in another order would choose others."""
+    m = Layer(5120, 64, 8, 4, 8, 128)
+    base = normal(8, 1, 5120, std=0.01, dtype=torch.float32)
+    m.router_w.copy_(base * (1 + 1e-6 * torch.rand(64, 1, device="cuda", generator=torch.Generator(
+        device="cuda").manual_seed(4))))
+    m.bias.zero_()
+    for seed in range(8):
+        h = normal(200 + seed, 16, 5120)
+        out, idx, w, _ = m.run(h)
+        m.check(h, out, idx, w)
+
+
+def test_routing_equals_the_oracle_without_removing_near_ties():
+    wl = W.WORKLOADS["decode"].with_tokens(16)
+    h, router_w, bias = W.hidden(wl), W.router_weight(wl), W.router_bias(wl)
+    _, ridx, rw, _, _ = oracle.layer_routing(h, router_w, bias, wl)
+    m = Layer(wl.d, wl.E, wl.n_group, wl.topk_group, wl.top_k, 128)
+    m.router_w, m.bias = router_w.cuda(), bias.cuda()
+    out, idx, w, _ = m.run(h.cuda())
+    assert np.array_equal(idx.cpu().numpy(), ridx)
+    np.testing.assert_allclose(w.cpu().numpy(), rw, rtol=1e-6)
+
+
+def test_unnormalised_weights_and_another_scale():
+    m = Layer(512, 16, 4, 2, 4, 256, norm=False, scale=1.25)
+    h = normal(4, 6, 512)
+    out, idx, w, _ = m.run(h)
+    m.check(h, out, idx, w)
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_a_nan_token_stays_alone(group):
+    m = Layer(512, 16, 4, 2, 4, 256, group)
+    h = normal(4, 6, 512)
+    h[2, 9] = float("nan")
+    h[4, 0] = float("inf")
+    out, idx, w, _ = m.run(h)
+    assert torch.isnan(out[2]).all()
+    assert ((idx >= 0) & (idx < 16)).all()
+    rest = [0, 1, 3, 5]
+    m.check(h[rest], out[rest], idx[rest], w[rest])
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_same_bits_every_time_and_without_optional_outputs(group):
+    m = Layer(2560, 64, 8, 4, 8, 1280, group)
+    h = normal(4, 5, 2560)
+    out, idx, w, ws = m.run(h)
+    for _ in range(10):
+        again = torch.empty_like(out)
+        m.call(h, again, ws=ws)
+        assert torch.equal(again, out)
+    # a token alone has the bits that it has among others
+    for t in range(5):
+        one = torch.empty_like(out[:1])
+        m.call(h[t:t + 1].clone(), one)
+        assert torch.equal(one[0], out[t])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_graph_replay_two_graphs_on_one_workspace(group):
+    m = Layer(1280, 32, 4, 2, 4, 640, group)
+    h1, h2 = normal(1, 3, 1280), normal(2, 9, 1280)
+    o1, o2 = torch.empty_like(h1), torch.empty_like(h2)
+    ws = bm.few_workspace(m.shape(9))
+    m.call(h1, o1, ws=ws)
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        m.call(h1, o1, ws=ws)
+        m.call(h1, o1, ws=ws)
+    with torch.cuda.graph(g2):
+        m.call(h2, o2, ws=ws)
+    for seed in (10, 20, 30):
+        h1.copy_(normal(seed, 3, 1280))
+        h2.copy_(normal(seed + 1, 9, 1280))
+        g1.replay()
+        g2.replay()
+        g1.replay()
+        torch.cuda.synchronize()
+        assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
+        for h, o in ((h1, o1), (h2, o2)):
+            got = o.clone()
+            again, idx, w, _ = m.run(h)
+            assert torch.equal(got, again)
+            m.check(h, got, idx, w)
+
+
+def test_two_streams_at_once_with_their_own_workspaces():
+    ms = [Layer(1280, 32, 4, 2, 4, 640, 0, seed=1), Layer(1280, 32, 4, 2, 4, 640, 64, seed=2)]
+    hs = [normal(5, 4, 1280), normal(6, 7, 1280)]
+    want = [m.run(h)[0].clone() for m, h in zip(ms, hs)]
+    streams = [torch.cuda.Stream() for _ in ms]
+    wss = [bm.few_workspace(m.shape(h.shape[0])) for m, h in zip(ms, hs)]
+    outs = [[torch.empty_like(h) for _ in range(10)] for h in hs]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for m, h, o, ws, st in zip(ms, hs, outs, wss, streams):
+            m.call(h, o[i], ws=ws, stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(x, w) for x in o)
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_wait_that_runs_out_is_reported_and_the_context_survives(group):
+    m = Layer(1280, 32, 4, 2, 4, 640, group)
+    h = normal(5, 4, 1280)
+    out, idx, w, ws = m.run(h)
+    good = out.clone()
+    old = bm.beam_moe_get_wait_limit_ns()
+    bm.beam_moe_set_wait_limit_ns(0)
+    try:
+        m.call(h, out, ws=ws)
+        assert bm.beam_moe_sync_status(ws) == bm.BEAM_ERR_TIMEOUT
+    finally:
+        bm.beam_moe_set_wait_limit_ns(old)
+    m.call(h, out, ws=ws)
+    assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
+    assert torch.equal(out, good)
+
+
+def test_agrees_with_the_many_token_layer():
+    """The same layer through beam_moe_forward, whose BF16 expert outputs its tolerance counts."""
+    wl = W.WORKLOADS["tiny"]
+    m = Layer(wl.d, wl.E, wl.n_group, wl.topk_group, wl.top_k, wl.I)
+    h = normal(3, 16, wl.d)
+    out, idx, w, _ = m.run(h)
+    other = torch.empty_like(out)
+    oidx = torch.empty_like(idx)
+    bm.beam_moe_forward(m.shape(16), h, m.router_w, m.bias, m.gate, m.up, m.down, other, oidx)
+    torch.cuda.synchronize()
+    same = (idx == oidx).all(dim=1).cpu()
+    assert same.sum() >= 12
+    ref, bound = R.layer_ref(h, idx.cpu().long(), w.cpu().double(), m.gate, m.up, m.down, 0)
+    # expert outputs rounded to BF16 before the weighted sum: another half step of each
+    assert ((other.double() - ref).abs().cpu() <= 2 * bound.cpu() + 2.5 * R.U16 * 4 *
+            ref.abs().amax().cpu())[same].all()
+
+
+def test_a_decode_step_of_dense_moe_and_head():
+    """Dense 4-bit MLP, the MoE layer with 4-bit experts, and an LM head, back to back on a stream:
+    each stage against the 64-bit form on the stage before."""
+    T, d, I, V = 4, 512, 1280, 1001
+    m = Layer(d, 32, 4, 2, 4, 384, 64)
+    h = normal(1, T, d)
+    g, u = (normal(s, 1, I, d, std=d ** -0.5) for s in (2, 3))
+    dn, head = normal(4, 1, d, I, std=I ** -0.5), normal(5, 1, V, d, std=d ** -0.5)
+    gu, dq = bm.beam_int4_quantize(g, u, group_size=64), bm.beam_int4_quantize(dn, group_size=64)
+    hq = bm.beam_int4_quantize(head, group_size=64)
+    x1, x2 = torch.empty_like(h), torch.empty_like(h)
+    idx = torch.empty(T, 4, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, 4, device="cuda")
+    logits = torch.empty(T, V, device="cuda")
+    dws, ws = bm.dense_int4_workspace(bm.dense_shape(T, d, I)), bm.few_workspace(m.shape(T))
+    for _ in range(3):
+        bm.beam_dense_forward_int4(bm.dense_shape(T, d, I), 64, h, gu, dq, x1, ws=dws)
+        m.call(x1, x2, idx, w, ws=ws)
+        bm.beam_int4_linear(bm.int4_shape(T, V, d, 64), x2, hq, logits)
+    assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
+    R.assert_within(x1, *R.dense_ref(h, g[0], u[0], dn[0], 64), "dense")
+    m.check(x1, x2, idx, w)
+    R.assert_within(logits, *R.linear_ref(x2, head[0], 64, True), "head")
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_beam_layer(group):
+    """The full Beam shape: expert rows beyond 32-bit element offsets."""
+    m = Layer(5120, 256, 8, 4, 8, 2560, group)
+    for T in (1, 16):
+        h = normal(7 + T, T, 5120)
+        out, idx, w, _ = m.run(h)
+        assert T == 1 or int(idx.max()) > 200
+        m.check(h, out, idx, w)
