@@ -342,16 +342,19 @@ BEAM_API beam_status beam_moe_bias_update(const beam_moe_shape* shape, const voi
  * 4-bit weights are integer codes with a BF16 scale per row and group of group_size (32, 64 or
  * 128) consecutive elements of the row; activations stay BF16:
  *   s = bf16(fl32(amax / 7)),  q = clamp(rne(fl32(x / s)), -8, 7),  value = s * q
- * with amax the group's largest magnitude; a group with s = 0 has zero codes.  Products of
- * codes and BF16 activations are exact; each group's sum, times its scale, is added in FP32.
+ * with amax the group's largest magnitude; a group with s = 0 has zero codes.  A product sums each
+ * group's codes times activations exactly or in FP32, multiplies by the scale and adds the groups in
+ * FP32.  (For up to 8 tokens the activations enter as 23-bit integers with a common power of two per
+ * token and K slice: exactly their BF16 values, unless an element is below 2^-14 of the slice's
+ * largest, when it is off by at most 2^-22 of that.  There a token with a non-finite element has NaN
+ * outputs.)
  *
  * Packed storage (what the kernels stream): tiles of 16 rows; in a tile, superblocks of 128
  * columns in order; a superblock is two 512-byte code blocks of 64 columns, then for each of its
  * 128 / group_size groups 16 BF16 scales, scale 2g for row g of the tile and 2g + 1 for row g + 8.
- * In a code block, 32-bit word v (0..3) of the 16 bytes at 16 (4g + c) (g 0..7, c 0..3) holds,
- * with k = 32 (v / 2) + 8c + 4 (v % 2), each as code + 8:
- *   row g:     column k in bits 0-3, k + 1 in 16-19, k + 2 in 8-11,  k + 3 in 24-27
- *   row g + 8: column k in bits 4-7, k + 1 in 20-23, k + 2 in 12-15, k + 3 in 28-31
+ * In a code block, byte i (0..3) of 32-bit word v (0..3) of the 16 bytes at 16 (4g + c) (g 0..7,
+ * c 0..3) holds the codes, in two's complement, of column 32 (v / 2) + 8c + 4 (v % 2) + i: row g in
+ * the high four bits, row g + 8 in the low four.
  * Rows past the last are zero codes with zero scales.  Weights must be finite. */
 #define BEAM_FEW_MAX_TOKENS 16
 #define BEAM_INT4_MAX_K 32768

@@ -9,9 +9,9 @@
 //
 //  - one persistent CTA per SM: a producer warp moves weights into a shared-memory ring of
 //    about 190 KB with bulk copies (4 us of one SM's share of the HBM bandwidth in flight, so
-//    synchronisation between phases does not stop the stream), 16 consumer warps multiply, one
+//    synchronisation between phases does not stop the stream), 8 consumer warps multiply, one
 //    warp finishes outputs;
-//  - a tile is 16 weight rows by the whole K range of the CTA; the 16 consumer warps split K.
+//  - a tile is 16 weight rows by the whole K range of the CTA; the 8 consumer warps split K.
 //    Each keeps its K slice of the token rows in registers, as B fragments of
 //    mma.sync.m16n8k16 (weights are the 16-row A operand, tokens the 8 columns), for as long as
 //    the CTA stays with the same tokens, so that shared memory carries weights only;
@@ -27,57 +27,72 @@
 namespace beam {
 
 constexpr int kFewMaxTokens = 16;     // tokens per call
-constexpr int kFewCols = 8;           // token columns of one MMA
-constexpr int kFewMaxK = 8192;        // K of one tile: 16 warps x 512 elements (64 B registers)
+constexpr int kFewCols = 8;           // tokens of one entry (an expert's product in the layer kernel)
+constexpr int kFewMaxK = 8192;        // K of one tile: 8 warps x 1024 elements (128 B registers)
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;  // (token, expert) slots = most entries
-constexpr int kFewWarps = 16;         // consumer warps
-constexpr int kFewThreads = (kFewWarps + 2) * 32;  // + producer + finishing warp
-constexpr int kFewSlotBytes = 21504;  // ring slot: 16 rows x (1280 + 64) bytes of BF16 weights
-constexpr int kFewRed = 3;            // partial-tile buffers
+constexpr int kFewWarps = 8;          // consumer warps
+// Consumers, then a warp group of producer, finishing warp and two that only keep it whole: register
+// budgets are given per warp group.  Launched with 168 registers a thread; while the roles run,
+// consumers hold 224 and the others 56 (256 * 224 + 128 * 56 = 384 * 168).
+constexpr int kFewThreads = (kFewWarps + 4) * 32;
+constexpr int kFewRegsLaunch = 168, kFewRegsConsumer = 224, kFewRegsOther = 56;
+static_assert(kFewWarps == 8 && kFewWarps * kFewRegsConsumer + 4 * kFewRegsOther ==
+                                    (kFewWarps + 4) * kFewRegsLaunch, "register budgets must add up");
+constexpr int kI4SlotBytes = 46080;   // ring slot, 4-bit weights: a tile of K = 5120, any group
+// Ring slot, BF16 weights: 16 rows x (2560 + 64) bytes.  Each row of a slot is a bulk copy, and one
+// SM starts a copy about every 39 ns whatever its size: segments of 640, 1280 and 2560 bytes
+// stream at 2.4, 4.8 and 7.4 TB/s over the GPU.
+constexpr int kBf16SlotBytes = 41984;
+constexpr int kFewRed = 3;            // partial-tile buffers, at most
+constexpr int kBf16Red = 2;           // with BF16 weights, whose tiles take four times as long
 constexpr int kFewMaxStages = 16;
 constexpr int kFewSmemMax = 232448;   // 227 KB
 constexpr int kBf16Unit = 32;         // K elements of the smallest BF16 slice of a warp
 
 // 4-bit weights: superblocks of 16 rows x 128 K elements, in K order inside a 16-row tile.
 // A superblock holds two 512-byte code blocks (64 K elements each) and then its BF16 scales.
-// Code block: 16 bytes per lane of the MMA fragment, lane = 4 g + c: word v (0..3) holds, with
-// k = 32 (v / 2) + 8 c + 4 (v % 2), the nibbles (bits 4i..4i+3)
-//   i = 0, 4: row g     k, k + 1        i = 1, 5: row g + 8  k, k + 1
-//   i = 2, 6: row g     k + 2, k + 3    i = 3, 7: row g + 8  k + 2, k + 3
-// each storing code + 8.  Scales: for every group of the superblock 16 BF16, position 2 g for row
-// g and 2 g + 1 for row g + 8.
+// Code block: 16 bytes per lane of the MMA fragment, lane = 4 g + c: byte i of word v (0..3) holds
+// the codes (two's complement) of column 32 (v / 2) + 8 c + 4 (v % 2) + i: row g in the high four
+// bits, row g + 8 in the low four.  The word masked with 0xf0f0f0f0, and the word shifted up by four
+// and masked, are A registers of an 8-bit MMA with the values 16 q.
+// Scales: for every group of the superblock 16 BF16, position 2 g for row g and 2 g + 1 for row
+// g + 8.
 constexpr int kI4Unit = 128;
 __host__ __device__ constexpr int i4_unit_bytes(int group) {
   return kI4Unit * 16 / 2 + (kI4Unit / group) * 32;
 }
 
-// Slices of n K units over the 16 consumer warps: the first n % 16 warps hold one more.
+// Slices of n K units over the consumer warps: the first n % kFewWarps warps hold one more.
 struct KSplit {
-  int n;        // units of the tile's K range
-  int log_cw;   // log2 of the warps that share one ring slot ("chunk")
+  int n;   // units of the tile's K range
+  int cw;  // warps that share one ring slot (a "chunk" of the tile)
   __host__ __device__ int start(int w) const {
+    if (w > kFewWarps) w = kFewWarps;
     const int q = n / kFewWarps, r = n % kFewWarps;
     return w * q + (w < r ? w : r);
   }
   __host__ __device__ int count(int w) const { return start(w + 1) - start(w); }
-  __host__ __device__ int chunks() const { return kFewWarps >> log_cw; }
+  __host__ __device__ int chunks() const { return (kFewWarps + cw - 1) / cw; }
 };
 
 // Ring bytes of a BF16 chunk of u units: 16 rows at a stride of 64 bytes modulo 128, so that the
 // eight rows of a fragment load fall into different banks.
 __host__ __device__ constexpr int bf16_row_stride(int u) { return u * 64 + ((u & 1) ? 0 : 64); }
 
-inline KSplit make_ksplit(int units, int slot_bytes, int unit_bytes_i4 /* 0: BF16 */) {
-  KSplit s{units, 4};
-  auto bytes = [&](int u) { return unit_bytes_i4 ? u * unit_bytes_i4 : 16 * bf16_row_stride(u); };
-  for (; s.log_cw > 0; --s.log_cw) {
-    int most = 0;
-    for (int w = 0; w < kFewWarps; w += 1 << s.log_cw) {
-      const int u = s.start(w + (1 << s.log_cw)) - s.start(w);
-      if (u > most) most = u;
-    }
-    if (bytes(most) <= slot_bytes) break;
+// Bytes of the largest chunk.
+inline int chunk_bytes(const KSplit& s, int unit_bytes_i4 /* 0: BF16 */) {
+  int most = 0;
+  for (int w = 0; w < kFewWarps; w += s.cw) {
+    const int u = s.start(w + s.cw) - s.start(w);
+    if (u > most) most = u;
   }
+  return unit_bytes_i4 ? most * unit_bytes_i4 : 16 * bf16_row_stride(most);
+}
+
+// The fewest chunks a tile that fit in a ring slot.
+inline KSplit make_ksplit(int units, int slot_bytes, int unit_bytes_i4) {
+  KSplit s{units, kFewWarps};
+  while (s.cw > 1 && chunk_bytes(s, unit_bytes_i4) > slot_bytes) s.cw = (s.cw + 1) / 2;
   return s;
 }
 
@@ -102,7 +117,7 @@ struct Int4LinearArgs {
   int T, N, K, tiles;
   int out_kind;            // Int4Out
   int cluster;             // CTAs that split K
-  int log_cw;              // KSplit::log_cw of the largest K range
+  int cw;                  // KSplit::cw of the largest K range
   int stages, slot_bytes;
 };
 
@@ -135,6 +150,7 @@ struct FewLayerArgs {
   int T, d, E, G, Gk, k, I;
   float scale;
   int norm;
+  int entry_max;           // tokens of an entry at most
   int stages, slot_bytes;
 };
 
@@ -171,21 +187,36 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The part of a wait that finds its phase open: the hardware parks the thread between checks
+// (a waiting warp that polls takes issue slots from the warps it waits for).  A limit of 0 gives
+// up at once (a try_wait may park the thread long enough to miss the open phase).
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            uint64_t limit_ns, uint32_t* status, uint32_t where) {
+  if (limit_ns != 0) {
+    // the timer is read once a wait is long: reading it takes longer than most waits
+#pragma unroll 1
+    for (int it = 0; it < 16; ++it)
+      if (mbar_try_wait_hint(bar, parity, 1000u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!*abort_flag && globaltimer_ns() - t0 <= limit_ns) {
+      if (mbar_try_wait_hint(bar, parity, 4000u)) return true;
+    }
+  }
+  if (!*abort_flag) {
+    *abort_flag = 1;
+    record_status(status, kDevTimeout, where);
+  }
+  return false;
+}
+
 // Bounded wait of a whole warp; every lane polls (each must see the phase complete before it reads
-// what the barrier guards).  False on all lanes when any lane gave up.  A limit of 0 gives up at
-// the first open phase (a try_wait may park the thread long enough to miss it).
+// what the barrier guards).  False on all lanes when any lane gave up.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
                                                volatile int* abort_flag, uint64_t limit_ns,
                                                uint32_t* status, uint32_t where) {
   bool ok = mbar_test_wait(bar, parity);
-  if (!ok) {
-    if (limit_ns != 0) {
-      ok = mbar_wait_bounded(bar, parity, abort_flag, limit_ns, status, where);
-    } else {
-      *abort_flag = 1;
-      record_status(status, kDevTimeout, where);
-    }
-  }
+  if (!ok) ok = mbar_wait_slow(bar, parity, abort_flag, limit_ns, status, where);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -201,6 +232,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  const uint4 v = lds128(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
 __device__ __forceinline__ void sts128(uint32_t a, float4 v) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z),
                "f"(v.w)
@@ -210,16 +249,35 @@ __device__ __forceinline__ void sts128(uint32_t a, float4 v) {
 // D (16 x 8, FP32) += A (16 x 16, BF16) * B (16 x 8, BF16).
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm(
+  asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D (16 x 8, INT32) += A (16 x 32, INT8) * B (32 x 8, INT8).
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with D = c + A * B.
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1, int c) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c));
+}
+
 // The MMA sums over k in any order as long as both operands agree: in each run of 32 elements
-// lane column c owns elements 8 c .. 8 c + 7 (one 16-byte load) and spends the first four on
-// the first MMA, the last four on the second.
+// lane column c owns elements 8 c .. 8 c + 7 (one 16-byte load of BF16); a BF16 run is two MMAs,
+// the first with the first four of each column, an INT8 run is one.
 
 // B fragments of one token row's K slice: `row` points at the slice (null: an unused column,
 // zeros), 4 registers per 32 elements.
@@ -260,60 +318,121 @@ __device__ __forceinline__ void bf16_slice(float (&acc)[4], const uint32_t (&b)[
   for (int i = 0; i < 4; ++i) acc[i] += d0[i] + d1[i];
 }
 
-// Two codes (nibbles at bits 0..3 and 16..19 of v) as exact BF16: 0x4300 | n is 128 + n, so
-// subtracting 136 leaves n - 8.
-__device__ __forceinline__ uint32_t i4_pair(uint32_t v) {
-  uint32_t u, d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(u) : "r"(v), "r"(0x000f000fu), "r"(0x43004300u));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(u), "r"(0x43084308u));
-  return d;
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// acc[nt] += 16 rows of 4-bit weights (`base`: the warp's first superblock) times the token
-// columns, over `units` superblocks.  The products of one group (or of the 64 elements of a
-// code block, if the group is longer) are summed exactly scaled: codes and tokens are exact in
-// BF16, the sum is FP32, and the group's scale multiplies it in FP32.
-template <int NT, int UNITS, int GROUP>
-__device__ __forceinline__ void i4_slice(float (&acc)[NT][4], const uint32_t (&b)[NT][UNITS * 16],
-                                         uint32_t base, int units, int lane) {
-  constexpr int kUnitBytes = i4_unit_bytes(GROUP);
+// Products with 4-bit weights run on INT8 MMAs for up to 8 tokens.  A code block of 16 rows x 64
+// columns takes 22 clocks of an SM to arrive (528 bytes at 6.5 TB/s over the GPU), and expanding it
+// to BF16 for m16n8k16 measured 20 whatever the number of warps: 28 shifts and masks, 16
+// subtractions and 4 MMAs of 2 clocks.  As 8-bit operands the codes take 12 shifts and masks and 2
+// MMAs of 2 clocks for each 8 columns of tokens, 9 clocks in all.  (E4M3 MMAs would take the codes
+// as they lie, but mma.sync expands E4M3 operands with ALU operations: 18.5 clocks.)
+//
+// The token is a 23-bit integer per element, in three signed 8-bit digits:
+//   x = 2^(E - 21) (65536 d0 + 256 d1 + d2),  2^E <= largest of the warp's K slice < 2^(E + 1)
+// which is x exactly for every element within 2^-14 of the slice's largest, and off by at most
+// 2^-22 of the largest otherwise -- a quarter step of FP32 in the sum that holds it.  The digits of a
+// token are columns of their own, in one of three arrangements by the number of tokens (MODE = MMAs
+// per run of 32):
+//   MODE 1, up to 2 tokens: column 2 p + t holds digit p of token t
+//   MODE 2, up to 4: of the first MMA column 4 p + t, p = 0, 1; of the second column t digit 2
+//   MODE 3, up to 8: MMA p, column t
+// Integer sums are exact.  A group's sum (|16 q d| <= 2^14, at most 128 of them) starts at the bit
+// pattern of 1.5 2^23, so that it is read as a float without a conversion.
+constexpr int kI4SumStart = 0x4b400000;
+constexpr float kI4SumStartF = 12582912.f;
+constexpr int kI4SliceMax = kFewMaxK / kFewWarps;
+constexpr int kI4SplitBytes = 3 * kI4SliceMax;  // a warp's buffer for the digits of one token
+constexpr int kI4NonFinite = 1 << 20;           // in the place of an exponent
+
+__host__ __device__ constexpr int i4_mode(int tokens) { return tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3; }
+
+// Splits the K slice of one token (`row`: its first element; n elements, a multiple of 128) over
+// the warp into its digits in `buf`; returns E - 25, the exponent of the result of digit d2 with
+// the codes' factor of 16, or kI4NonFinite.
+__device__ __forceinline__ int i4_split_token(const __nv_bfloat16* row, int n, uint8_t* buf,
+                                              int lane) {
+  constexpr int kLoads = kI4SliceMax / 256;  // 8 elements per lane and load
+  uint4 v[kLoads];
+  uint32_t top = 0;  // largest magnitude bits; NaN and infinity sort above
 #pragma unroll
-  for (int u = 0; u < UNITS; ++u) {
-    if (u < units) {
-      const uint32_t ub = base + u * kUnitBytes;
+  for (int i = 0; i < kLoads; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int k = (i * 32 + lane) * 8;
+    if (k < n) v[i] = __ldcg(reinterpret_cast<const uint4*>(row + k));
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const uint4 w4 = lds128(ub + blk * 512 + lane * 16);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        constexpr int kScaled = GROUP == 32 ? 2 : 1;  // scale changes inside a code block
+    for (int j = 0; j < 4; ++j)
+      top = max(top, max((w[j] << 16) & 0x7fff0000u, w[j] & 0x7fff0000u));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top >= 0x7f800000u) return kI4NonFinite;
+  const int E = max(static_cast<int>(top >> 23), 1) - 127;
+  // 2^(21 - E) in two factors, each a normal number
+  const int e1 = (21 - E) / 2, e2 = 21 - E - e1;
+  const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+  const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
 #pragma unroll
-        for (int p = 0; p < kScaled; ++p) {
-          const int gi = GROUP == 32 ? blk * 2 + p : GROUP == 64 ? blk : 0;
-          const uint32_t sc = lds32(ub + 1024 + gi * 32 + (lane >> 2) * 4);
-          float d[NT][4];
+  for (int i = 0; i < kLoads; ++i) {
+    const int k = (i * 32 + lane) * 8;
+    if (k >= n) break;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t d[3][2] = {};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+    for (int j = 0; j < 8; ++j) {
+      const float x = (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+      const int x2 = __float2int_rn(x * f1 * f2);
+      const int x1 = (x2 + 128) >> 8, x0 = (x1 + 128) >> 8;
+      const int at = 8 * (j & 3);
+      d[0][j >> 2] |= static_cast<uint32_t>(x0 & 255) << at;
+      d[1][j >> 2] |= static_cast<uint32_t>(x1 & 255) << at;
+      d[2][j >> 2] |= static_cast<uint32_t>(x2 & 255) << at;
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[nt][i] = 0.f;
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint2*>(buf + p * kI4SliceMax + k) = make_uint2(d[p][0], d[p][1]);
+  }
+  return E - 25;
+}
+
+// v 2^r for |r| <= 252, in two steps: 2^r itself may be out of range.
+__device__ __forceinline__ float scale_exp(float v, int r) {
+  if (r >= kI4NonFinite / 2) return __uint_as_float(0x7fc00000u);
+  return v * __uint_as_float(static_cast<uint32_t>(127 + r / 2) << 23) *
+         __uint_as_float(static_cast<uint32_t>(127 + r - r / 2) << 23);
+}
+
+// B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
+// row(t): the slice's first element of token t.  shift[h]: what i4_split_token returned for the
+// token of the lane's result column h.
+template <int MODE, int REGS, class Row>
+__device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], int (&shift)[2], Row row, int tokens,
+                                               int units, uint8_t* buf, int lane) {
+  constexpr int kRuns = REGS / (2 * MODE);
+  const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-          for (int v = p * (4 / kScaled); v < (p + 1) * (4 / kScaled); ++v) {
-            const uint32_t a0 = i4_pair(w[v]), a1 = i4_pair(w[v] >> 4), a2 = i4_pair(w[v] >> 8),
-                           a3 = i4_pair(w[v] >> 12);
+  for (int j = 0; j < REGS; ++j) b[j] = 0u;
+  shift[0] = shift[1] = 0;
+#pragma unroll 1
+  for (int t = 0; t < tokens; ++t) {
+    __syncwarp();
+    const int r = i4_split_token(row(t), units * kI4Unit, buf, lane);
+    __syncwarp();
+    const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of result column 0
+    if (t == first) shift[0] = r;
+    if (t == first + 1) shift[1] = r;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(d[nt], a0, a1, a2, a3, b[nt][(u * 2 + blk) * 8 + v * 2],
-                       b[nt][(u * 2 + blk) * 8 + v * 2 + 1]);
-          }
-          const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
+    for (int nt = 0; nt < MODE; ++nt) {
+      const int token = MODE == 1 ? (g & 1) : MODE == 2 ? (g & 3) : g;
+      const int digit = MODE == 1 ? (g >> 1) : MODE == 2 ? (nt ? 2 + (g >> 2) : (g >> 2)) : nt;
+      if (token == t && digit < 3) {
+        const uint8_t* p = buf + digit * kI4SliceMax + c * 8;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] = fmaf(s0, d[nt][0], acc[nt][0]);
-            acc[nt][1] = fmaf(s0, d[nt][1], acc[nt][1]);
-            acc[nt][2] = fmaf(s1, d[nt][2], acc[nt][2]);
-            acc[nt][3] = fmaf(s1, d[nt][3], acc[nt][3]);
+        for (int j = 0; j < kRuns; ++j) {
+          if (j < units * 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + j * 32);
+            b[(j * MODE + nt) * 2] = w.x;
+            b[(j * MODE + nt) * 2 + 1] = w.y;
           }
         }
       }
@@ -321,8 +440,188 @@ __device__ __forceinline__ void i4_slice(float (&acc)[NT][4], const uint32_t (&b
   }
 }
 
+// Sums of i4_slice, per MMA of a run.  Digits are kept apart to the end, so that a token's result has
+// the same bits in every arrangement.
+template <int MODE>
+struct I4Acc {
+  float v[MODE][4] = {};
+};
+
+// acc += 16 rows of 4-bit weights (`base`: the warp's first superblock) times the token digits, over
+// UNITS superblocks.  Each group is summed unscaled; its
+// scale multiplies the sum in FP32.
+template <int MODE, int GROUP, int UNITS, int REGS>
+__device__ __forceinline__ void i4_slice_of(I4Acc<MODE>& acc, const uint32_t (&b)[REGS], uint32_t base,
+                                            int lane) {
+  constexpr int kUnitBytes = i4_unit_bytes(GROUP);
+  constexpr uint32_t kMask = 0xf0f0f0f0u;
+  const uint32_t codes = base + lane * 16, scales = base + 1024 + (lane >> 2) * 4;
+  int d[MODE][4];
+  uint4 q;
+#pragma unroll
+  for (int j = 0; j < UNITS * 4; ++j) {  // runs of 32
+    const int u = j / 4, run = j % 4;
+    if (run % 2 == 0) q = lds128(codes + u * kUnitBytes + (run / 2) * 512);
+    const uint32_t lo = run % 2 ? q.z : q.x, hi = run % 2 ? q.w : q.y;
+    const uint32_t a0 = lo & kMask, a1 = (lo << 4) & kMask, a2 = hi & kMask, a3 = (hi << 4) & kMask;
+    constexpr int kRunsPerGroup = GROUP / 32;
+    const bool first = j % kRunsPerGroup == 0, last = j % kRunsPerGroup == kRunsPerGroup - 1;
+#pragma unroll
+    for (int nt = 0; nt < MODE; ++nt) {
+      const uint32_t b0 = b[(j * MODE + nt) * 2], b1 = b[(j * MODE + nt) * 2 + 1];
+      if (first)
+        mma_s8_first(d[nt], a0, a1, a2, a3, b0, b1, kI4SumStart);
+      else
+        mma_s8(d[nt], a0, a1, a2, a3, b0, b1);
+    }
+    if (last) {
+      const uint32_t s = lds32(scales + u * kUnitBytes + (run / kRunsPerGroup) * 32);
+      const float sc[2] = {bf16_lo(s), bf16_hi(s)};
+#pragma unroll
+      for (int nt = 0; nt < MODE; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc.v[nt][i] = fmaf(sc[i >> 1], __int_as_float(d[nt][i]) - kI4SumStartF, acc.v[nt][i]);
+    }
+  }
+}
+
+// One straight run of code for each number of superblocks: with a branch after every superblock
+// the loads and products of two of them do not overlap (a fifth slower).
+template <int GROUP, int MODE, int REGS>
+__device__ __forceinline__ void i4_slice(I4Acc<MODE>& acc, const uint32_t (&b)[REGS], uint32_t base,
+                                         int units, int lane) {
+  constexpr int kMax = REGS / (8 * MODE);
+  switch (units) {
+    case 1: i4_slice_of<MODE, GROUP, 1>(acc, b, base, lane); break;
+    case 2: i4_slice_of<MODE, GROUP, 2>(acc, b, base, lane); break;
+    case 3: i4_slice_of<MODE, GROUP, 3>(acc, b, base, lane); break;
+    case 4: i4_slice_of<MODE, GROUP, 4>(acc, b, base, lane); break;
+    case 5: if constexpr (kMax >= 5) i4_slice_of<MODE, GROUP, 5>(acc, b, base, lane); break;
+    case 6: if constexpr (kMax >= 6) i4_slice_of<MODE, GROUP, 6>(acc, b, base, lane); break;
+    case 7: if constexpr (kMax >= 7) i4_slice_of<MODE, GROUP, 7>(acc, b, base, lane); break;
+    case 8: if constexpr (kMax >= 8) i4_slice_of<MODE, GROUP, 8>(acc, b, base, lane); break;
+    default: break;
+  }
+}
+
+// The warp's partial tile of a slice: rows g, g of tokens 2 c, 2 c + 1, then rows g + 8.  Digits in
+// different lanes are added here.
+template <int MODE>
+__device__ __forceinline__ float4 i4_result(const I4Acc<MODE>& acc, const int (&shift)[2], int lane) {
+  const int c = lane & 3;
+  float o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = shift[i & 1];
+    if constexpr (MODE == 1) {  // lanes c hold digit c; lanes 3 zeros
+      o[i] = scale_exp(acc.v[0][i], r + 8 * (2 - (c < 3 ? c : 2)));
+      o[i] += __shfl_xor_sync(0xffffffffu, o[i], 1);
+      o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
+    } else if constexpr (MODE == 2) {  // lanes 0, 1 hold digits 0 and 2, lanes 2, 3 digit 1
+      o[i] = scale_exp(acc.v[0][i], r + 8 * (2 - (c >> 1)));
+      o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
+      o[i] += scale_exp(acc.v[1][i], r);
+    } else {
+      o[i] = scale_exp(acc.v[0][i], r + 16) + scale_exp(acc.v[1][i], r + 8) + scale_exp(acc.v[2][i], r);
+    }
+  }
+  return make_float4(o[0], o[1], o[2], o[3]);
+}
+
+// ---- 9 to 16 tokens: BF16 MMAs, two sets of 8 columns
+
+// Two codes (two's complement, bits 0..3 and 16..19 of v) as exact BF16: with the sign bit inverted
+// a code is q + 8, 0x4300 | (q + 8) is the BF16 value 136 + q.
+__device__ __forceinline__ uint32_t i4_pair(uint32_t v) {
+  uint32_t u, d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(u) : "r"(v), "r"(0x000f000fu), "r"(0x43084308u));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(u), "r"(0x43084308u));
+  return d;
+}
+
+// B fragments, 8 registers a run: per set of 8 tokens, the four registers of load_tokens with the
+// elements of each four paired (0, 2), (1, 3) as the codes' bytes are.
+template <int RUNS, class Row>
+__device__ __forceinline__ void i4_load_tokens16(uint32_t (&b)[RUNS * 8], Row row, int tokens, int units,
+                                                 int lane) {
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    const int t = nt * 8 + (lane >> 2);
+    const __nv_bfloat16* p = t < tokens ? row(t) + (lane & 3) * 8 : nullptr;
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (p != nullptr && j < units * 4) v = __ldcg(reinterpret_cast<const uint4*>(p + j * 32));
+      b[(j * 2 + nt) * 4 + 0] = __byte_perm(v.x, v.y, 0x5410);
+      b[(j * 2 + nt) * 4 + 1] = __byte_perm(v.x, v.y, 0x7632);
+      b[(j * 2 + nt) * 4 + 2] = __byte_perm(v.z, v.w, 0x5410);
+      b[(j * 2 + nt) * 4 + 3] = __byte_perm(v.z, v.w, 0x7632);
+    }
+  }
+}
+
+template <int GROUP, int UNITS, int REGS>
+__device__ __forceinline__ void i4_slice16_of(float (&acc)[2][4], const uint32_t (&b)[REGS], uint32_t base,
+                                              int lane) {
+  constexpr int kUnitBytes = i4_unit_bytes(GROUP);
+  const uint32_t codes = base + lane * 16, scales = base + 1024 + (lane >> 2) * 4;
+  float d[2][4];
+  uint4 q;
+#pragma unroll
+  for (int j = 0; j < UNITS * 4; ++j) {  // runs of 32
+    const int u = j / 4, run = j % 4;
+    if (run % 2 == 0) q = lds128(codes + u * kUnitBytes + (run / 2) * 512);
+    constexpr int kRunsPerGroup = GROUP / 32;
+    const bool first = j % kRunsPerGroup == 0, last = j % kRunsPerGroup == kRunsPerGroup - 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = run % 2 ? (h ? q.w : q.z) : (h ? q.y : q.x);
+      const uint32_t a0 = i4_pair(w >> 4), a1 = i4_pair(w), a2 = i4_pair(w >> 12), a3 = i4_pair(w >> 8);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        if (first && h == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[nt][i] = 0.f;
+        }
+        mma_bf16(d[nt], a0, a1, a2, a3, b[(j * 2 + nt) * 4 + h * 2], b[(j * 2 + nt) * 4 + h * 2 + 1]);
+      }
+    }
+    if (last) {
+      const uint32_t s = lds32(scales + u * kUnitBytes + (run / kRunsPerGroup) * 32);
+      const float sc[2] = {bf16_lo(s), bf16_hi(s)};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][i] = fmaf(sc[i >> 1], d[nt][i], acc[nt][i]);
+    }
+  }
+}
+
+template <int GROUP, int REGS>
+__device__ __forceinline__ void i4_slice16(float (&acc)[2][4], const uint32_t (&b)[REGS], uint32_t base,
+                                           int units, int lane) {
+  static_assert(REGS == 128, "four superblocks");
+  switch (units) {
+    case 1: i4_slice16_of<GROUP, 1>(acc, b, base, lane); break;
+    case 2: i4_slice16_of<GROUP, 2>(acc, b, base, lane); break;
+    case 3: i4_slice16_of<GROUP, 3>(acc, b, base, lane); break;
+    case 4: i4_slice16_of<GROUP, 4>(acc, b, base, lane); break;
+    default: break;
+  }
+}
+
 // SiLU(g) * u in FP32.
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() {

@@ -3,6 +3,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 namespace beam {
 namespace {
 
@@ -189,16 +191,16 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, FewShared& s
   }
 }
 
-// Lists the touched experts ascending, 8 tokens at most to an entry (a ninth token of an expert
-// opens a second entry that reads its weights again: with at most 16 tokens that takes a
-// routing where more than half of them agree).  Run by one warp.
+// Lists the touched experts ascending, entry_max tokens at most to an entry (one more token of an
+// expert opens a second entry that reads its weights again: with 8 to an entry and at most 16 tokens
+// that takes a routing where more than half of them agree).  Run by one warp.
 __device__ void few_entries(const FewLayerArgs& a, FewShared& sh, int lane) {
   int base = 0;
 #pragma unroll 1
   for (int e0 = 0; e0 < a.E; e0 += 32) {
     const int e = e0 + lane;
     uint32_t m = e < a.E ? sh.mask[e] : 0u;
-    const int need = (__popc(m) + kFewCols - 1) / kFewCols;
+    const int need = (__popc(m) + a.entry_max - 1) / a.entry_max;
     int incl = need;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -208,7 +210,7 @@ __device__ void few_entries(const FewLayerArgs& a, FewShared& sh, int lane) {
     int at = base + incl - need;
     for (int p = 0; p < need; ++p, ++at) {
       int n = 0;
-      while (m && n < kFewCols) {
+      while (m && n < a.entry_max) {
         const int t = __ffs(m) - 1;
         m &= m - 1;
         int j = 0;
@@ -235,13 +237,14 @@ __device__ void few_entries(const FewLayerArgs& a, FewShared& sh, int lane) {
 // Each CTA takes one contiguous run of items of either phase, cut so that both runs together are
 // the same number of weight bytes for every CTA; its producer goes from the first into the second
 // without waiting for anything but ring space, so the weights keep streaming while activations
-// cross the GPU.  GROUP = 0: BF16 weights.  HBM-bound on the touched experts' bytes.
-template <int GROUP>
+// cross the GPU.  GROUP = 0: BF16 weights.  MODES: the largest i4_mode of an entry.  HBM-bound on the touched experts' bytes.
+template <int GROUP, int MODES>
 __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLayerArgs a) {
   constexpr bool kI4 = GROUP != 0;
   constexpr int kUnit = kI4 ? kI4Unit : kBf16Unit;                       // K elements
   constexpr int kUnitBytes = kI4 ? i4_unit_bytes(kI4 ? GROUP : 128) : 0;  // packed bytes
   constexpr int kRuns = kFewMaxK / kFewWarps / 32;                       // runs of 32 per warp
+  constexpr int kRed = kI4 ? kFewRed : kBf16Red;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       mbar_init(smem_u32(&sh.full_bar[i]), 1);
       mbar_init(smem_u32(&sh.empty_bar[i]), kFewWarps);
     }
-    for (int i = 0; i < kFewRed; ++i) {
+    for (int i = 0; i < kRed; ++i) {
       mbar_init(smem_u32(&sh.red_full[i]), kFewWarps);
       mbar_init(smem_u32(&sh.red_empty[i]), 1);
     }
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
   float2* sc = reinterpret_cast<float2*>(smem);
   for (int i = threadIdx.x; i < a.T * a.E; i += kFewThreads) sc[i] = a.sc[i];
   __syncthreads();
-  if (warp < a.T) few_select(a, sc + warp * a.E, sh, warp, lane);
+  for (int t = warp; t < a.T; t += kFewThreads / 32) few_select(a, sc + t * a.E, sh, t, lane);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic reads before bulk writes
   __syncthreads();
   if (warp == 0) few_entries(a, sh, lane);
@@ -290,68 +293,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
   const int i1 = static_cast<int>(first1(blockIdx.x)), j1 = static_cast<int>(first1(blockIdx.x + 1));
   const int i2 = static_cast<int>(first2(blockIdx.x)), j2 = static_cast<int>(first2(blockIdx.x + 1));
 
-  if (warp == kFewWarps) {
-    // ---- producer
-    int slot = 0;
-    uint32_t par = 1, issued = 0;
-    bool ok = true;
-#pragma unroll 1
-    for (int ph = 0; ph < 2 && ok; ++ph) {
-      const KSplit ks = ph ? a.k2 : a.k1;
-      const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
-      const int cw = 1 << ks.log_cw;
-      int entry = (ph ? i2 : i1) / per, tile = (ph ? i2 : i1) % per;
-#pragma unroll 1
-      for (int it = ph ? i2 : i1; it < (ph ? j2 : j1) && ok; ++it) {
-        const int e = sh.entry_e[entry];
-        const uint8_t* src;
-        if (kI4) {
-          src = static_cast<const uint8_t*>(ph ? a.w_down : a.w_gate) +
-                (static_cast<size_t>(e) * per + tile) * ks.n * kUnitBytes;
-        } else {  // lane r < 16 copies row r of the tile
-          const int r = lane & 15;
-          const void* m = ph ? a.w_down : (r < 8 ? a.w_gate : a.w_up);
-          const size_t row = ph ? static_cast<size_t>(e) * a.d + tile * 16 + r
-                                : static_cast<size_t>(e) * a.I + tile * 8 + (r & 7);
-          src = static_cast<const uint8_t*>(m) + row * K * 2;
-        }
-        for (int w = 0; w < kFewWarps; w += cw) {
-          ok = mbar_wait_warp(smem_u32(&sh.empty_bar[slot]), par, abort_flag, a.wait_limit_ns,
-                              a.status, kWhereFew);
-          if (!ok) break;
-          const int s = ks.start(w), n = ks.start(w + cw) - s;
-          const uint32_t bar = smem_u32(&sh.full_bar[slot]);
-          const uint32_t dst = ring + slot * a.slot_bytes;
-          if (lane == 0) mbar_arrive_expect_tx(bar, kI4 ? n * kUnitBytes : 16 * n * 64);
-          __syncwarp();
-          if (kI4) {
-            if (lane == 0)
-              bulk_load(dst, src + static_cast<size_t>(s) * kUnitBytes, n * kUnitBytes, bar);
-          } else if (lane < 16 && n > 0) {
-            bulk_load(dst + lane * bf16_row_stride(n), src + static_cast<size_t>(s) * 64, n * 64, bar);
-          }
-          ++issued;
-          if (++slot == a.stages) {
-            slot = 0;
-            par ^= 1;
-          }
-        }
-        if (++tile == per) {
-          tile = 0;
-          ++entry;
-        }
-      }
-    }
-    if (!ok) {  // copies in flight must land before this CTA's shared memory is given up
-      volatile int never = 0;
-      const uint32_t back = issued < static_cast<uint32_t>(a.stages) ? issued : a.stages;
-      for (uint32_t i = issued - back; i < issued; ++i)
-        mbar_wait_bounded(smem_u32(&sh.full_bar[i % a.stages]), (i / a.stages) & 1, &never,
-                          2000000000ull, nullptr, 0);
-    }
-  } else if (warp < kFewWarps) {
+  if (warp < kFewWarps) {
+    more_registers<kFewRegsConsumer>();
     // ---- consumers
-    uint32_t b[1][kRuns * 4];
+    // token fragments: BF16 4 registers a run of 32; INT8 digits 2, 4 or 6 (up to 20 runs)
+    uint32_t b[kI4 && MODES == 1 ? 64 : 128];
+    [[maybe_unused]] int shift[2];
+    [[maybe_unused]] uint8_t* const split =
+        smem + a.stages * a.slot_bytes + kRed * kFewWarps * 512 + warp * kI4SplitBytes;
+    int n_tok = 0;
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
     bool ok = true;
@@ -360,9 +310,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       const KSplit ks = ph ? a.k2 : a.k1;
       const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
       const int first = ph ? i2 : i1, last = ph ? j2 : j1;
-      const int units = ks.count(warp), mine = warp >> ks.log_cw, chunks = ks.chunks();
-      const int cstart = ks.start(mine << ks.log_cw);
-      const int cunits = ks.start((mine + 1) << ks.log_cw) - cstart;
+      const int units = ks.count(warp), mine = warp / ks.cw, chunks = ks.chunks();
+      const int cstart = ks.start(mine * ks.cw);
+      const int cunits = ks.start((mine + 1) * ks.cw) - cstart;
       const int uoff = ks.start(warp) - cstart;
       const uint32_t off = kI4 ? uoff * kUnitBytes : uoff * 64;
       const int stride = bf16_row_stride(cunits);
@@ -398,16 +348,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          const int col = lane >> 2;
-          const __nv_bfloat16* row = nullptr;
-          if (col < sh.entry_n[entry]) {
+          n_tok = sh.entry_n[entry];
+          auto row = [&](int col) {
             const int s = sh.entry_slot[entry][col];
-            row = ph ? a.act + static_cast<size_t>(s) * K + k0
-                     : a.h + static_cast<size_t>(s / a.k) * K + k0;
+            return ph ? a.act + static_cast<size_t>(s) * K + k0
+                      : a.h + static_cast<size_t>(s / a.k) * K + k0;
+          };
+          if constexpr (kI4) {
+            if (MODES == 1 || n_tok <= 2)
+              i4_load_tokens<1>(b, shift, row, n_tok, units, split, lane);
+            else if (MODES == 2 || n_tok <= 4)
+              i4_load_tokens<(MODES > 1 ? 2 : 1)>(b, shift, row, n_tok, units, split, lane);
+            else
+              i4_load_tokens<MODES>(b, shift, row, n_tok, units, split, lane);
+          } else {
+            const int col = lane >> 2;
+            load_tokens<kRuns, true>(b, col < n_tok ? row(col) : nullptr, units, lane & 3);
           }
-          load_tokens<kRuns, true>(b[0], row, units * (kUnit / 32), lane & 3);
         }
-        float acc[1][4] = {};
+        float4 part = make_float4(0.f, 0.f, 0.f, 0.f);  // rows g, g of two tokens, then g + 8
         // every warp passes every chunk in order: a phase may only be waited for by who has seen
         // the slot's phase before
 #pragma unroll 1
@@ -417,10 +376,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           if (!ok) break;
           if (ch == mine) {
             const uint32_t base = ring + slot * a.slot_bytes + off;
-            if constexpr (kI4)
-              i4_slice<1, kRuns / 4, kI4 ? GROUP : 128>(acc, b, base, units, lane);
-            else
-              bf16_slice<kRuns>(acc[0], b[0], base, stride, units, lane);
+            if constexpr (kI4) {
+              constexpr std::integral_constant<int, kI4 ? GROUP : 128> kG{};
+              auto product = [&](auto acc) {
+                i4_slice<kG.value>(acc, b, base, units, lane);
+                part = i4_result(acc, shift, lane);
+              };
+              if (MODES == 1 || n_tok <= 2)
+                product(I4Acc<1>{});
+              else if (MODES == 2 || n_tok <= 4)
+                product(I4Acc<(MODES > 1 ? 2 : 1)>{});
+              else
+                product(I4Acc<MODES>{});
+            } else {
+              float acc[4] = {};
+              bf16_slice<kRuns>(acc, b, base, stride, units, lane);
+              part = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty_bar[slot]));
@@ -434,11 +406,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
                             kWhereFew + 3);
         if (!ok) break;
         if (units > 0)
-          sts128(red + (rb * kFewWarps + warp) * 512 + lane * 16,
-                 make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]));
+          sts128(red + (rb * kFewWarps + warp) * 512 + lane * 16, part);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.red_full[rb]));
-        if (++rb == kFewRed) {
+        if (++rb == kRed) {
           rb = 0;
           rpar ^= 1;
         }
@@ -448,7 +419,69 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
         }
       }
     }
+    __syncwarp();
+    fewer_registers<kFewRegsLaunch>();
   } else {
+    fewer_registers<kFewRegsOther>();
+  if (warp == kFewWarps) {
+    // ---- producer
+    int slot = 0;
+    uint32_t par = 1, issued = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int ph = 0; ph < 2 && ok; ++ph) {
+      const KSplit ks = ph ? a.k2 : a.k1;
+      const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
+      int entry = (ph ? i2 : i1) / per, tile = (ph ? i2 : i1) % per;
+#pragma unroll 1
+      for (int it = ph ? i2 : i1; it < (ph ? j2 : j1) && ok; ++it) {
+        const int e = sh.entry_e[entry];
+        const uint8_t* src;
+        if (kI4) {
+          src = static_cast<const uint8_t*>(ph ? a.w_down : a.w_gate) +
+                (static_cast<size_t>(e) * per + tile) * ks.n * kUnitBytes;
+        } else {  // lane r < 16 copies row r of the tile
+          const int r = lane & 15;
+          const void* m = ph ? a.w_down : (r < 8 ? a.w_gate : a.w_up);
+          const size_t row = ph ? static_cast<size_t>(e) * a.d + tile * 16 + r
+                                : static_cast<size_t>(e) * a.I + tile * 8 + (r & 7);
+          src = static_cast<const uint8_t*>(m) + row * K * 2;
+        }
+        for (int w = 0; w < kFewWarps; w += ks.cw) {
+          ok = mbar_wait_warp(smem_u32(&sh.empty_bar[slot]), par, abort_flag, a.wait_limit_ns,
+                              a.status, kWhereFew);
+          if (!ok) break;
+          const int s = ks.start(w), n = ks.start(w + ks.cw) - s;
+          const uint32_t bar = smem_u32(&sh.full_bar[slot]);
+          const uint32_t dst = ring + slot * a.slot_bytes;
+          if (lane == 0) mbar_arrive_expect_tx(bar, kI4 ? n * kUnitBytes : 16 * n * 64);
+          __syncwarp();
+          if (kI4) {
+            if (lane == 0)
+              bulk_load(dst, src + static_cast<size_t>(s) * kUnitBytes, n * kUnitBytes, bar);
+          } else if (lane < 16 && n > 0) {
+            bulk_load(dst + lane * bf16_row_stride(n), src + static_cast<size_t>(s) * 64, n * 64, bar);
+          }
+          ++issued;
+          if (++slot == a.stages) {
+            slot = 0;
+            par ^= 1;
+          }
+        }
+        if (++tile == per) {
+          tile = 0;
+          ++entry;
+        }
+      }
+    }
+    if (!ok) {  // copies in flight must land before this CTA's shared memory is given up
+      volatile int never = 0;
+      const uint32_t back = issued < static_cast<uint32_t>(a.stages) ? issued : a.stages;
+      for (uint32_t i = issued - back; i < issued; ++i)
+        mbar_wait_bounded(smem_u32(&sh.full_bar[i % a.stages]), (i / a.stages) & 1, &never,
+                          2000000000ull, nullptr, 0);
+    }
+  } else if (warp == kFewWarps + 1) {
     // ---- finishing warp
     const int g = lane >> 2, c = lane & 3;
     int rb = 0;
@@ -477,7 +510,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.red_empty[rb]));
-        if (++rb == kFewRed) {
+        if (++rb == kRed) {
           rb = 0;
           rpar ^= 1;
         }
@@ -515,6 +548,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       }
     }
   }
+    __syncwarp();
+    more_registers<kFewRegsLaunch>();
+  }
 
   // ---- combine: the output tiles whose last item this CTA finished
   __syncthreads();
@@ -546,17 +582,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
 }
 
 using LayerKernel = void (*)(FewLayerArgs);
-LayerKernel layer_kernel(int group) {
-  return group == 0    ? few_layer_kernel<0>
-         : group == 32 ? few_layer_kernel<32>
-         : group == 64 ? few_layer_kernel<64>
-                       : few_layer_kernel<128>;
+template <int GROUP>
+LayerKernel layer_kernel_of(int modes) {
+  return modes == 1 ? few_layer_kernel<GROUP, 1> : modes == 2 ? few_layer_kernel<GROUP, 2>
+                                                              : few_layer_kernel<GROUP, 3>;
+}
+LayerKernel layer_kernel(int group, int modes) {
+  return group == 0    ? few_layer_kernel<0, 0>
+         : group == 32 ? layer_kernel_of<32>(modes)
+         : group == 64 ? layer_kernel_of<64>(modes)
+                       : layer_kernel_of<128>(modes);
 }
 
 constexpr size_t kFewDynamicSmem = kFewSmemMax - 6144;  // the rest: FewShared
 static_assert(sizeof(FewShared) <= 6144, "FewShared must fit beside the ring");
 // the scores of 16 tokens fit in the ring
-static_assert(kFewMaxTokens * kMaxE * 8 <= 2 * kFewSlotBytes, "scores must fit in the ring");
+static_assert(kFewMaxTokens * kMaxE * 8 <= kI4SlotBytes && kFewMaxTokens * kMaxE * 8 <= kBf16SlotBytes, "scores must fit in the ring");
 
 }  // namespace
 
@@ -577,10 +618,13 @@ cudaError_t launch_few_router(const FewRouterArgs& a, cudaStream_t s) {
 
 cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
-  a.k1 = make_ksplit(a.d / unit, kFewSlotBytes, unit_bytes);
-  a.k2 = make_ksplit(a.I / unit, kFewSlotBytes, unit_bytes);
-  const size_t red = static_cast<size_t>(kFewRed) * kFewWarps * 512;
-  a.slot_bytes = kFewSlotBytes;
+  // the digits of 8 tokens fit in a warp's registers up to K = 5120, those of 4 up to 8192
+  a.entry_max = group && (a.d > 5120 || a.I > 5120) ? 4 : kFewCols;
+  a.slot_bytes = group ? kI4SlotBytes : kBf16SlotBytes;
+  a.k1 = make_ksplit(a.d / unit, a.slot_bytes, unit_bytes);
+  a.k2 = make_ksplit(a.I / unit, a.slot_bytes, unit_bytes);
+  const size_t red = static_cast<size_t>(group ? kFewRed : kBf16Red) * kFewWarps * 512 +
+                     (group ? static_cast<size_t>(kFewWarps) * kI4SplitBytes : 0);
   a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);
   if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
   // no more CTAs than gate|up items can exist
@@ -596,16 +640,17 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, layer_kernel(group), a);
+  return cudaLaunchKernelEx(&cfg, layer_kernel(group, i4_mode(a.T < a.entry_max ? a.T : a.entry_max)), a);
 }
 
 cudaError_t prepare_few_kernels() {
-  for (int group : {0, 32, 64, 128}) {
-    const cudaError_t e = cudaFuncSetAttribute(layer_kernel(group),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kFewDynamicSmem));
-    if (e != cudaSuccess) return e;
-  }
+  for (int group : {0, 32, 64, 128})
+    for (int modes : {1, 2, 3}) {
+      const cudaError_t e = cudaFuncSetAttribute(layer_kernel(group, modes),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(kFewDynamicSmem));
+      if (e != cudaSuccess) return e;
+    }
   return cudaSuccess;
 }
 

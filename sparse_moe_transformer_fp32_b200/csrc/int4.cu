@@ -78,10 +78,8 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const Int4QuantArgs 
         const float x = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
         float q = s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
         q = fminf(fmaxf(q, -8.f), 7.f);
-        const uint32_t n = static_cast<uint32_t>(static_cast<int>(q) + 8) & 15u;
-        // word 2 j + i / 4; element pair (i % 4) / 2 of row half h is nibble h + 2 ((i % 4) / 2),
-        // its second element four nibbles up
-        word[j * 2 + (i >> 2)] |= n << (4 * (h + 2 * ((i & 3) >> 1) + 4 * (i & 1)));
+        const uint32_t n = static_cast<uint32_t>(static_cast<int>(q)) & 15u;
+        word[j * 2 + (i >> 2)] |= n << (8 * (i & 3) + (h ? 0 : 4));
       }
     }
   }
@@ -151,7 +149,7 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
   return __all_sync(0xffffffffu, ok);
 }
 
-// y = x W^T, T <= 8 NT tokens.  A tile is 16 rows of W; a cluster of C CTAs shares a tile, each
+// y = x W^T; MODE 1, 2, 3: up to 2, 4, 8 tokens on INT8 MMAs, 4: up to 16 on BF16 MMAs.  A tile is 16 rows of W; a cluster of C CTAs shares a tile, each
 // taking a K range, and the CTA whose turn it is (tile index mod C) receives the others' partial
 // tiles in its shared memory and adds them in rank order.  C > 1 is for matrices with few tiles
 // (the spread over 148 SMs would be uneven) and for K ranges whose token fragments do not fit in
@@ -161,11 +159,16 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
 // previous kernel of the stream drains; tokens are read, and outputs written, after
 // griddepcontrol.wait.  (Weights written by the previous kernel are safe: only kernels of this
 // kind let their successor start early, and they write no weights.)
-template <int NT, int GROUP>
+// Superblocks per warp at most: 64 (MODE 1) or up to 128 registers of token fragments.
+__host__ __device__ constexpr int lin_units(int mode) { return mode <= 2 ? 8 : mode == 3 ? 5 : 4; }
+__host__ __device__ constexpr int lin_sets(int mode) { return mode == 4 ? 2 : 1; }  // of 8 tokens
+
+template <int MODE, int GROUP>
 __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4LinearArgs a) {
-  constexpr int kUnits = NT == 1 ? 4 : 2;  // superblocks per warp: 64 registers of fragments
+  constexpr int kUnits = lin_units(MODE);
+  constexpr int kSets = lin_sets(MODE);
   constexpr int kUnitBytes = i4_unit_bytes(GROUP);
-  constexpr int kRedBytes = 512 * NT;      // one partial tile
+  constexpr int kRedBytes = 512 * kSets;   // one partial tile
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[kFewMaxStages], empty_bar[kFewMaxStages];
   __shared__ __align__(8) uint64_t red_full[kFewRed], red_empty[kFewRed];
@@ -176,6 +179,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   const uint32_t ring = smem_u32(smem);
   const uint32_t red = ring + a.stages * a.slot_bytes;
   const uint32_t recv = red + kFewRed * kFewWarps * kRedBytes;
+  [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kRedBytes +
+                         kLinRecv * (a.cluster - 1) * kRedBytes + (threadIdx.x >> 5) * kI4SplitBytes;
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
@@ -206,9 +211,71 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   const int units_all = a.K / kI4Unit;
   const int u0 = rank * units_all / C, u1 = (rank + 1) * units_all / C;
   // the chunk size is chosen on the host for the largest K range
-  KSplit ks{u1 - u0, a.log_cw};
-  const int cw = 1 << a.log_cw;
+  const KSplit ks{u1 - u0, a.cw};
 
+  if (warp < kFewWarps) {
+    more_registers<kFewRegsConsumer>();
+    // ---- consumers
+    const int units = ks.count(warp), mine = warp / ks.cw, chunks = ks.chunks();
+    const uint32_t off = (ks.start(warp) - ks.start(mine * ks.cw)) * kUnitBytes;
+    uint32_t b[kUnits * 8 * MODE];
+    [[maybe_unused]] int shift[2];
+    pdl_wait();
+    const __nv_bfloat16* x0 = a.x + static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit;
+    auto row = [&](int t) { return x0 + static_cast<size_t>(t) * a.K; };
+    if constexpr (MODE == 4)
+      i4_load_tokens16<kUnits * 4>(b, row, a.T, units, lane);
+    else
+      i4_load_tokens<MODE>(b, shift, row, a.T, units, split, lane);
+    int slot = 0, rb = 0;
+    uint32_t par = 0, rpar = 1;
+    bool ok = true;
+    for (int tile = tile0; tile < tile1; ++tile) {
+      float4 part[kSets];
+      // every warp passes every chunk in order: a phase may only be waited for by who has seen the
+      // slot's phase before
+#pragma unroll 1
+      for (int ch = 0; ch < chunks; ++ch) {
+        ok = mbar_wait_warp(smem_u32(&full_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
+        if (!ok) break;
+        if (ch == mine) {
+          const uint32_t base = ring + slot * a.slot_bytes + off;
+          if constexpr (MODE == 4) {
+            float acc[2][4] = {};
+            i4_slice16<GROUP>(acc, b, base, units, lane);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) part[i] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+          } else {
+            I4Acc<MODE> acc;
+            i4_slice<GROUP>(acc, b, base, units, lane);
+            part[0] = i4_result(acc, shift, lane);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[slot]));
+        if (++slot == a.stages) {
+          slot = 0;
+          par ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (!mbar_wait_warp(smem_u32(&red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0)) break;
+      if (units > 0) {
+#pragma unroll
+        for (int i = 0; i < kSets; ++i)
+          sts128(red + (rb * kFewWarps + warp) * kRedBytes + i * 512 + lane * 16, part[i]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&red_full[rb]));
+      if (++rb == kFewRed) {
+        rb = 0;
+        rpar ^= 1;
+      }
+    }
+    __syncwarp();
+    fewer_registers<kFewRegsLaunch>();
+  } else {
+    fewer_registers<kFewRegsOther>();
   if (warp == kFewWarps) {
     // ---- producer
     int slot = 0;
@@ -216,11 +283,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     bool ok = true;
     for (int tile = tile0; tile < tile1 && ok; ++tile) {
       const uint8_t* src = a.w + (static_cast<size_t>(tile) * units_all + u0) * kUnitBytes;
-      for (int w = 0; w < kFewWarps; w += cw) {
+      for (int w = 0; w < kFewWarps; w += ks.cw) {
         ok = mbar_wait_warp(smem_u32(&empty_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
         if (!ok) break;
         if (lane == 0) {
-          const int s = ks.start(w), n = ks.start(w + cw) - s;
+          const int s = ks.start(w), n = ks.start(w + ks.cw) - s;
           const uint32_t bar = smem_u32(&full_bar[slot]);
           mbar_arrive_expect_tx(bar, n * kUnitBytes);
           bulk_load(ring + slot * a.slot_bytes, src + static_cast<size_t>(s) * kUnitBytes,
@@ -240,56 +307,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         mbar_wait_bounded(smem_u32(&full_bar[i % a.stages]), (i / a.stages) & 1, &never,
                           2000000000ull, nullptr, 0);
     }
-  } else if (warp < kFewWarps) {
-    // ---- consumers
-    const int units = ks.count(warp), mine = warp >> a.log_cw, chunks = ks.chunks();
-    const uint32_t off = (ks.start(warp) - ks.start(mine << a.log_cw)) * kUnitBytes;
-    uint32_t b[NT][kUnits * 16];
-    pdl_wait();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int t = nt * kFewCols + (lane >> 2);
-      load_tokens<kUnits * 4, true>(
-          b[nt],
-          t < a.T ? a.x + static_cast<size_t>(t) * a.K + static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit
-                  : nullptr,
-          units * 4, lane & 3);
-    }
-    int slot = 0, rb = 0;
-    uint32_t par = 0, rpar = 1;
-    bool ok = true;
-    for (int tile = tile0; tile < tile1; ++tile) {
-      float acc[NT][4] = {};
-      // every warp passes every chunk in order: a phase may only be waited for by who has seen the
-      // slot's phase before
-#pragma unroll 1
-      for (int ch = 0; ch < chunks; ++ch) {
-        ok = mbar_wait_warp(smem_u32(&full_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
-        if (!ok) break;
-        if (ch == mine) i4_slice<NT, kUnits, GROUP>(acc, b, ring + slot * a.slot_bytes + off, units, lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[slot]));
-        if (++slot == a.stages) {
-          slot = 0;
-          par ^= 1;
-        }
-      }
-      if (!ok) break;
-      if (!mbar_wait_warp(smem_u32(&red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0)) break;
-      if (units > 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          sts128(red + (rb * kFewWarps + warp) * kRedBytes + nt * 512 + lane * 16,
-                 make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&red_full[rb]));
-      if (++rb == kFewRed) {
-        rb = 0;
-        rpar ^= 1;
-      }
-    }
-  } else {
+  } else if (warp == kFewWarps + 1) {
     // ---- finishing warp
     const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
     const int g = lane >> 2, c = lane & 3;
@@ -298,21 +316,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     bool ok = true;
     pdl_wait();
     for (int i = 0; i < tile1 - tile0; ++i) {
-      float4 v[NT];
+      float4 v[kSets];  // rows g, g of tokens 2 c, 2 c + 1, then rows g + 8
       if (ok) ok = mbar_wait_warp(smem_u32(&red_full[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0);
       if (ok) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) v[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < kSets; ++s) v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int w = 0; w < active; ++w) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 p = lds128(red + (rb * kFewWarps + w) * kRedBytes + nt * 512 + lane * 16);
-            v[nt].x += __uint_as_float(p.x);
-            v[nt].y += __uint_as_float(p.y);
-            v[nt].z += __uint_as_float(p.z);
-            v[nt].w += __uint_as_float(p.w);
-          }
+          for (int s = 0; s < kSets; ++s)
+            v[s] = add4(v[s], lds_f4(red + (rb * kFewWarps + w) * kRedBytes + s * 512 + lane * 16));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&red_empty[rb]));
@@ -333,34 +346,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
             const uint32_t dst =
                 map_rank(recv + (slot * (C - 1) + src) * kRedBytes + lane * 16, owner);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) remote_store(dst + nt * 512, v[nt]);
+            for (int s = 0; s < kSets; ++s) remote_store(dst + s * 512, v[s]);
             __syncwarp();
             if (lane == 0) remote_arrive(map_rank(smem_u32(&recv_full[slot]), owner));
           }
         } else {
           ok = wait_cluster(smem_u32(&recv_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns);
           if (ok) {
-            float4 own[NT];
+            float4 own[kSets];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              own[nt] = v[nt];
-              v[nt] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = 0; s < kSets; ++s) {
+              own[s] = v[s];
+              v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
             for (uint32_t r = 0; r < C; ++r) {
               const uint32_t src = r < rank ? r : r - 1;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float4 p = own[nt];
-                if (r != rank) {
-                  const uint4 u = lds128(recv + (slot * (C - 1) + src) * kRedBytes + nt * 512 + lane * 16);
-                  p = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                  __uint_as_float(u.w));
-                }
-                v[nt].x += p.x;
-                v[nt].y += p.y;
-                v[nt].z += p.z;
-                v[nt].w += p.w;
-              }
+              for (int s = 0; s < kSets; ++s)
+                v[s] = add4(v[s], r == rank ? own[s]
+                                            : lds_f4(recv + (slot * (C - 1) + src) * kRedBytes + s * 512 + lane * 16));
             }
             __syncwarp();
             if (lane < static_cast<int>(C) && lane != static_cast<int>(rank))
@@ -370,19 +374,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       }
       if (owner != rank) continue;
       if (!ok) {  // a wait ran out: the tile's outputs say so
+        const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float nan = __uint_as_float(0x7fc00000u);
-          v[nt] = make_float4(nan, nan, nan, nan);
-        }
+        for (int s = 0; s < kSets; ++s) v[s] = make_float4(nan, nan, nan, nan);
       }
       const int tile = tile0 + i;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float lo[2] = {v[nt].x, v[nt].y}, hi[2] = {v[nt].z, v[nt].w};
+      for (int s = 0; s < kSets; ++s) {
+        const float lo[2] = {v[s].x, v[s].y}, hi[2] = {v[s].z, v[s].w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int t = nt * kFewCols + c * 2 + h;
+          const int t = s * kFewCols + c * 2 + h;
           if (t >= a.T) continue;
           if (a.out_kind == kI4OutSwiglu) {  // row g: gate, row g + 8: up
             const int n = tile * 8 + g;
@@ -404,6 +406,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       }
     }
   }
+    __syncwarp();
+  }
   if (C > 1) {  // no CTA leaves while another may still write its shared memory
     __syncwarp();
     cluster_sync_all();
@@ -411,12 +415,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
 }
 
 using LinearKernel = void (*)(Int4LinearArgs);
-LinearKernel linear_kernel(int nt, int group) {
-  if (nt == 1)
-    return group == 32 ? int4_linear_kernel<1, 32> : group == 64 ? int4_linear_kernel<1, 64>
-                                                                 : int4_linear_kernel<1, 128>;
-  return group == 32 ? int4_linear_kernel<2, 32> : group == 64 ? int4_linear_kernel<2, 64>
-                                                               : int4_linear_kernel<2, 128>;
+template <int MODE>
+LinearKernel linear_kernel_of(int group) {
+  return group == 32 ? int4_linear_kernel<MODE, 32> : group == 64 ? int4_linear_kernel<MODE, 64>
+                                                                  : int4_linear_kernel<MODE, 128>;
+}
+LinearKernel linear_kernel(int mode, int group) {
+  return mode == 1   ? linear_kernel_of<1>(group)
+         : mode == 2 ? linear_kernel_of<2>(group)
+         : mode == 3 ? linear_kernel_of<3>(group)
+                     : linear_kernel_of<4>(group);
 }
 
 // Co-resident clusters of C CTAs on this device, by log2 C (filled by prepare_int4_kernels; one
@@ -452,9 +460,9 @@ cudaError_t launch_int4_quantize(const Int4QuantArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_t s) {
-  const int nt = a.T > kFewCols ? 2 : 1;
+  const int mode = a.T > kFewCols ? 4 : i4_mode(a.T);
   const int units = a.K / kI4Unit, unit_bytes = i4_unit_bytes(group);
-  const int max_units = kFewWarps * (nt == 1 ? 4 : 2);  // K range of a CTA
+  const int max_units = kFewWarps * lin_units(mode);  // K range of a CTA
   // The cluster size that finishes soonest: the largest share of bytes of one CTA at its share of
   // the HBM rate, and about 1 us for the exchange between the CTAs of a cluster.
   int best = 0, best_clus = 0;
@@ -476,23 +484,26 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   }
   if (!best) return cudaErrorInvalidConfiguration;
   a.cluster = best;
-  const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * nt +
-                      static_cast<size_t>(kLinRecv) * (best - 1) * 512 * nt;
+  const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * lin_sets(mode) +
+                      static_cast<size_t>(kLinRecv) * (best - 1) * 512 * lin_sets(mode) +
+                      static_cast<size_t>(kFewWarps) * kI4SplitBytes;
   const int per = (units + best - 1) / best;
-  a.log_cw = make_ksplit(per, kFewSlotBytes, unit_bytes).log_cw;
-  a.slot_bytes = kFewSlotBytes;
+  // a whole tile to a slot where it fits
+  const KSplit ks = make_ksplit(per, kI4SlotBytes, unit_bytes);
+  a.cw = ks.cw;
+  a.slot_bytes = chunk_bytes(ks, unit_bytes);
   a.stages = static_cast<int>((kLinDynamicSmem - rest) / a.slot_bytes);
   if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg =
       linear_config(best * best_clus, a.stages * static_cast<size_t>(a.slot_bytes) + rest, s, best, attr);
-  return cudaLaunchKernelEx(&cfg, linear_kernel(nt, group), a);
+  return cudaLaunchKernelEx(&cfg, linear_kernel(mode, group), a);
 }
 
 cudaError_t prepare_int4_kernels() {
-  for (int nt = 1; nt <= 2; ++nt)
+  for (int mode : {1, 2, 3, 4})
     for (int group : {32, 64, 128}) {
-      const cudaError_t e = cudaFuncSetAttribute(linear_kernel(nt, group),
+      const cudaError_t e = cudaFuncSetAttribute(linear_kernel(mode, group),
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(kLinDynamicSmem));
       if (e != cudaSuccess) return e;

@@ -51,50 +51,56 @@ def unpack(packed: torch.Tensor, rows: int, cols: int, group: int):
     scales = p[..., 1024:].contiguous().view(torch.bfloat16).view(groups, tiles, sbs, per, 16)
     q = torch.empty(groups, tiles, 16, sbs, 128, dtype=torch.float64)
     s = torch.empty(groups, tiles, 16, sbs, per, dtype=torch.float64)
-    bits = {(0, 0): 0, (0, 1): 16, (0, 2): 8, (0, 3): 24, (1, 0): 4, (1, 1): 20, (1, 2): 12, (1, 3): 28}
     for g in range(8):
         for c in range(4):
             for blk in range(2):
                 for v in range(4):
                     w = words[:, :, :, blk, 4 * g + c, v]
-                    for half in range(2):
-                        for i in range(4):
-                            k = 64 * blk + 32 * (v // 2) + 8 * c + 4 * (v % 2) + i
-                            q[:, :, g + 8 * half, :, k] = ((w >> bits[half, i]) & 15).double() - 8
+                    for i in range(4):
+                        k = 64 * blk + 32 * (v // 2) + 8 * c + 4 * (v % 2) + i
+                        for half, at in ((0, 8 * i + 4), (8, 8 * i)):
+                            n = (w >> at) & 15
+                            q[:, :, g + half, :, k] = torch.where(n >= 8, n - 16, n).double()
         s[:, :, g] = scales[..., 2 * g].double()
         s[:, :, g + 8] = scales[..., 2 * g + 1].double()
     return q.reshape(groups, tiles * 16, cols), s.reshape(groups, tiles * 16, sbs * per)
 
 
-def matmul_ref(x: torch.Tensor, w: torch.Tensor, dx=None):
-    """x [n, K] FP64, w [R, K] FP64 -> (x w^T, bound); dx: bound of x's own error."""
+def matmul_ref(x: torch.Tensor, w: torch.Tensor, dx=None, pieces=False):
+    """x [n, K] FP64, w [R, K] FP64 -> (x w^T, bound); dx: bound of x's own error; pieces: x enters
+    as 23-bit integers (4-bit weights), where elements below 2^-14 of the largest are off by up to
+    2^-22 of it."""
     y = x @ w.T
     bound = DEPTH * U32 * (x.abs() @ w.abs().T)
+    if pieces:
+        top = x.abs().amax(1, keepdim=True)
+        small = (x.abs() < 2.0 ** -14 * top * (1 + U16)) * top * 2.0 ** -22
+        bound = bound + small @ w.abs().T
     if dx is not None:
         bound = bound + dx @ w.abs().T
     return y, bound
 
 
 def linear_ref(x: torch.Tensor, w: torch.Tensor, group: int, fp32: bool):
-    y, b = matmul_ref(x.double(), values(w, group))
+    y, b = matmul_ref(x.double(), values(w, group), pieces=True)
     return y, b + (0 if fp32 else U16 * y.abs()) + 1e-37
 
 
-def mlp_ref(x: torch.Tensor, gate, up, down):
+def mlp_ref(x: torch.Tensor, gate, up, down, pieces=False):
     """SwiGLU MLP of x [n, d] FP64 with FP64 weights -> (y, bound); the activation is rounded to
     BF16 by definition, which the bound counts (the value leaves it out)."""
-    g, dg = matmul_ref(x, gate)
-    u, du = matmul_ref(x, up)
+    g, dg = matmul_ref(x, gate, pieces=pieces)
+    u, du = matmul_ref(x, up, pieces=pieces)
     sig = torch.sigmoid(g)
     a = g * sig * u
     # |silu'| <= 1.1; expf, the division and the two products: at most 8 half steps
     da = 1.1 * u.abs() * dg + (g * sig).abs() * du + 1.1 * dg * du + 8 * U32 * a.abs()
     da = da + U16 * (a.abs() + da)
-    return matmul_ref(a, down, da)
+    return matmul_ref(a, down, da, pieces)
 
 
 def dense_ref(x, gate, up, down, group):
-    y, b = mlp_ref(x.double(), values(gate, group), values(up, group), values(down, group))
+    y, b = mlp_ref(x.double(), values(gate, group), values(up, group), values(down, group), True)
     return y, b + U16 * y.abs() + 1e-37
 
 
@@ -132,7 +138,7 @@ def layer_ref(h, idx, w, gate, up, down, group):
     idx, w = idx.to(h.device), w.to(h.device)
     for e in idx.unique().tolist():
         t, j = (idx == e).nonzero(as_tuple=True)
-        y, b = mlp_ref(x[t], values(gate[e], group), values(up[e], group), values(down[e], group))
+        y, b = mlp_ref(x[t], values(gate[e], group), values(up[e], group), values(down[e], group), group > 0)
         wt = w[t, j][:, None]
         out.index_add_(0, t, wt * y)
         bound.index_add_(0, t, wt * b)

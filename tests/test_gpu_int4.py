@@ -115,6 +115,30 @@ def test_linear_keeps_tokens_apart(T):
     R.assert_within(out[rest], ref, bound)
 
 
+@pytest.mark.parametrize("spread", [4, 12, 24, 60])
+def test_linear_with_a_wide_range_of_magnitudes(spread):
+    """Elements spread over 2^-spread .. 1 of the largest, and tokens of very different size."""
+    T, N, K = 6, 300, 2560
+    x = normal(1, T, K)
+    e = torch.randint(-spread, 1, (T, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    x = (x.double() * 2.0 ** e).to(torch.bfloat16)
+    x = (x.double() * (2.0 ** torch.tensor([0, 90, -60, 7, -100, 30], device="cuda").double())[:, None])
+    x = x.to(torch.bfloat16)
+    x, w, _, out = run_linear(T, N, K, 64, True, x=x)
+    ref, bound = R.linear_ref(x, w[0], 64, True)
+    R.assert_within(out, ref, bound)
+
+
+def test_linear_zero_tokens_and_extremes():
+    x = torch.zeros(3, 256, device="cuda", dtype=torch.bfloat16)
+    x[1, 3] = 2.0 ** -130   # subnormal
+    x[2, 200] = 1e38
+    x, w, _, out = run_linear(3, 64, 256, 32, True, x=x)
+    assert (out[0] == 0).all()
+    ref, bound = R.linear_ref(x, w[0], 32, True)
+    R.assert_within(out, ref, bound + 2.0 ** -126)
+
+
 def test_linear_same_bits_every_time():
     for T, N, K in ((1, 2571, 5120), (16, 5120, 20480)):
         x, w, packed, out = run_linear(T, N, K, 128, True)
