@@ -1220,8 +1220,7 @@ beam_status check_dense_int4(const beam_dense_shape* s, int32_t group_size) {
 }
 
 struct FewLayout {
-  size_t ctl, sc, act, y, total;
-  int ctl_words;
+  size_t status, sc, act, y, total;
 };
 
 beam_status check_few_shape(const beam_moe_shape* s) {
@@ -1232,7 +1231,7 @@ beam_status check_few_shape(const beam_moe_shape* s) {
   return BEAM_OK;
 }
 
-// Status words first, as in every workspace, then the counters (cleared together).
+// Status words first, as in every workspace.
 FewLayout plan_few(const beam_moe_shape& s) {
   FewLayout L{};
   size_t o = 0;
@@ -1242,8 +1241,7 @@ FewLayout plan_few(const beam_moe_shape& s) {
     return r;
   };
   const size_t R = static_cast<size_t>(s.T) * s.top_k;
-  L.ctl_words = 4 + kFewMaxSlots + s.d / 16;
-  L.ctl = take(sizeof(uint32_t) * L.ctl_words);
+  L.status = take(256);
   L.sc = take(sizeof(float2) * s.T * s.E);
   L.act = take(sizeof(__nv_bfloat16) * R * s.I);
   L.y = take(sizeof(float) * R * s.d);
@@ -1273,8 +1271,9 @@ beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void
   ra.W = router_w;
   ra.bias = bias;
   ra.sc = at<float2>(ws, L.sc);
-  ra.ctl = at<uint32_t>(ws, L.ctl);
-  ra.ctl_words = L.ctl_words;
+  ra.status = at<uint32_t>(ws, L.status);
+  ra.unwritten = at<uint4>(ws, L.act);  // act and y, and what lies between them
+  ra.unwritten_n = static_cast<int64_t>((L.total - L.act) / sizeof(uint4));
   ra.T = shape->T;
   ra.d = shape->d;
   ra.E = shape->E;
@@ -1290,9 +1289,7 @@ beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void
   la.out = static_cast<__nv_bfloat16*>(out);
   la.idx = topk_idx;
   la.wts = topk_w;
-  la.status = ra.ctl;
-  la.ready = ra.ctl + 4;
-  la.done = ra.ctl + 4 + kFewMaxSlots;
+  la.status = ra.status;
   la.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   la.T = shape->T;
   la.d = shape->d;

@@ -31,8 +31,8 @@ constexpr int kFewCols = 8;           // tokens of one entry (an expert's produc
 constexpr int kFewMaxK = 8192;        // K of one tile: 8 warps x 1024 elements (128 B registers)
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;  // (token, expert) slots = most entries
 constexpr int kFewWarps = 8;          // consumer warps
-// Consumers, then a warp group of producer, finishing warp and two that only keep it whole: register
-// budgets are given per warp group.  Launched with 168 registers a thread; while the roles run,
+// Consumers, then a warp group of producer, two finishing warps and one that only keeps it whole:
+// register budgets are given per warp group.  Launched with 168 registers a thread; while the roles run,
 // consumers hold 224 and the others 56 (256 * 224 + 128 * 56 = 384 * 168).
 constexpr int kFewThreads = (kFewWarps + 4) * 32;
 constexpr int kFewRegsLaunch = 168, kFewRegsConsumer = 224, kFewRegsOther = 56;
@@ -43,7 +43,7 @@ constexpr int kI4SlotBytes = 46080;   // ring slot, 4-bit weights: a tile of K =
 // SM starts a copy about every 39 ns whatever its size: segments of 640, 1280 and 2560 bytes
 // stream at 2.4, 4.8 and 7.4 TB/s over the GPU.
 constexpr int kBf16SlotBytes = 41984;
-constexpr int kFewRed = 3;            // partial-tile buffers, at most
+constexpr int kFewRed = 4;            // partial-tile buffers, at most
 constexpr int kBf16Red = 2;           // with BF16 weights, whose tiles take four times as long
 constexpr int kFewMaxStages = 16;
 constexpr int kFewSmemMax = 232448;   // 227 KB
@@ -117,6 +117,7 @@ struct Int4LinearArgs {
   int T, N, K, tiles;
   int out_kind;            // Int4Out
   int cluster;             // CTAs that split K
+  int recv;                // receive buffers of partial tiles (cluster > 1)
   int cw;                  // KSplit::cw of the largest K range
   int stages, slot_bytes;
 };
@@ -126,8 +127,9 @@ struct FewRouterArgs {
   const float* W;          // [E, d]
   const float* bias;       // [E]
   float2* sc;              // [T, E] out: score, biased score
-  uint32_t* ctl;           // control words cleared for the layer kernel
-  int ctl_words;
+  uint32_t* status;        // cleared (4 words)
+  uint4* unwritten;        // what the layer kernel exchanges, set to all ones
+  int64_t unwritten_n;     // in 16-byte units
   int T, d, E;
 };
 
@@ -137,13 +139,11 @@ struct FewLayerArgs {
   const void* w_gate;      // BF16 [E, I, d], or packed gate|up
   const void* w_up;        // BF16 [E, I, d], or null
   const void* w_down;      // BF16 [E, d, I], or packed
-  __nv_bfloat16* act;      // [T * k, I]
-  float* y;                // [T * k, d]
+  __nv_bfloat16* act;      // [T * k, I], all ones on entry
+  float* y;                // [T * k, d], all ones on entry
   __nv_bfloat16* out;      // [T, d]
   int32_t* idx;            // [T, k] out, or null
   float* wts;              // [T, k] out, or null
-  uint32_t* ready;         // [kFewMaxSlots] finished gate/up tiles per entry; zero on entry
-  uint32_t* done;          // [d / 16] finished down tiles per output tile; zero on entry
   uint32_t* status;
   uint64_t wait_limit_ns;
   KSplit k1, k2;           // gate/up and down K slices
@@ -279,22 +279,93 @@ __device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t 
 // lane column c owns elements 8 c .. 8 c + 7 (one 16-byte load of BF16); a BF16 run is two MMAs,
 // the first with the first four of each column, an INT8 run is one.
 
+// ---- reading token rows
+
+__device__ __forceinline__ uint4 ld_relaxed(const void* p) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Rows that were complete before the kernel.
+struct TokenRow {
+  static constexpr bool kPolled = false;
+  __device__ __forceinline__ uint4 load(const __nv_bfloat16* p) const {
+    return __ldcg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void settle(uint4&, const __nv_bfloat16*) const {}
+};
+
+// Rows that other CTAs of the kernel are writing.  Every element was set to kUnwritten16 (a NaN that
+// no computation produces) before the kernel, so an element tells by itself whether it is there:
+// no flag has to follow the data through a fence and an atomic, which take 2 us together.
+constexpr uint32_t kUnwritten16 = 0xffffu;
+constexpr uint32_t kUnwritten32 = 0xffffffffu;
+__device__ __forceinline__ bool has_unwritten16(uint4 v) {
+  const uint32_t w[4] = {~v.x, ~v.y, ~v.z, ~v.w};
+  uint32_t z = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z |= (w[i] - 0x00010001u) & ~w[i];  // a zero half sets its top bit
+  return (z & 0x80008000u) != 0u;
+}
+
+struct PolledRow {
+  static constexpr bool kPolled = true;
+  volatile int* abort_flag;
+  uint64_t limit_ns;
+  uint32_t* status;
+  uint32_t where;
+  bool ok = true;
+  // Whether to look again; gives up after limit_ns, or when another wait did.
+  __device__ bool again(uint64_t& t0) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    uint32_t other;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(other) : "l"(status) : "memory");
+    if (*abort_flag || other || now - t0 >= limit_ns) {
+      if (!*abort_flag) {
+        *abort_flag = 1;
+        if (!other) record_status(status, kDevTimeout, where);
+      }
+      ok = false;
+    }
+    return ok;
+  }
+  __device__ __forceinline__ uint4 load(const __nv_bfloat16* p) const { return ld_relaxed(p); }
+  __device__ __forceinline__ void settle(uint4& v, const __nv_bfloat16* p) {
+    uint64_t t0 = 0;
+    while (has_unwritten16(v) && ok && again(t0)) v = ld_relaxed(p);
+  }
+};
+
 // B fragments of one token row's K slice: `row` points at the slice (null: an unused column,
 // zeros), 4 registers per 32 elements.
-template <int RUNS, bool COHERENT>
-__device__ __forceinline__ void load_tokens(uint32_t (&b)[RUNS * 4], const __nv_bfloat16* row,
+template <int RUNS, int REGS, class Src>
+__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], Src& src, const __nv_bfloat16* row,
                                             int runs, int c) {
+  static_assert(RUNS * 4 <= REGS, "the fragments must fit");
 #pragma unroll
   for (int j = 0; j < RUNS; ++j) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row != nullptr && j < runs) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + j * 32 + c * 8);
-      v = COHERENT ? __ldcg(p) : __ldg(p);
-    }
+    if (row != nullptr && j < runs) v = src.load(row + j * 32 + c * 8);
     b[j * 4 + 0] = v.x;
     b[j * 4 + 1] = v.y;
     b[j * 4 + 2] = v.z;
     b[j * 4 + 3] = v.w;
+  }
+  if constexpr (Src::kPolled) {
+#pragma unroll
+    for (int j = 0; j < RUNS; ++j) {
+      uint4 v = make_uint4(b[j * 4], b[j * 4 + 1], b[j * 4 + 2], b[j * 4 + 3]);
+      if (row != nullptr && j < runs) src.settle(v, row + j * 32 + c * 8);
+      b[j * 4 + 0] = v.x;
+      b[j * 4 + 1] = v.y;
+      b[j * 4 + 2] = v.z;
+      b[j * 4 + 3] = v.w;
+    }
   }
 }
 
@@ -345,99 +416,196 @@ constexpr int kI4SliceMax = kFewMaxK / kFewWarps;
 constexpr int kI4SplitBytes = 3 * kI4SliceMax;  // a warp's buffer for the digits of one token
 constexpr int kI4NonFinite = 1 << 20;           // in the place of an exponent
 
+// Runs of 32 of a warp's K slice at most: 64, 80 or 120 registers of fragments.
+__host__ __device__ constexpr int i4_mode_runs(int mode) { return mode == 1 ? 32 : 20; }
+
 __host__ __device__ constexpr int i4_mode(int tokens) { return tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3; }
 
+// E of a K slice from its largest magnitude's FP32 bits, and 2^(21 - E) as two normal factors.
+struct I4Scale {
+  int E;
+  float f1, f2;
+};
+__device__ __forceinline__ I4Scale i4_scale(uint32_t top) {
+  I4Scale s;
+  s.E = max(static_cast<int>(top >> 23), 1) - 127;
+  const int e1 = (21 - s.E) / 2, e2 = 21 - s.E - e1;
+  s.f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+  s.f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+  return s;
+}
+__device__ __forceinline__ uint32_t i4_top(uint4 v) {  // NaN and infinity sort above the rest
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) top = max(top, max((w[j] << 16) & 0x7fff0000u, w[j] & 0x7fff0000u));
+  return top;
+}
+// Digits of 8 elements: d[p] holds digit p of elements 0..3 and 4..7, a byte each.
+__device__ __forceinline__ void i4_digits(uint2 (&d)[3], uint4 v, const I4Scale& s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[3][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = (j & 1) ? bf16_hi(w[h * 2 + (j >> 1)]) : bf16_lo(w[h * 2 + (j >> 1)]);
+      // rounded to an integer by the addition of 1.5 2^23
+      const uint32_t i = __float_as_uint(fmaf(f * s.f1, s.f2, kI4SumStartF)) - kI4SumStart;
+      x[2][j] = i;
+      x[1][j] = static_cast<uint32_t>(static_cast<int>(i + 128) >> 8);
+      x[0][j] = static_cast<uint32_t>(static_cast<int>(x[1][j] + 128) >> 8);
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      o[p][h] = __byte_perm(__byte_perm(x[p][0], x[p][1], 0x0040), __byte_perm(x[p][2], x[p][3], 0x0040),
+                            0x5410);
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p) d[p] = make_uint2(o[p][0], o[p][1]);
+}
+
 // Splits the K slice of one token (`row`: its first element; n elements, a multiple of 128) over
-// the warp into its digits in `buf`; returns E - 25, the exponent of the result of digit d2 with
-// the codes' factor of 16, or kI4NonFinite.
-__device__ __forceinline__ int i4_split_token(const __nv_bfloat16* row, int n, uint8_t* buf,
+// the warp into its digits in `buf`; returns E, or kI4NonFinite.  `src` reads 16 bytes (TokenRow,
+// PolledRow).
+template <class Src>
+__device__ __forceinline__ int i4_split_token(Src& src, const __nv_bfloat16* row, int n, uint8_t* buf,
                                               int lane) {
   constexpr int kLoads = kI4SliceMax / 256;  // 8 elements per lane and load
   uint4 v[kLoads];
-  uint32_t top = 0;  // largest magnitude bits; NaN and infinity sort above
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     v[i] = make_uint4(0u, 0u, 0u, 0u);
     const int k = (i * 32 + lane) * 8;
-    if (k < n) v[i] = __ldcg(reinterpret_cast<const uint4*>(row + k));
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    if (k < n) v[i] = src.load(row + k);
+  }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      top = max(top, max((w[j] << 16) & 0x7fff0000u, w[j] & 0x7fff0000u));
+  for (int i = 0; i < kLoads; ++i) {
+    const int k = (i * 32 + lane) * 8;
+    if (k < n) src.settle(v[i], row + k);
+    top = max(top, i4_top(v[i]));
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if (top >= 0x7f800000u) return kI4NonFinite;
-  const int E = max(static_cast<int>(top >> 23), 1) - 127;
-  // 2^(21 - E) in two factors, each a normal number
-  const int e1 = (21 - E) / 2, e2 = 21 - E - e1;
-  const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
-  const float f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+  const I4Scale s = i4_scale(top);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int k = (i * 32 + lane) * 8;
     if (k >= n) break;
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t d[3][2] = {};
+    uint2 d[3];
+    i4_digits(d, v[i], s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = (j & 1) ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-      const int x2 = __float2int_rn(x * f1 * f2);
-      const int x1 = (x2 + 128) >> 8, x0 = (x1 + 128) >> 8;
-      const int at = 8 * (j & 3);
-      d[0][j >> 2] |= static_cast<uint32_t>(x0 & 255) << at;
-      d[1][j >> 2] |= static_cast<uint32_t>(x1 & 255) << at;
-      d[2][j >> 2] |= static_cast<uint32_t>(x2 & 255) << at;
-    }
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint2*>(buf + p * kI4SliceMax + k) = make_uint2(d[p][0], d[p][1]);
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(buf + p * kI4SliceMax + k) = d[p];
   }
-  return E - 25;
+  return s.E;
 }
 
-// v 2^r for |r| <= 252, in two steps: 2^r itself may be out of range.
-__device__ __forceinline__ float scale_exp(float v, int r) {
-  if (r >= kI4NonFinite / 2) return __uint_as_float(0x7fc00000u);
-  return v * __uint_as_float(static_cast<uint32_t>(127 + r / 2) << 23) *
-         __uint_as_float(static_cast<uint32_t>(127 + r - r / 2) << 23);
+// What a token's products have to be multiplied with, 2^(E - 9) for sums in units of digit 0 (codes
+// count 16 times), in two factors (2^(E - 9) may be out of range); NaN for a non-finite token.
+struct I4Factor {
+  float a, b;
+};
+__device__ __forceinline__ I4Factor i4_factor(int E) {
+  if (E >= kI4NonFinite / 2) return {__uint_as_float(0x7fc00000u), 1.f};
+  const int r = E - 9;
+  return {__uint_as_float(static_cast<uint32_t>(127 + r / 2) << 23),
+          __uint_as_float(static_cast<uint32_t>(127 + r - r / 2) << 23)};
 }
 
 // B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
-// row(t): the slice's first element of token t.  shift[h]: what i4_split_token returned for the
-// token of the lane's result column h.
-template <int MODE, int REGS, class Row>
-__device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], int (&shift)[2], Row row, int tokens,
-                                               int units, uint8_t* buf, int lane) {
-  constexpr int kRuns = REGS / (2 * MODE);
+// row(t): the slice's first element of token t.  factor[h]: of the token of the lane's result column h.
+//
+// MODE 1 splits a token at a time with the whole warp, through shared memory: a lane's share of the
+// conversion is 1/32 of the slice.  With more tokens each lane converts the elements of its own
+// column's token (8 lane columns, 8 tokens; 4 of them twice in MODE 2), all loads in flight at once,
+// and keeps the digits it needs.
+template <int MODE, int REGS, class Src, class Row>
+__device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&factor)[2], Src& src,
+                                               Row row, int tokens, int units,
+                                               [[maybe_unused]] uint8_t* buf, int lane) {
+  constexpr int kRuns = i4_mode_runs(MODE);
+  static_assert(kRuns * 2 * MODE <= REGS, "the fragments must fit");
   const int g = lane >> 2, c = lane & 3;
+  int E[2] = {0, 0};
+  if constexpr (MODE == 1) {
 #pragma unroll
-  for (int j = 0; j < REGS; ++j) b[j] = 0u;
-  shift[0] = shift[1] = 0;
+    for (int j = 0; j < REGS; ++j) b[j] = 0u;
 #pragma unroll 1
-  for (int t = 0; t < tokens; ++t) {
-    __syncwarp();
-    const int r = i4_split_token(row(t), units * kI4Unit, buf, lane);
-    __syncwarp();
-    const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of result column 0
-    if (t == first) shift[0] = r;
-    if (t == first + 1) shift[1] = r;
-#pragma unroll
-    for (int nt = 0; nt < MODE; ++nt) {
-      const int token = MODE == 1 ? (g & 1) : MODE == 2 ? (g & 3) : g;
-      const int digit = MODE == 1 ? (g >> 1) : MODE == 2 ? (nt ? 2 + (g >> 2) : (g >> 2)) : nt;
-      if (token == t && digit < 3) {
-        const uint8_t* p = buf + digit * kI4SliceMax + c * 8;
+    for (int t = 0; t < tokens; ++t) {
+      __syncwarp();
+      const int e = i4_split_token(src, row(t), units * kI4Unit, buf, lane);
+      E[0] = t == 0 ? e : E[0];
+      E[1] = t == 1 ? e : E[1];
+      __syncwarp();
+      if ((g & 1) == t && g < 6) {
+        const uint8_t* p = buf + (g >> 1) * kI4SliceMax + c * 8;
 #pragma unroll
         for (int j = 0; j < kRuns; ++j) {
           if (j < units * 4) {
             const uint2 w = *reinterpret_cast<const uint2*>(p + j * 32);
-            b[(j * MODE + nt) * 2] = w.x;
-            b[(j * MODE + nt) * 2 + 1] = w.y;
+            b[j * 2] = w.x;
+            b[j * 2 + 1] = w.y;
           }
         }
       }
     }
+  } else {
+    const int t = MODE == 2 ? (g & 3) : g;
+    const __nv_bfloat16* p = t < tokens ? row(t) + c * 8 : nullptr;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (p != nullptr && j < units * 4) v = src.load(p + j * 32);
+      b[j * 2 * MODE] = v.x;
+      b[j * 2 * MODE + 1] = v.y;
+      b[j * 2 * MODE + 2] = v.z;
+      b[j * 2 * MODE + 3] = v.w;
+    }
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {
+      uint4 v = make_uint4(b[j * 2 * MODE], b[j * 2 * MODE + 1], b[j * 2 * MODE + 2], b[j * 2 * MODE + 3]);
+      if constexpr (Src::kPolled) {
+        if (p != nullptr && j < units * 4) src.settle(v, p + j * 32);
+        b[j * 2 * MODE] = v.x;
+        b[j * 2 * MODE + 1] = v.y;
+        b[j * 2 * MODE + 2] = v.z;
+        b[j * 2 * MODE + 3] = v.w;
+      }
+      top = max(top, i4_top(v));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const I4Scale s = i4_scale(top);
+    const int r = top >= 0x7f800000u ? kI4NonFinite : s.E;
+    // result column h of lane column c: token 2 (c % 2) + h or 2 c + h, in lane 4 token
+    const int first = MODE == 2 ? 2 * (c & 1) : 2 * c;
+    E[0] = __shfl_sync(0xffffffffu, r, first * 4);
+    E[1] = __shfl_sync(0xffffffffu, r, first * 4 + 4);
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {
+      uint2 d[3];
+      i4_digits(d, make_uint4(b[j * 2 * MODE], b[j * 2 * MODE + 1], b[j * 2 * MODE + 2],
+                              b[j * 2 * MODE + 3]), s);
+      if constexpr (MODE == 2) {
+        const uint2 x = g < 4 ? d[0] : d[1], y = g < 4 ? d[2] : make_uint2(0u, 0u);
+        b[j * 4] = x.x;
+        b[j * 4 + 1] = x.y;
+        b[j * 4 + 2] = y.x;
+        b[j * 4 + 3] = y.y;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          b[j * 6 + q * 2] = d[q].x;
+          b[j * 6 + q * 2 + 1] = d[q].y;
+        }
+      }
+    }
   }
+  factor[0] = i4_factor(E[0]);
+  factor[1] = i4_factor(E[1]);
 }
 
 // Sums of i4_slice, per MMA of a run.  Digits are kept apart to the end, so that a token's result has
@@ -491,7 +659,7 @@ __device__ __forceinline__ void i4_slice_of(I4Acc<MODE>& acc, const uint32_t (&b
 template <int GROUP, int MODE, int REGS>
 __device__ __forceinline__ void i4_slice(I4Acc<MODE>& acc, const uint32_t (&b)[REGS], uint32_t base,
                                          int units, int lane) {
-  constexpr int kMax = REGS / (8 * MODE);
+  constexpr int kMax = i4_mode_runs(MODE) / 4;
   switch (units) {
     case 1: i4_slice_of<MODE, GROUP, 1>(acc, b, base, lane); break;
     case 2: i4_slice_of<MODE, GROUP, 2>(acc, b, base, lane); break;
@@ -508,23 +676,24 @@ __device__ __forceinline__ void i4_slice(I4Acc<MODE>& acc, const uint32_t (&b)[R
 // The warp's partial tile of a slice: rows g, g of tokens 2 c, 2 c + 1, then rows g + 8.  Digits in
 // different lanes are added here.
 template <int MODE>
-__device__ __forceinline__ float4 i4_result(const I4Acc<MODE>& acc, const int (&shift)[2], int lane) {
+__device__ __forceinline__ float4 i4_result(const I4Acc<MODE>& acc, const I4Factor (&factor)[2], int lane) {
+  constexpr float k1 = 1.f / 256, k2 = 1.f / 65536;  // digits 1 and 2 in units of digit 0
   const int c = lane & 3;
   float o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = shift[i & 1];
     if constexpr (MODE == 1) {  // lanes c hold digit c; lanes 3 zeros
-      o[i] = scale_exp(acc.v[0][i], r + 8 * (2 - (c < 3 ? c : 2)));
+      o[i] = acc.v[0][i] * (c == 0 ? 1.f : c == 1 ? k1 : k2);
       o[i] += __shfl_xor_sync(0xffffffffu, o[i], 1);
       o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
     } else if constexpr (MODE == 2) {  // lanes 0, 1 hold digits 0 and 2, lanes 2, 3 digit 1
-      o[i] = scale_exp(acc.v[0][i], r + 8 * (2 - (c >> 1)));
+      o[i] = acc.v[0][i] * (c < 2 ? 1.f : k1);
       o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
-      o[i] += scale_exp(acc.v[1][i], r);
+      o[i] = fmaf(acc.v[1][i], k2, o[i]);
     } else {
-      o[i] = scale_exp(acc.v[0][i], r + 16) + scale_exp(acc.v[1][i], r + 8) + scale_exp(acc.v[2][i], r);
+      o[i] = fmaf(acc.v[2][i], k2, fmaf(acc.v[1][i], k1, acc.v[0][i]));
     }
+    o[i] = o[i] * factor[i & 1].a * factor[i & 1].b;
   }
   return make_float4(o[0], o[1], o[2], o[3]);
 }

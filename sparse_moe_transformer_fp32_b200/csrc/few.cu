@@ -11,45 +11,66 @@ namespace {
 // ------------------------------------------------------------------ router scores
 
 // logits = h W_r^T, s = sigmoid(logit), sb = s + bias.  The sums run in FP64 and are rounded to
-// FP32 once, and so is the sigmoid: with a few tokens the FP64 units are far from busy (one FMA
-// per router weight and token: 21 M at T = 16, under 2 us) and the scores then equal the exactly
-// rounded ones, so that near ties fall as the definition has them.  Two experts per CTA: 128 CTAs
-// for 256 experts, each reading 2 d FP32 weights; latency-bound at 5.2 MB in all.
+// FP32 once, and so is the sigmoid, so that the scores are the exactly rounded ones and near ties
+// fall as the definition has them.  Operands are widened with integer operations: the conversion
+// instruction takes about 20 clocks of an SM a warp (at T = 16 the kernel took 39 us with it).  Two
+// experts per CTA: 128 CTAs for 256 experts, each reading 2 d FP32 weights; latency-bound at 5.2 MB
+// in all.
 //
-// Block 0 also clears the control words that the layer kernel counts in.
+// The kernel also clears the status words and marks as unwritten what the layer kernel exchanges.
 constexpr int kRtThreads = 256, kRtExperts = 2;
+
+// FP32 to FP64: exponent rebiased by 896; subnormals count as zero (they are below 2^-126).
+__device__ __forceinline__ double widen(float v) {
+  const uint32_t u = __float_as_uint(v), m = u & 0x7fffffffu;
+  uint32_t hi = (m >> 3) + 0x38000000u;
+  if (m < 0x00800000u) hi = 0u;
+  if (m >= 0x7f800000u) hi |= 0x7ff00000u;
+  return __hiloint2double(static_cast<int>(hi | (u & 0x80000000u)),
+                          m < 0x00800000u ? 0 : static_cast<int>(u << 29));
+}
 
 template <int TM>
 __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterArgs a) {
   __shared__ double part[kRtThreads / 32][kRtExperts * TM];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.ctl_words; i += kRtThreads) a.ctl[i] = 0u;
+  if (blockIdx.x == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0u;
+  for (int64_t i = blockIdx.x * kRtThreads + threadIdx.x; i < a.unwritten_n;
+       i += static_cast<int64_t>(gridDim.x) * kRtThreads)
+    a.unwritten[i] = make_uint4(kUnwritten32, kUnwritten32, kUnwritten32, kUnwritten32);
   const int e0 = blockIdx.x * kRtExperts;
   double acc[kRtExperts][TM];
 #pragma unroll
   for (int j = 0; j < kRtExperts; ++j)
 #pragma unroll
     for (int t = 0; t < TM; ++t) acc[j][t] = 0.0;
-#pragma unroll 2
+#pragma unroll(TM <= 2 ? 5 : 2)
   for (int k = threadIdx.x * 4; k < a.d; k += kRtThreads * 4) {
     float4 w[kRtExperts];
+    uint2 h[TM];
 #pragma unroll
     for (int j = 0; j < kRtExperts; ++j)
       w[j] = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e0 + j) * a.d + k));
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      if (t < a.T) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.h + static_cast<size_t>(t) * a.d + k));
-        const double h0 = bf16_lo(v.x), h1 = bf16_hi(v.x), h2 = bf16_lo(v.y), h3 = bf16_hi(v.y);
+    for (int t = 0; t < TM; ++t)
+      h[t] = t < a.T ? __ldg(reinterpret_cast<const uint2*>(a.h + static_cast<size_t>(t) * a.d + k))
+                     : make_uint2(0u, 0u);
+    double wd[kRtExperts][4];
 #pragma unroll
-        for (int j = 0; j < kRtExperts; ++j) {
-          acc[j][t] = fma(static_cast<double>(w[j].x), h0, acc[j][t]);
-          acc[j][t] = fma(static_cast<double>(w[j].y), h1, acc[j][t]);
-          acc[j][t] = fma(static_cast<double>(w[j].z), h2, acc[j][t]);
-          acc[j][t] = fma(static_cast<double>(w[j].w), h3, acc[j][t]);
-        }
-      }
+    for (int j = 0; j < kRtExperts; ++j) {
+      wd[j][0] = widen(w[j].x);
+      wd[j][1] = widen(w[j].y);
+      wd[j][2] = widen(w[j].z);
+      wd[j][3] = widen(w[j].w);
+    }
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const double hd[4] = {widen(bf16_lo(h[t].x)), widen(bf16_hi(h[t].x)), widen(bf16_lo(h[t].y)),
+                            widen(bf16_hi(h[t].y))};
+#pragma unroll
+      for (int j = 0; j < kRtExperts; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][t] = fma(wd[j][i], hd[i], acc[j][t]);
     }
   }
 #pragma unroll
@@ -77,10 +98,16 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
 
 // ------------------------------------------------------------------ the layer
 
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+// Stores of what other CTAs poll for.  A NaN is stored as the one that is not kUnwritten.
+__device__ __forceinline__ void st_relaxed16(__nv_bfloat16* p, __nv_bfloat16 v) {
+  unsigned short u = __bfloat16_as_ushort(v);
+  if (u == kUnwritten16) u = 0x7fff;
+  asm volatile("st.relaxed.gpu.global.u16 [%0], %1;" ::"l"(p), "h"(u) : "memory");
+}
+__device__ __forceinline__ void st_relaxed32(float* p, float v) {
+  uint32_t u = __float_as_uint(v);
+  if (u == kUnwritten32) u = 0x7fffffffu;
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(u) : "memory");
 }
 
 // Order-preserving map of a score to unsigned; NaN above everything, nothing maps to 0.
@@ -101,8 +128,7 @@ struct FewShared {
   uint8_t entry_e[kFewMaxSlots];        // expert of each entry
   uint8_t entry_n[kFewMaxSlots];        // its tokens, 1..8
   uint8_t entry_slot[kFewMaxSlots][kFewCols];  // their slots
-  uint16_t last[kMaxD / 16];            // output tiles that this CTA completes
-  int n_entries, n_last, abort_flag;
+  int n_entries, abort_flag;
 };
 
 // Selection of token `t` by one warp from its E (score, biased score) pairs in `sc`:
@@ -114,10 +140,11 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, FewShared& s
   if (lane < a.G) {
     float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
     bool nan = false;
+    int jj = lane % P;  // start at different banks
+#pragma unroll 4
     for (int j = 0; j < P; ++j) {
-      int jj = j + lane;  // start at different banks
-      jj -= jj >= P ? (jj / P) * P : 0;
       const float v = sc[lane * P + jj].y;
+      if (++jj == P) jj = 0;
       nan |= v != v;
       if (v > m1) {
         m2 = m1;
@@ -230,10 +257,10 @@ __device__ void few_entries(const FewLayerArgs& a, FewShared& sh, int lane) {
 //   gate|up          items (entry, 8 intermediate rows): a 16-row tile holds 8 gate rows and the
 //                    same 8 up rows, so one lane ends up with both and applies SwiGLU; BF16
 //                    activations, the down product's MMA operand, as the layer defines them
-//   down             items (entry, 16 output rows); an item needs its entry's activations
-//                    complete, which a counter per entry tells; FP32 partial outputs per slot
-//   combine          per output tile by the CTA that finishes its last item: each token's k
-//                    slots in ascending expert order, FP32, rounded to BF16 once
+//   down             items (entry, 16 output rows): the entry's activations, polled for; FP32
+//                    partial outputs per slot
+//   combine          every CTA an even share of the output columns: each token's k slots, polled
+//                    for, in ascending expert order, FP32, rounded to BF16 once
 // Each CTA takes one contiguous run of items of either phase, cut so that both runs together are
 // the same number of weight bytes for every CTA; its producer goes from the first into the second
 // without waiting for anything but ring space, so the weights keep streaming while activations
@@ -263,7 +290,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       mbar_init(smem_u32(&sh.red_empty[i]), 1);
     }
     sh.abort_flag = 0;
-    sh.n_last = 0;
     fence_mbarrier_init();
   }
   // the tokens' scores, in the ring's space until the weights need it
@@ -278,27 +304,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
 
   // ---- this CTA's items
   const int n_gu = a.I / 8, n_dn = a.d / 16;
-  const int64_t N1 = static_cast<int64_t>(sh.n_entries) * n_gu;
-  const int64_t N2 = static_cast<int64_t>(sh.n_entries) * n_dn;
-  const int64_t grid = gridDim.x;
-  auto first1 = [&](int64_t b) { return b * N1 / grid; };
+  // 32 bits suffice: at most 128 entries, and K in units of 128
+  const uint32_t N1 = sh.n_entries * n_gu, N2 = sh.n_entries * n_dn, K1 = a.d / 128, K2 = a.I / 128;
+  const uint32_t grid = gridDim.x;
+  auto first1 = [&](uint32_t b) { return b * N1 / grid; };
   // Down items start where the CTAs before b have b / grid of all bytes (an item's are 16 K;
   // gate|up: K = d, down: K = I).  That is monotone in b as long as a CTA's down bytes cover the
   // one gate|up item by which the first runs differ; below that, an even cut.
-  auto first2 = [&](int64_t b) {
-    if (N2 * a.I < grid * a.d) return b * N2 / grid;
-    const int64_t v = (b * (N1 * a.d + N2 * a.I) / grid - first1(b) * a.d) / a.I;
+  auto first2 = [&](uint32_t b) {
+    if (N2 * K2 < grid * K1) return b * N2 / grid;
+    const uint32_t v = (b * (N1 * K1 + N2 * K2) / grid - first1(b) * K1) / K2;
     return b == grid || v > N2 ? N2 : v;
   };
-  const int i1 = static_cast<int>(first1(blockIdx.x)), j1 = static_cast<int>(first1(blockIdx.x + 1));
-  const int i2 = static_cast<int>(first2(blockIdx.x)), j2 = static_cast<int>(first2(blockIdx.x + 1));
+  const int i1 = first1(blockIdx.x), j1 = first1(blockIdx.x + 1);
+  const int i2 = first2(blockIdx.x), j2 = first2(blockIdx.x + 1);
 
   if (warp < kFewWarps) {
     more_registers<kFewRegsConsumer>();
     // ---- consumers
-    // token fragments: BF16 4 registers a run of 32; INT8 digits 2, 4 or 6 (up to 20 runs)
-    uint32_t b[kI4 && MODES == 1 ? 64 : 128];
-    [[maybe_unused]] int shift[2];
+    // token fragments: BF16 4 registers a run of 32; INT8 digits 2, 4 or 6 (4 and 6: up to 20 runs)
+    uint32_t b[!kI4 ? 128 : MODES == 1 ? 64 : MODES == 2 ? 80 : 120];
+    [[maybe_unused]] I4Factor factor[2];
     [[maybe_unused]] uint8_t* const split =
         smem + a.stages * a.slot_bytes + kRed * kFewWarps * 512 + warp * kI4SplitBytes;
     int n_tok = 0;
@@ -322,48 +348,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       for (int it = first; it < last; ++it) {
         if (entry != loaded) {  // token fragments of the entry
           loaded = entry;
-          if (ph) {
-            // activations of the entry complete?
-            ok = true;
-            if (lane == 0) {
-              const uint32_t want = n_gu;
-              uint64_t t0 = 0;
-              while (ld_acquire(a.ready + entry) < want) {
-                const uint64_t now = globaltimer_ns();
-                if (!t0) t0 = now;
-                if (*abort_flag || ld_acquire(a.status)) {  // here or in another CTA
-                  *abort_flag = 1;
-                  ok = false;
-                  break;
-                }
-                if (now - t0 >= a.wait_limit_ns) {
-                  *abort_flag = 1;
-                  record_status(a.status, kDevTimeout, kWhereFew + 1);
-                  ok = false;
-                  break;
-                }
-                __nanosleep(40);
-              }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
           n_tok = sh.entry_n[entry];
           auto row = [&](int col) {
             const int s = sh.entry_slot[entry][col];
             return ph ? a.act + static_cast<size_t>(s) * K + k0
                       : a.h + static_cast<size_t>(s / a.k) * K + k0;
           };
-          if constexpr (kI4) {
-            if (MODES == 1 || n_tok <= 2)
-              i4_load_tokens<1>(b, shift, row, n_tok, units, split, lane);
-            else if (MODES == 2 || n_tok <= 4)
-              i4_load_tokens<(MODES > 1 ? 2 : 1)>(b, shift, row, n_tok, units, split, lane);
-            else
-              i4_load_tokens<MODES>(b, shift, row, n_tok, units, split, lane);
+          auto load = [&](auto& src) {
+            if constexpr (kI4) {
+              if (MODES == 1 || n_tok <= 2)
+                i4_load_tokens<1>(b, factor, src, row, n_tok, units, split, lane);
+              else if (MODES == 2 || n_tok <= 4)
+                i4_load_tokens<(MODES > 1 ? 2 : 1)>(b, factor, src, row, n_tok, units, split, lane);
+              else
+                i4_load_tokens<MODES>(b, factor, src, row, n_tok, units, split, lane);
+            } else {
+              const int col = lane >> 2;
+              load_tokens<kRuns>(b, src, col < n_tok ? row(col) : nullptr, units, lane & 3);
+            }
+          };
+          if (ph) {
+            PolledRow src{abort_flag, a.wait_limit_ns, a.status, kWhereFew + 1};
+            load(src);
+            ok = __all_sync(0xffffffffu, src.ok);
+            if (!ok) break;
           } else {
-            const int col = lane >> 2;
-            load_tokens<kRuns, true>(b, col < n_tok ? row(col) : nullptr, units, lane & 3);
+            TokenRow src;
+            load(src);
           }
         }
         float4 part = make_float4(0.f, 0.f, 0.f, 0.f);  // rows g, g of two tokens, then g + 8
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
               constexpr std::integral_constant<int, kI4 ? GROUP : 128> kG{};
               auto product = [&](auto acc) {
                 i4_slice<kG.value>(acc, b, base, units, lane);
-                part = i4_result(acc, shift, lane);
+                part = i4_result(acc, factor, lane);
               };
               if (MODES == 1 || n_tok <= 2)
                 product(I4Acc<1>{});
@@ -481,11 +492,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
         mbar_wait_bounded(smem_u32(&sh.full_bar[i % a.stages]), (i / a.stages) & 1, &never,
                           2000000000ull, nullptr, 0);
     }
-  } else if (warp == kFewWarps + 1) {
-    // ---- finishing warp
+  } else if (warp <= kFewWarps + 2) {
+    // ---- finishing warps, tiles in turn
     const int g = lane >> 2, c = lane & 3;
     int rb = 0;
-    uint32_t rpar = 0;
+    uint32_t rpar = 0, turn = warp - kFewWarps - 1;
     bool ok = true;
 #pragma unroll 1
     for (int ph = 0; ph < 2 && ok; ++ph) {
@@ -493,9 +504,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       const int per = ph ? n_dn : n_gu;
       const int first = ph ? i2 : i1, last = ph ? j2 : j1;
       const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
-      int entry = first / per, tile = first % per, run = 0;
+      int entry = first / per, tile = first % per;
 #pragma unroll 1
-      for (int it = first; it < last; ++it) {
+      for (int it = first; it < last; ++it, turn ^= 1) {
+        if (turn) {
+          if (++rb == kRed) {
+            rb = 0;
+            rpar ^= 1;
+          }
+          if (++tile == per) {
+            tile = 0;
+            ++entry;
+          }
+          continue;
+        }
         ok = mbar_wait_warp(smem_u32(&sh.red_full[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
                             kWhereFew + 4);
         if (!ok) break;
@@ -522,62 +544,55 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           if (col < n) {
             const size_t s = sh.entry_slot[entry][col];
             if (ph == 0) {
-              a.act[s * a.I + tile * 8 + g] = __float2bfloat16_rn(swiglu(lo[h], hi[h]));
+              st_relaxed16(a.act + s * a.I + tile * 8 + g, __float2bfloat16_rn(swiglu(lo[h], hi[h])));
             } else {
               float* y = a.y + s * a.d + tile * 16 + g;
-              __stcg(y, lo[h]);
-              __stcg(y + 8, hi[h]);
+              st_relaxed32(y, lo[h]);
+              st_relaxed32(y + 8, hi[h]);
             }
           }
         }
-        ++run;
-        if (++tile == per || it + 1 == last) {
-          if (ph == 0) {  // publish the activations of this run of the entry's tiles
-            __syncwarp();
-            if (lane == 0) {
-              __threadfence();
-              atomicAdd(a.ready + entry, static_cast<uint32_t>(run));
-            }
-          }
-          run = 0;
-          if (tile == per) {
-            tile = 0;
-            ++entry;
-          }
+        if (++tile == per) {
+          tile = 0;
+          ++entry;
         }
       }
     }
-  }
+    }
     __syncwarp();
     more_registers<kFewRegsLaunch>();
   }
 
-  // ---- combine: the output tiles whose last item this CTA finished
+  // ---- combine: every CTA an even share of the output columns, four to a thread; the partial
+  // outputs come from all CTAs
   __syncthreads();
   if (sh.abort_flag) return;
-  const uint32_t items = static_cast<uint32_t>(sh.n_entries);
-  for (int it = i2 + static_cast<int>(threadIdx.x); it < j2; it += kFewThreads) {
-    const int tile = it % n_dn;
-    __threadfence();
-    if (atomicAdd(a.done + tile, 1u) == items - 1u)
-      sh.last[atomicAdd(&sh.n_last, 1)] = static_cast<uint16_t>(tile);
-  }
-  __syncthreads();
-  const int work = sh.n_last * a.T * 16;
-  if (work == 0) return;
-  __threadfence();
-  for (int u = threadIdx.x; u < work; u += kFewThreads) {
-    const int cc = u & 15, t = (u >> 4) % a.T, tile = sh.last[(u >> 4) / a.T];
-    const float* y = a.y + static_cast<size_t>(t) * a.k * a.d + tile * 16 + cc;
-    float v[kMaxTopK];
+  const int q0 = blockIdx.x * (a.d / 4) / gridDim.x, nq = (blockIdx.x + 1) * (a.d / 4) / gridDim.x - q0;
+  PolledRow poll{abort_flag, a.wait_limit_ns, a.status, kWhereFew + 5};
+  for (int u = threadIdx.x; u < nq * a.T; u += kFewThreads) {
+    const int t = u / nq, col = (q0 + u % nq) * 4;
+    const float* y = a.y + static_cast<size_t>(t) * a.k * a.d + col;
+    uint4 v[kMaxTopK];
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j)
-      if (j < a.k) v[j] = __ldcg(y + static_cast<size_t>(j) * a.d);
-    float o = 0.f;
+      if (j < a.k) v[j] = ld_relaxed(y + static_cast<size_t>(j) * a.d);
+    float o[4] = {};
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j)
-      if (j < a.k) o = fmaf(sh.wts[t * a.k + j], v[j], o);
-    a.out[static_cast<size_t>(t) * a.d + tile * 16 + cc] = __float2bfloat16_rn(o);
+    for (int j = 0; j < kMaxTopK; ++j) {
+      if (j >= a.k) break;
+      uint64_t t0 = 0;
+      while ((v[j].x == kUnwritten32 || v[j].y == kUnwritten32 || v[j].z == kUnwritten32 ||
+              v[j].w == kUnwritten32) && poll.ok && poll.again(t0))
+        v[j] = ld_relaxed(y + static_cast<size_t>(j) * a.d);
+      const float w = sh.wts[t * a.k + j];
+      o[0] = fmaf(w, __uint_as_float(v[j].x), o[0]);
+      o[1] = fmaf(w, __uint_as_float(v[j].y), o[1]);
+      o[2] = fmaf(w, __uint_as_float(v[j].z), o[2]);
+      o[3] = fmaf(w, __uint_as_float(v[j].w), o[3]);
+    }
+    __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<size_t>(t) * a.d + col);
+    out[0] = __floats2bfloat162_rn(o[0], o[1]);
+    out[1] = __floats2bfloat162_rn(o[2], o[3]);
   }
 }
 
@@ -618,8 +633,8 @@ cudaError_t launch_few_router(const FewRouterArgs& a, cudaStream_t s) {
 
 cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
-  // the digits of 8 tokens fit in a warp's registers up to K = 5120, those of 4 up to 8192
-  a.entry_max = group && (a.d > 5120 || a.I > 5120) ? 4 : kFewCols;
+  // the digits of 3 to 8 tokens fit in a warp's registers up to K = 5120, those of 2 up to 8192
+  a.entry_max = group && (a.d > 5120 || a.I > 5120) ? 2 : kFewCols;
   a.slot_bytes = group ? kI4SlotBytes : kBf16SlotBytes;
   a.k1 = make_ksplit(a.d / unit, a.slot_bytes, unit_bytes);
   a.k2 = make_ksplit(a.I / unit, a.slot_bytes, unit_bytes);

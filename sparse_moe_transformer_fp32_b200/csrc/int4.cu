@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const Int4QuantArgs 
 
 // ------------------------------------------------------------------ linear product
 
-constexpr int kLinRecv = 2;        // receive buffers of a tile's other K ranges
+constexpr int kLinRecv = 8;             // receive buffers for a tile's partial results, at most
+constexpr int kLinRecvBytes = 16384;    // all of them
 constexpr int kLinMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -115,10 +116,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void remote_store(uint32_t a, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
+// 16 bytes into another CTA's shared memory, counted by the mbarrier `bar` there.
+__device__ __forceinline__ void remote_store(uint32_t a, float4 v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+      "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
+      "r"(__float_as_uint(v.w)), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -150,8 +154,9 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
 }
 
 // y = x W^T; MODE 1, 2, 3: up to 2, 4, 8 tokens on INT8 MMAs, 4: up to 16 on BF16 MMAs.  A tile is 16 rows of W; a cluster of C CTAs shares a tile, each
-// taking a K range, and the CTA whose turn it is (tile index mod C) receives the others' partial
-// tiles in its shared memory and adds them in rank order.  C > 1 is for matrices with few tiles
+// taking a K range, and the CTA whose turn it is (tile index mod C) receives the partial tiles of
+// all in its shared memory and adds them in rank order.  One warp sends and another receives, several
+// tiles apart: with one warp for both a tile took the exchange's 1.5 us.  C > 1 is for matrices with few tiles
 // (the spread over 148 SMs would be uneven) and for K ranges whose token fragments do not fit in
 // registers.  HBM-bound on N K (1/2 + 2 / group) bytes.
 //
@@ -159,8 +164,8 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
 // previous kernel of the stream drains; tokens are read, and outputs written, after
 // griddepcontrol.wait.  (Weights written by the previous kernel are safe: only kernels of this
 // kind let their successor start early, and they write no weights.)
-// Superblocks per warp at most: 64 (MODE 1) or up to 128 registers of token fragments.
-__host__ __device__ constexpr int lin_units(int mode) { return mode <= 2 ? 8 : mode == 3 ? 5 : 4; }
+// Superblocks per warp at most: 64 to 128 registers of token fragments.
+__host__ __device__ constexpr int lin_units(int mode) { return mode == 4 ? 4 : i4_mode_runs(mode) / 4; }
 __host__ __device__ constexpr int lin_sets(int mode) { return mode == 4 ? 2 : 1; }  // of 8 tokens
 
 template <int MODE, int GROUP>
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   const uint32_t red = ring + a.stages * a.slot_bytes;
   const uint32_t recv = red + kFewRed * kFewWarps * kRedBytes;
   [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kRedBytes +
-                         kLinRecv * (a.cluster - 1) * kRedBytes + (threadIdx.x >> 5) * kI4SplitBytes;
+                         (a.cluster > 1 ? a.recv * a.cluster * kRedBytes : 0) + (threadIdx.x >> 5) * kI4SplitBytes;
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       mbar_init(smem_u32(&red_empty[i]), 1);
     }
     for (int i = 0; i < kLinRecv; ++i) {
-      mbar_init(smem_u32(&recv_full[i]), C > 1 ? C - 1 : 1);
+      mbar_init(smem_u32(&recv_full[i]), 2);  // the receiver, and this CTA's own part
       for (int r = 0; r < kLinMaxCluster; ++r) mbar_init(smem_u32(&recv_free[r][i]), 1);
     }
     abort_sh = 0;
@@ -219,14 +224,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     const int units = ks.count(warp), mine = warp / ks.cw, chunks = ks.chunks();
     const uint32_t off = (ks.start(warp) - ks.start(mine * ks.cw)) * kUnitBytes;
     uint32_t b[kUnits * 8 * MODE];
-    [[maybe_unused]] int shift[2];
+    [[maybe_unused]] I4Factor factor[2];
     pdl_wait();
     const __nv_bfloat16* x0 = a.x + static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit;
     auto row = [&](int t) { return x0 + static_cast<size_t>(t) * a.K; };
+    [[maybe_unused]] TokenRow src;
     if constexpr (MODE == 4)
       i4_load_tokens16<kUnits * 4>(b, row, a.T, units, lane);
     else
-      i4_load_tokens<MODE>(b, shift, row, a.T, units, split, lane);
+      i4_load_tokens<MODE>(b, factor, src, row, a.T, units, split, lane);
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
     bool ok = true;
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
           } else {
             I4Acc<MODE> acc;
             i4_slice<GROUP>(acc, b, base, units, lane);
-            part[0] = i4_result(acc, shift, lane);
+            part[0] = i4_result(acc, factor, lane);
           }
         }
         __syncwarp();
@@ -307,72 +313,70 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         mbar_wait_bounded(smem_u32(&full_bar[i % a.stages]), (i / a.stages) & 1, &never,
                           2000000000ull, nullptr, 0);
     }
-  } else if (warp == kFewWarps + 1) {
-    // ---- finishing warp
+  } else if (warp == kFewWarps + 1 || (warp == kFewWarps + 2 && C > 1)) {
+    // ---- finishing warps: the first adds the consumers' partial tiles, and stores the result of a
+    // tile that is whole (C = 1) or sends it to the tile's owner; the second adds what an owner got
     const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
     const int g = lane >> 2, c = lane & 3;
+    const bool receiver = warp == kFewWarps + 2;
     int rb = 0;
     uint32_t rpar = 0;
     bool ok = true;
     pdl_wait();
-    for (int i = 0; i < tile1 - tile0; ++i) {
+    for (int i = receiver ? rank : 0; i < tile1 - tile0; i += receiver ? C : 1) {
       float4 v[kSets];  // rows g, g of tokens 2 c, 2 c + 1, then rows g + 8
-      if (ok) ok = mbar_wait_warp(smem_u32(&red_full[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0);
-      if (ok) {
 #pragma unroll
-        for (int s = 0; s < kSets; ++s) v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < kSets; ++s) v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      // of an owner's n-th tile: its buffer, and how often that was used before
+      const int n = i / C, slot = n % a.recv, use = n / a.recv;
+      const uint32_t owner = i % C, buffer = recv + slot * C * kRedBytes + lane * 16;
+      if (receiver) {
+        if (ok) {
+          if (lane == 0) mbar_arrive_expect_tx(smem_u32(&recv_full[slot]), (C - 1) * kRedBytes);
+          ok = wait_cluster(smem_u32(&recv_full[slot]), use & 1, abort_flag, a.wait_limit_ns);
+        }
+        if (ok) {
+          for (uint32_t r = 0; r < C; ++r)
+#pragma unroll
+            for (int s = 0; s < kSets; ++s) v[s] = add4(v[s], lds_f4(buffer + r * kRedBytes + s * 512));
+          __syncwarp();
+          if (lane < static_cast<int>(C)) remote_arrive(map_rank(smem_u32(&recv_free[rank][slot]), lane));
+        }
+      } else {
+        if (ok) ok = mbar_wait_warp(smem_u32(&red_full[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0);
+        if (ok) {
 #pragma unroll 4
-        for (int w = 0; w < active; ++w) {
+          for (int w = 0; w < active; ++w) {
 #pragma unroll
-          for (int s = 0; s < kSets; ++s)
-            v[s] = add4(v[s], lds_f4(red + (rb * kFewWarps + w) * kRedBytes + s * 512 + lane * 16));
+            for (int s = 0; s < kSets; ++s)
+              v[s] = add4(v[s], lds_f4(red + (rb * kFewWarps + w) * kRedBytes + s * 512 + lane * 16));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&red_empty[rb]));
+          if (++rb == kFewRed) {
+            rb = 0;
+            rpar ^= 1;
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&red_empty[rb]));
-        if (++rb == kFewRed) {
-          rb = 0;
-          rpar ^= 1;
-        }
-      }
-      const uint32_t owner = C > 1 ? i % C : 0;
-      if (C > 1 && ok) {
-        const int n = i / C, slot = n & 1;  // the owner's n-th tile
-        if (owner != rank) {
-          if (n >= kLinRecv)
-            ok = wait_cluster(smem_u32(&recv_free[owner][slot]), ((n >> 1) - 1) & 1, abort_flag,
+        if (C > 1) {
+          if (ok && use > 0)
+            ok = wait_cluster(smem_u32(&recv_free[owner][slot]), (use - 1) & 1, abort_flag,
                               a.wait_limit_ns);
-          if (ok) {
-            const uint32_t src = rank < owner ? rank : rank - 1;
-            const uint32_t dst =
-                map_rank(recv + (slot * (C - 1) + src) * kRedBytes + lane * 16, owner);
+          if (!ok) break;
+          const uint32_t full = smem_u32(&recv_full[slot]);
 #pragma unroll
-            for (int s = 0; s < kSets; ++s) remote_store(dst + s * 512, v[s]);
-            __syncwarp();
-            if (lane == 0) remote_arrive(map_rank(smem_u32(&recv_full[slot]), owner));
+          for (int s = 0; s < kSets; ++s) {
+            const uint32_t dst = buffer + rank * kRedBytes + s * 512;
+            if (owner == rank)
+              sts128(dst, v[s]);
+            else
+              remote_store(map_rank(dst, owner), v[s], map_rank(full, owner));
           }
-        } else {
-          ok = wait_cluster(smem_u32(&recv_full[slot]), (n >> 1) & 1, abort_flag, a.wait_limit_ns);
-          if (ok) {
-            float4 own[kSets];
-#pragma unroll
-            for (int s = 0; s < kSets; ++s) {
-              own[s] = v[s];
-              v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            for (uint32_t r = 0; r < C; ++r) {
-              const uint32_t src = r < rank ? r : r - 1;
-#pragma unroll
-              for (int s = 0; s < kSets; ++s)
-                v[s] = add4(v[s], r == rank ? own[s]
-                                            : lds_f4(recv + (slot * (C - 1) + src) * kRedBytes + s * 512 + lane * 16));
-            }
-            __syncwarp();
-            if (lane < static_cast<int>(C) && lane != static_cast<int>(rank))
-              remote_arrive(map_rank(smem_u32(&recv_free[rank][slot]), lane));
-          }
+          __syncwarp();
+          if (owner == rank && lane == 0) mbar_arrive(full);
+          continue;
         }
       }
-      if (owner != rank) continue;
       if (!ok) {  // a wait ran out: the tile's outputs say so
         const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
@@ -409,6 +413,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     __syncwarp();
   }
   if (C > 1) {  // no CTA leaves while another may still write its shared memory
+    if (*abort_flag) {  // stores that nobody waited for
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 20000) {
+      }
+    }
     __syncwarp();
     cluster_sync_all();
   }
@@ -484,8 +493,10 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   }
   if (!best) return cudaErrorInvalidConfiguration;
   a.cluster = best;
+  a.recv = kLinRecvBytes / (best * 512 * lin_sets(mode));
+  if (a.recv > kLinRecv) a.recv = kLinRecv;
   const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * lin_sets(mode) +
-                      static_cast<size_t>(kLinRecv) * (best - 1) * 512 * lin_sets(mode) +
+                      (best > 1 ? static_cast<size_t>(a.recv) * best * 512 * lin_sets(mode) : 0) +
                       static_cast<size_t>(kFewWarps) * kI4SplitBytes;
   const int per = (units + best - 1) / best;
   // a whole tile to a slot where it fits
