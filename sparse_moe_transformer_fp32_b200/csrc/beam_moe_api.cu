@@ -1274,13 +1274,20 @@ beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void
   ra.status = at<uint32_t>(ws, L.status);
   ra.unwritten = at<uint4>(ws, L.act);  // act and y, and what lies between them
   ra.unwritten_n = static_cast<int64_t>((L.total - L.act) / sizeof(uint4));
-  ra.T = shape->T;
+  ra.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   ra.d = shape->d;
   ra.E = shape->E;
-  BEAM_LAUNCH(kKFewRouter, st, launch_few_router(ra, st));
+  // one launch up to d = 5120 (and up to 10 tokens at any d)
+  const int per = few_router_tokens(shape->d);
+  for (int t = 0; t < shape->T; t += per) {
+    ra.T = shape->T - t < per ? shape->T - t : per;
+    BEAM_LAUNCH(kKFewRouter, st, launch_few_router(ra, st));
+    ra.h += static_cast<size_t>(per) * shape->d;
+    ra.sc += static_cast<size_t>(per) * shape->E;
+  }
   FewLayerArgs la{};
-  la.h = ra.h;
-  la.sc = ra.sc;
+  la.h = static_cast<const __nv_bfloat16*>(hidden);
+  la.sc = at<float2>(ws, L.sc);
   la.w_gate = w_gate;
   la.w_up = w_up;
   la.w_down = w_down;

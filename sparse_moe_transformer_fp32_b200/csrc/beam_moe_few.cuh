@@ -33,12 +33,14 @@ constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;  // (token, expert) slots
 constexpr int kFewWarps = 8;          // consumer warps
 // Consumers, then a warp group of producer, two finishing warps and one that only keeps it whole:
 // register budgets are given per warp group.  Launched with 168 registers a thread; while the roles run,
-// consumers hold 224 and the others 56 (256 * 224 + 128 * 56 = 384 * 168).
+// consumers hold 216 and the others 72 (256 * 216 + 128 * 72 = 384 * 168).
 constexpr int kFewThreads = (kFewWarps + 4) * 32;
-constexpr int kFewRegsLaunch = 168, kFewRegsConsumer = 224, kFewRegsOther = 56;
+constexpr int kFewRegsLaunch = 168, kFewRegsConsumer = 216, kFewRegsOther = 72;
 static_assert(kFewWarps == 8 && kFewWarps * kFewRegsConsumer + 4 * kFewRegsOther ==
                                     (kFewWarps + 4) * kFewRegsLaunch, "register budgets must add up");
-constexpr int kI4SlotBytes = 46080;   // ring slot, 4-bit weights: a tile of K = 5120, any group
+// Ring slot, 4-bit weights: a tile of K = 2560 (any group), half a tile of K = 5120.  A slot takes its
+// consumption and a round trip to HBM (about 2 us) to be ready again, so there have to be eight.
+constexpr int kI4SlotBytes = 23040;
 // Ring slot, BF16 weights: 16 rows x (2560 + 64) bytes.  Each row of a slot is a bulk copy, and one
 // SM starts a copy about every 39 ns whatever its size: segments of 640, 1280 and 2560 bytes
 // stream at 2.4, 4.8 and 7.4 TB/s over the GPU.
@@ -119,7 +121,7 @@ struct Int4LinearArgs {
   int cluster;             // CTAs that split K
   int recv;                // receive buffers of partial tiles (cluster > 1)
   int cw;                  // KSplit::cw of the largest K range
-  int stages, slot_bytes;
+  int stages, slot_bytes, stage_bytes;  // the last: of a warp's token buffer
 };
 
 struct FewRouterArgs {
@@ -130,6 +132,7 @@ struct FewRouterArgs {
   uint32_t* status;        // cleared (4 words)
   uint4* unwritten;        // what the layer kernel exchanges, set to all ones
   int64_t unwritten_n;     // in 16-byte units
+  uint64_t wait_limit_ns;
   int T, d, E;
 };
 
@@ -151,12 +154,13 @@ struct FewLayerArgs {
   float scale;
   int norm;
   int entry_max;           // tokens of an entry at most
-  int stages, slot_bytes;
+  int stages, slot_bytes, stage_bytes;  // the last: of a warp's token buffer
 };
 
 cudaError_t launch_int4_quantize(const Int4QuantArgs& a, cudaStream_t s);
 cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_t s);
 cudaError_t launch_few_router(const FewRouterArgs& a, cudaStream_t s);
+int few_router_tokens(int d);  // of one launch_few_router at most
 cudaError_t launch_few_layer(FewLayerArgs a, int group /* 0: BF16 */, int sms, cudaStream_t s);
 cudaError_t prepare_int4_kernels();
 cudaError_t prepare_few_kernels();
@@ -290,15 +294,6 @@ __device__ __forceinline__ uint4 ld_relaxed(const void* p) {
   return v;
 }
 
-// Rows that were complete before the kernel.
-struct TokenRow {
-  static constexpr bool kPolled = false;
-  __device__ __forceinline__ uint4 load(const __nv_bfloat16* p) const {
-    return __ldcg(reinterpret_cast<const uint4*>(p));
-  }
-  __device__ __forceinline__ void settle(uint4&, const __nv_bfloat16*) const {}
-};
-
 // Rows that other CTAs of the kernel are writing.  Every element was set to kUnwritten16 (a NaN that
 // no computation produces) before the kernel, so an element tells by itself whether it is there:
 // no flag has to follow the data through a fence and an atomic, which take 2 us together.
@@ -312,12 +307,12 @@ __device__ __forceinline__ bool has_unwritten16(uint4 v) {
   return (z & 0x80008000u) != 0u;
 }
 
-struct PolledRow {
-  static constexpr bool kPolled = true;
-  volatile int* abort_flag;
-  uint64_t limit_ns;
-  uint32_t* status;
-  uint32_t where;
+struct TokenSource {
+  bool polled = false;  // whether others may still be writing the rows
+  volatile int* abort_flag = nullptr;
+  uint64_t limit_ns = 0;
+  uint32_t* status = nullptr;
+  uint32_t where = 0;
   bool ok = true;
   // Whether to look again; gives up after limit_ns, or when another wait did.
   __device__ bool again(uint64_t& t0) {
@@ -334,38 +329,77 @@ struct PolledRow {
     }
     return ok;
   }
-  __device__ __forceinline__ uint4 load(const __nv_bfloat16* p) const { return ld_relaxed(p); }
   __device__ __forceinline__ void settle(uint4& v, const __nv_bfloat16* p) {
+    if (!polled) return;
     uint64_t t0 = 0;
     while (has_unwritten16(v) && ok && again(t0)) v = ld_relaxed(p);
   }
 };
 
-// B fragments of one token row's K slice: `row` points at the slice (null: an unused column,
-// zeros), 4 registers per 32 elements.
-template <int RUNS, int REGS, class Src>
-__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], Src& src, const __nv_bfloat16* row,
-                                            int runs, int c) {
-  static_assert(RUNS * 4 <= REGS, "the fragments must fit");
+// The K slice of a token row is brought in by the whole warp, 16 bytes a lane and load, and staged in
+// shared memory, from where each lane picks its fragments.  Everything that runs once per entry
+// is kept short and in loops: code that is not in the instruction cache costs about 10 ns an
+// instruction, more than its execution.
+constexpr int kRowLoads = kFewMaxK / kFewWarps / 256;
+__device__ __forceinline__ void fetch_row(uint4 (&v)[kRowLoads], const __nv_bfloat16* row, int n, int lane) {
 #pragma unroll
-  for (int j = 0; j < RUNS; ++j) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row != nullptr && j < runs) v = src.load(row + j * 32 + c * 8);
-    b[j * 4 + 0] = v.x;
-    b[j * 4 + 1] = v.y;
-    b[j * 4 + 2] = v.z;
-    b[j * 4 + 3] = v.w;
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = (i * 32 + lane) * 8;
+    if (row != nullptr && k < n) v[i] = ld_relaxed(row + k);
   }
-  if constexpr (Src::kPolled) {
+}
+// Stages what fetch_row brought; returns the largest magnitude bits of the lane's elements.
+__device__ __forceinline__ uint32_t stage_row(uint4 (&v)[kRowLoads], TokenSource& src,
+                                              const __nv_bfloat16* row, int n, uint8_t* raw, int lane) {
+  uint32_t top = 0;
 #pragma unroll
-    for (int j = 0; j < RUNS; ++j) {
-      uint4 v = make_uint4(b[j * 4], b[j * 4 + 1], b[j * 4 + 2], b[j * 4 + 3]);
-      if (row != nullptr && j < runs) src.settle(v, row + j * 32 + c * 8);
-      b[j * 4 + 0] = v.x;
-      b[j * 4 + 1] = v.y;
-      b[j * 4 + 2] = v.z;
-      b[j * 4 + 3] = v.w;
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = (i * 32 + lane) * 8;
+    if (k < n) {
+      src.settle(v[i], row + k);
+      *reinterpret_cast<uint4*>(raw + k * 2) = v[i];
+      // magnitudes, two at a time; NaN and infinity are the largest
+      const uint32_t w = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                  __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+      top = max(top, max(w << 16, w & 0xffff0000u));
     }
+  }
+  return top;
+}
+
+// B fragments of the K slices of up to 8 BF16 tokens (n elements), 4 registers per 32 elements: column
+// t is token t.  row(t): the slice's first element of token t, or null (a column of zeros).
+template <int RUNS, int REGS, class Row>
+__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& src, Row row, int tokens,
+                                            int n, uint8_t* raw, const uint8_t* zeros, int lane) {
+  static_assert(RUNS * 4 <= REGS, "the fragments must fit");
+  const int g = lane >> 2, c = lane & 3;
+  uint4 v[kRowLoads];
+  const __nv_bfloat16* next = row(0);
+  fetch_row(v, next, n, lane);
+#pragma unroll 1
+  for (int t = 0; t < tokens; ++t) {
+    const __nv_bfloat16* from = next;
+    if (from != nullptr) stage_row(v, src, from, n, raw, lane);
+    __syncwarp();
+    next = t + 1 < tokens ? row(t + 1) : nullptr;
+    fetch_row(v, next, n, lane);
+    const bool mine = g == t && from != nullptr;
+    if (mine || t == 0) {  // the first token also clears the other columns
+      const uint8_t* p = mine ? raw + c * 16 : zeros;
+      const int step = mine ? 64 : 0;
+#pragma unroll
+      for (int j = 0; j < RUNS; ++j) {
+        if (j * 32 < n) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p + j * step);
+          b[j * 4 + 0] = w.x;
+          b[j * 4 + 1] = w.y;
+          b[j * 4 + 2] = w.z;
+          b[j * 4 + 3] = w.w;
+        }
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -413,7 +447,8 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 constexpr int kI4SumStart = 0x4b400000;
 constexpr float kI4SumStartF = 12582912.f;
 constexpr int kI4SliceMax = kFewMaxK / kFewWarps;
-constexpr int kI4SplitBytes = 3 * kI4SliceMax;  // a warp's buffer for the digits of one token
+// A warp's buffer for one token of n elements: BF16, and for 4-bit weights three bytes of digits.
+__host__ __device__ constexpr int stage_bytes(int n, bool i4) { return i4 ? 5 * n : 2 * n; }
 constexpr int kI4NonFinite = 1 << 20;           // in the place of an exponent
 
 // Runs of 32 of a warp's K slice at most: 64, 80 or 120 registers of fragments.
@@ -434,23 +469,17 @@ __device__ __forceinline__ I4Scale i4_scale(uint32_t top) {
   s.f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
   return s;
 }
-__device__ __forceinline__ uint32_t i4_top(uint4 v) {  // NaN and infinity sort above the rest
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) top = max(top, max((w[j] << 16) & 0x7fff0000u, w[j] & 0x7fff0000u));
-  return top;
-}
-// Digits of 8 elements: d[p] holds digit p of elements 0..3 and 4..7, a byte each.
-__device__ __forceinline__ void i4_digits(uint2 (&d)[3], uint4 v, const I4Scale& s) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[3][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
+// Splits a staged slice (n elements, a multiple of 128) into its digits, n bytes each.
+__device__ __forceinline__ void i4_split(const uint8_t* raw, uint8_t* digits, int n, const I4Scale& s,
+                                         int lane) {
+#pragma unroll 1
+  for (int k = lane * 4; k < n; k += 128) {
+    const uint2 w = *reinterpret_cast<const uint2*>(raw + k * 2);
     uint32_t x[3][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float f = (j & 1) ? bf16_hi(w[h * 2 + (j >> 1)]) : bf16_lo(w[h * 2 + (j >> 1)]);
+      const uint32_t u = j < 2 ? w.x : w.y;
+      const float f = (j & 1) ? bf16_hi(u) : bf16_lo(u);
       // rounded to an integer by the addition of 1.5 2^23
       const uint32_t i = __float_as_uint(fmaf(f * s.f1, s.f2, kI4SumStartF)) - kI4SumStart;
       x[2][j] = i;
@@ -459,47 +488,9 @@ __device__ __forceinline__ void i4_digits(uint2 (&d)[3], uint4 v, const I4Scale&
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p)
-      o[p][h] = __byte_perm(__byte_perm(x[p][0], x[p][1], 0x0040), __byte_perm(x[p][2], x[p][3], 0x0040),
-                            0x5410);
+      *reinterpret_cast<uint32_t*>(digits + p * n + k) =
+          __byte_perm(__byte_perm(x[p][0], x[p][1], 0x0040), __byte_perm(x[p][2], x[p][3], 0x0040), 0x5410);
   }
-#pragma unroll
-  for (int p = 0; p < 3; ++p) d[p] = make_uint2(o[p][0], o[p][1]);
-}
-
-// Splits the K slice of one token (`row`: its first element; n elements, a multiple of 128) over
-// the warp into its digits in `buf`; returns E, or kI4NonFinite.  `src` reads 16 bytes (TokenRow,
-// PolledRow).
-template <class Src>
-__device__ __forceinline__ int i4_split_token(Src& src, const __nv_bfloat16* row, int n, uint8_t* buf,
-                                              int lane) {
-  constexpr int kLoads = kI4SliceMax / 256;  // 8 elements per lane and load
-  uint4 v[kLoads];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    const int k = (i * 32 + lane) * 8;
-    if (k < n) v[i] = src.load(row + k);
-  }
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int k = (i * 32 + lane) * 8;
-    if (k < n) src.settle(v[i], row + k);
-    top = max(top, i4_top(v[i]));
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (top >= 0x7f800000u) return kI4NonFinite;
-  const I4Scale s = i4_scale(top);
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int k = (i * 32 + lane) * 8;
-    if (k >= n) break;
-    uint2 d[3];
-    i4_digits(d, v[i], s);
-#pragma unroll
-    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(buf + p * kI4SliceMax + k) = d[p];
-  }
-  return s.E;
 }
 
 // What a token's products have to be multiplied with, 2^(E - 9) for sums in units of digit 0 (codes
@@ -515,94 +506,54 @@ __device__ __forceinline__ I4Factor i4_factor(int E) {
 }
 
 // B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
-// row(t): the slice's first element of token t.  factor[h]: of the token of the lane's result column h.
-//
-// MODE 1 splits a token at a time with the whole warp, through shared memory: a lane's share of the
-// conversion is 1/32 of the slice.  With more tokens each lane converts the elements of its own
-// column's token (8 lane columns, 8 tokens; 4 of them twice in MODE 2), all loads in flight at once,
-// and keeps the digits it needs.
-template <int MODE, int REGS, class Src, class Row>
-__device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&factor)[2], Src& src,
-                                               Row row, int tokens, int units,
-                                               [[maybe_unused]] uint8_t* buf, int lane) {
+// row(t): the slice's first element of token t, or null.  factor[h]: of the token of the lane's
+// result column h.
+template <int MODE, int REGS, class Row>
+__device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&factor)[2], TokenSource& src,
+                                               Row row, int tokens, int units, uint8_t* raw,
+                                               const uint8_t* zeros, int lane) {
   constexpr int kRuns = i4_mode_runs(MODE);
   static_assert(kRuns * 2 * MODE <= REGS, "the fragments must fit");
-  const int g = lane >> 2, c = lane & 3;
+  const int g = lane >> 2, c = lane & 3, n = units * kI4Unit;
+  uint8_t* const digits = raw + 2 * n;
+  const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of result column 0
   int E[2] = {0, 0};
-  if constexpr (MODE == 1) {
-#pragma unroll
-    for (int j = 0; j < REGS; ++j) b[j] = 0u;
+  uint4 v[kRowLoads];
+  const __nv_bfloat16* next = row(0);
+  fetch_row(v, next, n, lane);
 #pragma unroll 1
-    for (int t = 0; t < tokens; ++t) {
-      __syncwarp();
-      const int e = i4_split_token(src, row(t), units * kI4Unit, buf, lane);
-      E[0] = t == 0 ? e : E[0];
-      E[1] = t == 1 ? e : E[1];
-      __syncwarp();
-      if ((g & 1) == t && g < 6) {
-        const uint8_t* p = buf + (g >> 1) * kI4SliceMax + c * 8;
+  for (int t = 0; t < tokens; ++t) {
+    const __nv_bfloat16* from = next;
+    uint32_t top = 0;
+    if (from != nullptr) top = stage_row(v, src, from, n, raw, lane);
+    top = __reduce_max_sync(0xffffffffu, top);
+    next = t + 1 < tokens ? row(t + 1) : nullptr;
+    fetch_row(v, next, n, lane);
+    const I4Scale s = i4_scale(top);
+    if (from != nullptr) i4_split(raw, digits, n, s, lane);
+    __syncwarp();
+    const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
+    if (t == first) E[0] = e;
+    if (t == first + 1) E[1] = e;
+#pragma unroll
+    for (int nt = 0; nt < MODE; ++nt) {
+      const int token = MODE == 1 ? (g & 1) : MODE == 2 ? (g & 3) : g;
+      const int digit = MODE == 1 ? (g >> 1) : MODE == 2 ? (nt ? 2 + (g >> 2) : (g >> 2)) : nt;
+      const bool mine = token == t && digit < 3 && from != nullptr;
+      if (mine || t == 0) {  // the first token also clears the other columns
+        const uint8_t* p = mine ? digits + digit * n + c * 8 : zeros;
+        const int step = mine ? 32 : 0;
 #pragma unroll
         for (int j = 0; j < kRuns; ++j) {
           if (j < units * 4) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p + j * 32);
-            b[j * 2] = w.x;
-            b[j * 2 + 1] = w.y;
+            const uint2 w = *reinterpret_cast<const uint2*>(p + j * step);
+            b[(j * MODE + nt) * 2] = w.x;
+            b[(j * MODE + nt) * 2 + 1] = w.y;
           }
         }
       }
     }
-  } else {
-    const int t = MODE == 2 ? (g & 3) : g;
-    const __nv_bfloat16* p = t < tokens ? row(t) + c * 8 : nullptr;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (p != nullptr && j < units * 4) v = src.load(p + j * 32);
-      b[j * 2 * MODE] = v.x;
-      b[j * 2 * MODE + 1] = v.y;
-      b[j * 2 * MODE + 2] = v.z;
-      b[j * 2 * MODE + 3] = v.w;
-    }
-#pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
-      uint4 v = make_uint4(b[j * 2 * MODE], b[j * 2 * MODE + 1], b[j * 2 * MODE + 2], b[j * 2 * MODE + 3]);
-      if constexpr (Src::kPolled) {
-        if (p != nullptr && j < units * 4) src.settle(v, p + j * 32);
-        b[j * 2 * MODE] = v.x;
-        b[j * 2 * MODE + 1] = v.y;
-        b[j * 2 * MODE + 2] = v.z;
-        b[j * 2 * MODE + 3] = v.w;
-      }
-      top = max(top, i4_top(v));
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const I4Scale s = i4_scale(top);
-    const int r = top >= 0x7f800000u ? kI4NonFinite : s.E;
-    // result column h of lane column c: token 2 (c % 2) + h or 2 c + h, in lane 4 token
-    const int first = MODE == 2 ? 2 * (c & 1) : 2 * c;
-    E[0] = __shfl_sync(0xffffffffu, r, first * 4);
-    E[1] = __shfl_sync(0xffffffffu, r, first * 4 + 4);
-#pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
-      uint2 d[3];
-      i4_digits(d, make_uint4(b[j * 2 * MODE], b[j * 2 * MODE + 1], b[j * 2 * MODE + 2],
-                              b[j * 2 * MODE + 3]), s);
-      if constexpr (MODE == 2) {
-        const uint2 x = g < 4 ? d[0] : d[1], y = g < 4 ? d[2] : make_uint2(0u, 0u);
-        b[j * 4] = x.x;
-        b[j * 4 + 1] = x.y;
-        b[j * 4 + 2] = y.x;
-        b[j * 4 + 3] = y.y;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          b[j * 6 + q * 2] = d[q].x;
-          b[j * 6 + q * 2 + 1] = d[q].y;
-        }
-      }
-    }
+    __syncwarp();
   }
   factor[0] = i4_factor(E[0]);
   factor[1] = i4_factor(E[1]);

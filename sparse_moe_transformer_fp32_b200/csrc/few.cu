@@ -12,87 +12,99 @@ namespace {
 
 // logits = h W_r^T, s = sigmoid(logit), sb = s + bias.  The sums run in FP64 and are rounded to
 // FP32 once, and so is the sigmoid, so that the scores are the exactly rounded ones and near ties
-// fall as the definition has them.  Operands are widened with integer operations: the conversion
-// instruction takes about 20 clocks of an SM a warp (at T = 16 the kernel took 39 us with it).  Two
-// experts per CTA: 128 CTAs for 256 experts, each reading 2 d FP32 weights; latency-bound at 5.2 MB
-// in all.
+// fall as the definition has them.
+//
+// Two experts per CTA: 128 CTAs for 256 experts.  Their rows and all tokens are copied into shared
+// memory (2 bulk copies), and a warp takes a pair of tokens and a part of K.  Operands are widened
+// with integer operations: the conversion instruction takes about 20 clocks of an SM a warp (at
+// T = 16 the kernel took 39 us with it).  Bound by latency: 5.2 MB in all, and code that runs once.
 //
 // The kernel also clears the status words and marks as unwritten what the layer kernel exchanges.
-constexpr int kRtThreads = 256, kRtExperts = 2;
+constexpr int kRtThreads = 256, kRtExperts = 2, kRtWarps = kRtThreads / 32;
 
-// FP32 to FP64: exponent rebiased by 896; subnormals count as zero (they are below 2^-126).
-__device__ __forceinline__ double widen(float v) {
-  const uint32_t u = __float_as_uint(v), m = u & 0x7fffffffu;
-  uint32_t hi = (m >> 3) + 0x38000000u;
-  if (m < 0x00800000u) hi = 0u;
-  if (m >= 0x7f800000u) hi |= 0x7ff00000u;
-  return __hiloint2double(static_cast<int>(hi | (u & 0x80000000u)),
-                          m < 0x00800000u ? 0 : static_cast<int>(u << 29));
+// FP32 to FP64: exponent rebiased by 896.  Zero and subnormals become values of at most 2^-126,
+// infinity and NaN values of at least 2^128 (such a token's outputs are NaN whatever its experts).
+__device__ __forceinline__ double widen(uint32_t u) {
+  const int hi = ((static_cast<int>(u) >> 3) & static_cast<int>(0x8fffffffu)) + 0x38000000;
+  return __hiloint2double(hi, static_cast<int>(u << 29));
 }
 
-template <int TM>
 __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterArgs a) {
-  __shared__ double part[kRtThreads / 32][kRtExperts * TM];
+  extern __shared__ __align__(128) uint8_t rt_smem[];
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ double part[kRtWarps][2 * kRtExperts];
+  __shared__ int abort_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch();
+  const int e0 = blockIdx.x * kRtExperts;
+  const uint32_t w_bytes = kRtExperts * a.d * 4, h_bytes = a.T * a.d * 2;
+  if (threadIdx.x == 0) {
+    abort_sh = 0;
+    mbar_init(smem_u32(&bar), 1);
+    fence_mbarrier_init();
+    mbar_arrive_expect_tx(smem_u32(&bar), w_bytes + h_bytes);
+    bulk_load(smem_u32(rt_smem), a.W + static_cast<size_t>(e0) * a.d, w_bytes, smem_u32(&bar));
+    bulk_load(smem_u32(rt_smem) + w_bytes, a.h, h_bytes, smem_u32(&bar));
+  }
   if (blockIdx.x == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0u;
   for (int64_t i = blockIdx.x * kRtThreads + threadIdx.x; i < a.unwritten_n;
        i += static_cast<int64_t>(gridDim.x) * kRtThreads)
     a.unwritten[i] = make_uint4(kUnwritten32, kUnwritten32, kUnwritten32, kUnwritten32);
-  const int e0 = blockIdx.x * kRtExperts;
-  double acc[kRtExperts][TM];
-#pragma unroll
-  for (int j = 0; j < kRtExperts; ++j)
-#pragma unroll
-    for (int t = 0; t < TM; ++t) acc[j][t] = 0.0;
-#pragma unroll(TM <= 2 ? 5 : 2)
-  for (int k = threadIdx.x * 4; k < a.d; k += kRtThreads * 4) {
-    float4 w[kRtExperts];
-    uint2 h[TM];
-#pragma unroll
-    for (int j = 0; j < kRtExperts; ++j)
-      w[j] = __ldg(reinterpret_cast<const float4*>(a.W + static_cast<size_t>(e0 + j) * a.d + k));
-#pragma unroll
-    for (int t = 0; t < TM; ++t)
-      h[t] = t < a.T ? __ldg(reinterpret_cast<const uint2*>(a.h + static_cast<size_t>(t) * a.d + k))
-                     : make_uint2(0u, 0u);
-    double wd[kRtExperts][4];
-#pragma unroll
-    for (int j = 0; j < kRtExperts; ++j) {
-      wd[j][0] = widen(w[j].x);
-      wd[j][1] = widen(w[j].y);
-      wd[j][2] = widen(w[j].z);
-      wd[j][3] = widen(w[j].w);
-    }
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      const double hd[4] = {widen(bf16_lo(h[t].x)), widen(bf16_hi(h[t].x)), widen(bf16_lo(h[t].y)),
-                            widen(bf16_hi(h[t].y))};
-#pragma unroll
-      for (int j = 0; j < kRtExperts; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][t] = fma(wd[j][i], hd[i], acc[j][t]);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kRtExperts; ++j)
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      double v = acc[j][t];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) part[warp][j * TM + t] = v;
-    }
   __syncthreads();
-  if (threadIdx.x < kRtExperts * TM) {
-    const int j = threadIdx.x / TM, t = threadIdx.x % TM;
-    if (t < a.T) {
-      double v = 0.0;
+  // a copy that never lands leaves the CTA's scores undefined; the layer kernel's waits do not
+  // depend on them
+  mbar_wait_bounded(smem_u32(&bar), 0, &abort_sh, a.wait_limit_ns ? a.wait_limit_ns : 1000000000ull, nullptr, 0);
+  const float* W = reinterpret_cast<const float*>(rt_smem);
+  const __nv_bfloat16* h = reinterpret_cast<const __nv_bfloat16*>(rt_smem + w_bytes);
+  // warps: pairs of tokens, and parts of K while there are warps to spare
+  const int pairs = (a.T + 1) / 2;
+  const int log_parts = pairs == 1 ? 3 : pairs == 2 ? 2 : pairs <= 4 ? 1 : 0;
+  const int pair = warp >> log_parts, t0 = pair * 2, t1 = t0 + 1 < a.T ? t0 + 1 : t0;
+  const int span = a.d >> log_parts;
+  if (pair < pairs) {
+    double acc[2][kRtExperts] = {};
+    const int k0 = (warp & ((1 << log_parts) - 1)) * span;
+#pragma unroll 1
+    for (int k = k0 + lane * 4; k < k0 + span; k += 128) {
+      const uint2 x[2] = {*reinterpret_cast<const uint2*>(h + static_cast<size_t>(t0) * a.d + k),
+                          *reinterpret_cast<const uint2*>(h + static_cast<size_t>(t1) * a.d + k)};
+      double hd[2][4];
 #pragma unroll
-      for (int w = 0; w < kRtThreads / 32; ++w) v += part[w][threadIdx.x];
-      const float logit = static_cast<float>(v);
-      const float s = static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logit))));
-      a.sc[static_cast<size_t>(t) * a.E + e0 + j] = make_float2(s, s + a.bias[e0 + j]);
+      for (int t = 0; t < 2; ++t) {
+        hd[t][0] = widen(x[t].x << 16);
+        hd[t][1] = widen(x[t].x & 0xffff0000u);
+        hd[t][2] = widen(x[t].y << 16);
+        hd[t][3] = widen(x[t].y & 0xffff0000u);
+      }
+#pragma unroll
+      for (int j = 0; j < kRtExperts; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(W + j * a.d + k);
+        const double wd[4] = {widen(w.x), widen(w.y), widen(w.z), widen(w.w)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[0][j] = fma(wd[i], hd[0][i], acc[0][j]);
+          acc[1][j] = fma(wd[i], hd[1][i], acc[1][j]);
+        }
+      }
     }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < kRtExperts; ++j) acc[t][j] += __shfl_xor_sync(0xffffffffu, acc[t][j], o);
+    if (lane < 2 * kRtExperts)
+      part[warp][lane] = lane == 0 ? acc[0][0] : lane == 1 ? acc[0][1] : lane == 2 ? acc[1][0] : acc[1][1];
+  }
+  __syncthreads();
+  if (threadIdx.x < kRtExperts * a.T) {
+    const int j = threadIdx.x % kRtExperts, t = threadIdx.x / kRtExperts;
+    double v = 0.0;
+    for (int p = 0; p < 1 << log_parts; ++p)
+      v += part[((t >> 1) << log_parts) + p][(t & 1) * kRtExperts + j];
+    const float logit = static_cast<float>(v);
+    const float s = static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logit))));
+    a.sc[static_cast<size_t>(t) * a.E + e0 + j] = make_float2(s, s + a.bias[e0 + j]);
   }
 }
 
@@ -119,6 +131,9 @@ __device__ __forceinline__ uint32_t score_key(float v) {
 
 constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..24
 
+constexpr uint8_t kNoSlot = 255;
+constexpr int kSlotTable = kFewMaxTokens * kMaxE * 8;  // offset in the ring, behind the scores
+
 struct FewShared {
   uint64_t full_bar[kFewMaxStages], empty_bar[kFewMaxStages];
   uint64_t red_full[kFewRed], red_empty[kFewRed];
@@ -126,89 +141,87 @@ struct FewShared {
   uint32_t mask[kMaxE];                 // tokens of each expert
   uint8_t chosen[kFewMaxTokens][kMaxTopK];  // chosen experts of each token, ascending
   uint8_t entry_e[kFewMaxSlots];        // expert of each entry
-  uint8_t entry_n[kFewMaxSlots];        // its tokens, 1..8
-  uint8_t entry_slot[kFewMaxSlots][kFewCols];  // their slots
+  uint8_t entry_n[kFewMaxSlots];        // its token columns, 1..8
+  uint8_t entry_slot[kFewMaxSlots][kFewCols];  // their slots, or kNoSlot
+  int warp_entries[kFewWarps];
+  alignas(16) uint8_t zeros[16];
   int n_entries, abort_flag;
 };
 
 // Selection of token `t` by one warp from its E (score, biased score) pairs in `sc`:
 // the Gk groups with the largest sums of their two best biased scores, the k best experts in
 // them, ties to the lower index; ascending experts and normalised weights out.
-__device__ void few_select(const FewLayerArgs& a, const float2* sc, FewShared& sh, int t, int lane) {
+// slot_of[t * E + e]: the slot j of expert e.
+__device__ void few_select(const FewLayerArgs& a, const float2* sc, uint8_t* slot_of, FewShared& sh,
+                           int t, int lane) {
   const int P = a.E / a.G;
   uint32_t gkey = 0;
-  if (lane < a.G) {
-    float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
-    bool nan = false;
+  if (lane < a.G) {  // lane g: the sum of group g's two best
+    float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F, n = 0.f;
     int jj = lane % P;  // start at different banks
 #pragma unroll 4
     for (int j = 0; j < P; ++j) {
       const float v = sc[lane * P + jj].y;
       if (++jj == P) jj = 0;
-      nan |= v != v;
-      if (v > m1) {
-        m2 = m1;
-        m1 = v;
-      } else if (v > m2) {
-        m2 = v;
-      }
+      n += v - v;  // NaN if a score is NaN (or infinite)
+      m2 = fmaxf(m2, fminf(m1, v));
+      m1 = fmaxf(m1, v);
     }
-    gkey = nan ? 0xffffffffu : score_key(P >= 2 ? m1 + m2 : m1);
+    gkey = score_key((P >= 2 ? m1 + m2 : m1) + n);
   }
   int grank = 0;
+#pragma unroll 1
   for (int g = 0; g < a.G; ++g) {
     const uint32_t o = __shfl_sync(0xffffffffu, gkey, g);
-    if (o > gkey || (o == gkey && g < lane)) ++grank;
+    grank += o > gkey || (o == gkey && g < lane);
   }
   const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.G && grank < a.Gk);
-  // experts lane, lane + 32, ...: ties between lanes fall to the lower expert below
+  // experts lane, lane + 32, ...
+  const uint32_t inv = (65536u + P - 1) / P;  // e / P = e inv / 65536 for e, P <= 256
   uint32_t key[kMaxE / 32];
 #pragma unroll
   for (int i = 0; i < kMaxE / 32; ++i) {
     const int e = lane + 32 * i;
-    key[i] = e < a.E && ((kept >> (e / P)) & 1u) ? score_key(sc[e].y) : 0u;
+    key[i] = e < a.E && ((kept >> ((e * inv) >> 16)) & 1u) ? score_key(sc[e].y) : 0u;
   }
-  uint32_t chosen = 0;  // bit i: expert lane + 32 i
+  // k times the best; ties to the lower expert
+  uint32_t at = 0;  // experts chosen, in the lane's registers: bit i of `chosen`
+  uint32_t chosen = 0;
+#pragma unroll 1
   for (int r = 0; r < a.k; ++r) {
-    uint32_t best = 0;
-    int bi = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < kMaxE / 32; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
-      }
+    for (int i = 1; i < kMaxE / 32; ++i) best = max(best, key[i]);
     const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-    const uint32_t cand = best == m ? static_cast<uint32_t>(lane + 32 * bi) : 0xffffffffu;
-    const uint32_t win = __reduce_min_sync(0xffffffffu, cand);
-    if (cand == win) {
-      chosen |= 1u << bi;
+    uint32_t cand = kMaxE;  // the lane's lowest expert with that key
 #pragma unroll
-      for (int i = 0; i < kMaxE / 32; ++i)
-        if (i == bi) key[i] = 0u;
-    }
+    for (int i = kMaxE / 32 - 1; i >= 0; --i) cand = key[i] == m ? static_cast<uint32_t>(32 * i + lane) : cand;
+    cand = __reduce_min_sync(0xffffffffu, cand);
+    const uint32_t mine = (cand & 31u) == static_cast<uint32_t>(lane) ? cand >> 5 : kMaxE;
+    chosen |= mine < 32u ? 1u << mine : 0u;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; ++i) key[i] = mine == static_cast<uint32_t>(i) ? 0u : key[i];
   }
-  // ascending expert ids, and the sum of the chosen scores in that order
-  int at = 0;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxE / 32; ++i) {
-    uint32_t b = __ballot_sync(0xffffffffu, (chosen >> i) & 1u);
-    while (b) {
-      const int e = (__ffs(b) - 1) + 32 * i;
-      b &= b - 1;
-      sum += sc[e].x;
-      if (lane == 0) {
-        sh.chosen[t][at] = static_cast<uint8_t>(e);
-        atomicOr(&sh.mask[e], 1u << t);
-      }
-      ++at;
+  // slots: chosen experts in ascending order
+#pragma unroll 1
+  for (int i = 0; i < (a.E + 31) / 32; ++i) {
+    const bool c = (chosen >> i) & 1u;
+    const uint32_t b = __ballot_sync(0xffffffffu, c);
+    if (c) {
+      const int e = lane + 32 * i, j = at + __popc(b & ((1u << lane) - 1u));
+      sh.chosen[t][j] = static_cast<uint8_t>(e);
+      slot_of[t * a.E + e] = static_cast<uint8_t>(j);
+      atomicOr(&sh.mask[e], 1u << t);
     }
+    at += __popc(b);
   }
   __syncwarp();
+  const int e = lane < a.k ? sh.chosen[t][lane] : 0;
+  const float s = lane < a.k ? sc[e].x : 0.f;
+  float sum = 0.f;  // in ascending order
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, s, j);
   if (lane < a.k) {
-    const int e = sh.chosen[t][lane];
-    const float s = sc[e].x;
     const float w = a.norm ? a.scale * s / sum : a.scale * s;
     sh.wts[t * a.k + lane] = w;
     if (blockIdx.x == 0) {
@@ -218,38 +231,44 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, FewShared& s
   }
 }
 
-// Lists the touched experts ascending, entry_max tokens at most to an entry (one more token of an
-// expert opens a second entry that reads its weights again: with 8 to an entry and at most 16 tokens
-// that takes a routing where more than half of them agree).  Run by one warp.
-__device__ void few_entries(const FewLayerArgs& a, FewShared& sh, int lane) {
-  int base = 0;
-#pragma unroll 1
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    const int e = e0 + lane;
-    uint32_t m = e < a.E ? sh.mask[e] : 0u;
-    const int need = (__popc(m) + a.entry_max - 1) / a.entry_max;
-    int incl = need;
+// Lists the touched experts ascending, run by the consumer warps, a thread to an expert.
+//   by_token: an entry's column t is token t (kNoSlot where the token has other experts), so that all
+//             entries share the token fragments of gate|up;
+//   else      its columns are its tokens, entry_max at most; one more opens a second entry that reads
+//             the weights again (with 8 to an entry and at most 16 tokens that takes a routing where
+//             more than half of them agree).
+__device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewShared& sh, bool by_token) {
+  const int e = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(kFewWarps * 32 == kMaxE, "a thread to an expert");
+  uint32_t m = e < a.E ? sh.mask[e] : 0u;
+  const int shift = a.entry_max == 2 ? 1 : 3;
+  const int need = by_token ? m != 0u : (__popc(m) + a.entry_max - 1) >> shift;
+  int incl = need;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    int at = base + incl - need;
-    for (int p = 0; p < need; ++p, ++at) {
-      int n = 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh.warp_entries[warp] = incl;
+  asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
+  int at = incl - need;
+  for (int w = 0; w < warp; ++w) at += sh.warp_entries[w];
+  if (e == kMaxE - 1) sh.n_entries = at + need;
+  for (int p = 0; p < need; ++p, ++at) {
+    int n = 0;
+    if (by_token) {
+      for (; n < a.T; ++n)
+        sh.entry_slot[at][n] = (m >> n) & 1u ? static_cast<uint8_t>(n * a.k + slot_of[n * a.E + e]) : kNoSlot;
+    } else {
       while (m && n < a.entry_max) {
         const int t = __ffs(m) - 1;
         m &= m - 1;
-        int j = 0;
-        while (sh.chosen[t][j] != e) ++j;
-        sh.entry_slot[at][n++] = static_cast<uint8_t>(t * a.k + j);
+        sh.entry_slot[at][n++] = static_cast<uint8_t>(t * a.k + slot_of[t * a.E + e]);
       }
-      sh.entry_e[at] = static_cast<uint8_t>(e);
-      sh.entry_n[at] = static_cast<uint8_t>(n);
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    sh.entry_e[at] = static_cast<uint8_t>(e);
+    sh.entry_n[at] = static_cast<uint8_t>(n);
   }
-  if (lane == 0) sh.n_entries = base;
 }
 
 // Everything after the router scores, in one cooperative persistent kernel:
@@ -290,34 +309,47 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       mbar_init(smem_u32(&sh.red_empty[i]), 1);
     }
     sh.abort_flag = 0;
+    *reinterpret_cast<uint4*>(sh.zeros) = make_uint4(0u, 0u, 0u, 0u);
     fence_mbarrier_init();
   }
   // the tokens' scores, in the ring's space until the weights need it
   float2* sc = reinterpret_cast<float2*>(smem);
+  uint8_t* slot_of = smem + kSlotTable;
+  // With few enough tokens the columns of every entry are the tokens: the fragments of gate|up are
+  // loaded once, while other warps select.
+  const bool by_token = a.T <= (kI4 ? 2 : kFewCols);
+  auto select = [&](int first, int step) {
+    for (int t = first; t < a.T; t += step) few_select(a, sc + t * a.E, slot_of, sh, t, lane);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic accesses before bulk writes
+  };
+  pdl_wait();
   for (int i = threadIdx.x; i < a.T * a.E; i += kFewThreads) sc[i] = a.sc[i];
-  __syncthreads();
-  for (int t = warp; t < a.T; t += kFewThreads / 32) few_select(a, sc + t * a.E, sh, t, lane);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic reads before bulk writes
-  __syncthreads();
-  if (warp == 0) few_entries(a, sh, lane);
   __syncthreads();
 
   // ---- this CTA's items
   const int n_gu = a.I / 8, n_dn = a.d / 16;
-  // 32 bits suffice: at most 128 entries, and K in units of 128
-  const uint32_t N1 = sh.n_entries * n_gu, N2 = sh.n_entries * n_dn, K1 = a.d / 128, K2 = a.I / 128;
-  const uint32_t grid = gridDim.x;
-  auto first1 = [&](uint32_t b) { return b * N1 / grid; };
-  // Down items start where the CTAs before b have b / grid of all bytes (an item's are 16 K;
-  // gate|up: K = d, down: K = I).  That is monotone in b as long as a CTA's down bytes cover the
-  // one gate|up item by which the first runs differ; below that, an even cut.
-  auto first2 = [&](uint32_t b) {
-    if (N2 * K2 < grid * K1) return b * N2 / grid;
-    const uint32_t v = (b * (N1 * K1 + N2 * K2) / grid - first1(b) * K1) / K2;
-    return b == grid || v > N2 ? N2 : v;
+  int i1, j1, i2, j2;
+  auto cut = [&] {
+    // 32 bits suffice: at most 128 entries, and K in units of 128
+    const uint32_t N1 = sh.n_entries * n_gu, N2 = sh.n_entries * n_dn, K1 = a.d / 128, K2 = a.I / 128;
+    const uint32_t grid = gridDim.x;
+    // Lanes 0, 1: this CTA's and the next one's first gate|up item; 2, 3: down items.  Those start
+    // where the CTAs before b have b / grid of all bytes (an item's are 16 K; gate|up: K = d, down:
+    // K = I).  That is monotone in b as long as a CTA's down bytes cover the one gate|up item by
+    // which the first runs differ; below that, an even cut.
+    const uint32_t b = blockIdx.x + (lane & 1);
+    const bool even = N2 * K2 < grid * K1;
+    uint32_t v = b * N1 / grid;
+    if (lane & 2) {
+      const uint32_t w = (even ? b * N2 : b * (N1 * K1 + N2 * K2)) / grid;
+      v = even ? w : (w - v * K1) / K2;
+      if (b == grid || v > N2) v = N2;
+    }
+    i1 = __shfl_sync(0xffffffffu, v, 0);
+    j1 = __shfl_sync(0xffffffffu, v, 1);
+    i2 = __shfl_sync(0xffffffffu, v, 2);
+    j2 = __shfl_sync(0xffffffffu, v, 3);
   };
-  const int i1 = first1(blockIdx.x), j1 = first1(blockIdx.x + 1);
-  const int i2 = first2(blockIdx.x), j2 = first2(blockIdx.x + 1);
 
   if (warp < kFewWarps) {
     more_registers<kFewRegsConsumer>();
@@ -325,57 +357,63 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
     // token fragments: BF16 4 registers a run of 32; INT8 digits 2, 4 or 6 (4 and 6: up to 20 runs)
     uint32_t b[!kI4 ? 128 : MODES == 1 ? 64 : MODES == 2 ? 80 : 120];
     [[maybe_unused]] I4Factor factor[2];
-    [[maybe_unused]] uint8_t* const split =
-        smem + a.stages * a.slot_bytes + kRed * kFewWarps * 512 + warp * kI4SplitBytes;
+    uint8_t* const raw = smem + a.stages * a.slot_bytes + kRed * kFewWarps * 512 + warp * a.stage_bytes;
     int n_tok = 0;
+    auto load = [&](int ph, int entry) {  // entry < 0: all tokens
+      const KSplit ks = ph ? a.k2 : a.k1;
+      const int K = ph ? a.I : a.d, units = ks.count(warp);
+      const __nv_bfloat16* from = (ph ? a.act : a.h) + ks.start(warp) * kUnit;
+      TokenSource src{ph != 0, abort_flag, a.wait_limit_ns, a.status, kWhereFew + 1};
+      auto row = [&](int col) -> const __nv_bfloat16* {
+        if (entry < 0) return from + static_cast<size_t>(col) * K;
+        const int s = sh.entry_slot[entry][col];
+        return s == kNoSlot ? nullptr : from + static_cast<size_t>(ph ? s : s / a.k) * K;
+      };
+      n_tok = entry < 0 ? a.T : sh.entry_n[entry];
+      if constexpr (kI4) {
+        if (MODES == 1 || n_tok <= 2)
+          i4_load_tokens<1>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
+        else if (MODES == 2 || n_tok <= 4)
+          i4_load_tokens<(MODES > 1 ? 2 : 1)>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
+        else
+          i4_load_tokens<MODES>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
+      } else {
+        load_tokens<kRuns>(b, src, row, n_tok, units * kUnit, raw, sh.zeros, lane);
+      }
+      return __all_sync(0xffffffffu, src.ok) != 0;
+    };
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
     bool ok = true;
+    // Phase -1 is the selection, with the loading of all tokens if they stay; as a turn of the same
+    // loop so that there is one copy of the loading code.
 #pragma unroll 1
-    for (int ph = 0; ph < 2 && ok; ++ph) {
-      const KSplit ks = ph ? a.k2 : a.k1;
-      const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
-      const int first = ph ? i2 : i1, last = ph ? j2 : j1;
+    for (int ph = -1; ph < 2 && ok; ++ph) {
+      const KSplit ks = ph > 0 ? a.k2 : a.k1;
+      const int per = ph > 0 ? n_dn : n_gu;
+      const int first = ph < 0 ? 0 : ph ? i2 : i1, last = ph < 0 ? 1 : ph ? j2 : j1;
       const int units = ks.count(warp), mine = warp / ks.cw, chunks = ks.chunks();
       const int cstart = ks.start(mine * ks.cw);
       const int cunits = ks.start((mine + 1) * ks.cw) - cstart;
       const int uoff = ks.start(warp) - cstart;
       const uint32_t off = kI4 ? uoff * kUnitBytes : uoff * 64;
       const int stride = bf16_row_stride(cunits);
-      const int k0 = ks.start(warp) * kUnit;
       int entry = first / per, tile = first % per, loaded = -1;
 #pragma unroll 1
       for (int it = first; it < last; ++it) {
-        if (entry != loaded) {  // token fragments of the entry
+        if (ph < 0 ? by_token : entry != loaded && !(ph == 0 && by_token)) {
           loaded = entry;
-          n_tok = sh.entry_n[entry];
-          auto row = [&](int col) {
-            const int s = sh.entry_slot[entry][col];
-            return ph ? a.act + static_cast<size_t>(s) * K + k0
-                      : a.h + static_cast<size_t>(s / a.k) * K + k0;
-          };
-          auto load = [&](auto& src) {
-            if constexpr (kI4) {
-              if (MODES == 1 || n_tok <= 2)
-                i4_load_tokens<1>(b, factor, src, row, n_tok, units, split, lane);
-              else if (MODES == 2 || n_tok <= 4)
-                i4_load_tokens<(MODES > 1 ? 2 : 1)>(b, factor, src, row, n_tok, units, split, lane);
-              else
-                i4_load_tokens<MODES>(b, factor, src, row, n_tok, units, split, lane);
-            } else {
-              const int col = lane >> 2;
-              load_tokens<kRuns>(b, src, col < n_tok ? row(col) : nullptr, units, lane & 3);
-            }
-          };
-          if (ph) {
-            PolledRow src{abort_flag, a.wait_limit_ns, a.status, kWhereFew + 1};
-            load(src);
-            ok = __all_sync(0xffffffffu, src.ok);
-            if (!ok) break;
-          } else {
-            TokenRow src;
-            load(src);
-          }
+          ok = load(ph > 0 ? 1 : 0, ph < 0 ? -1 : entry);
+          if (!ok) break;
+        }
+        if (ph < 0) {
+          if (!by_token) select(warp, kFewThreads / 32);
+          __syncthreads();  // every token's selection is there
+          few_entries(a, slot_of, sh, by_token);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncthreads();  // and the entries; the ring is the producer's
+          cut();
+          continue;
         }
         float4 part = make_float4(0.f, 0.f, 0.f, 0.f);  // rows g, g of two tokens, then g + 8
         // every warp passes every chunk in order: a phase may only be waited for by who has seen
@@ -434,6 +472,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
     fewer_registers<kFewRegsLaunch>();
   } else {
     fewer_registers<kFewRegsOther>();
+    if (by_token)
+      select(warp - kFewWarps, kFewThreads / 32 - kFewWarps);
+    else
+      select(warp, kFewThreads / 32);
+    __syncthreads();
+    __syncthreads();
+    cut();
   if (warp == kFewWarps) {
     // ---- producer
     int slot = 0;
@@ -541,7 +586,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = c * 2 + h;
-          if (col < n) {
+          if (col < n && sh.entry_slot[entry][col] != kNoSlot) {
             const size_t s = sh.entry_slot[entry][col];
             if (ph == 0) {
               st_relaxed16(a.act + s * a.I + tile * 8 + g, __float2bfloat16_rn(swiglu(lo[h], hi[h])));
@@ -568,7 +613,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
   __syncthreads();
   if (sh.abort_flag) return;
   const int q0 = blockIdx.x * (a.d / 4) / gridDim.x, nq = (blockIdx.x + 1) * (a.d / 4) / gridDim.x - q0;
-  PolledRow poll{abort_flag, a.wait_limit_ns, a.status, kWhereFew + 5};
+  TokenSource poll{true, abort_flag, a.wait_limit_ns, a.status, kWhereFew + 5};
   for (int u = threadIdx.x; u < nq * a.T; u += kFewThreads) {
     const int t = u / nq, col = (q0 + u % nq) * 4;
     const float* y = a.y + static_cast<size_t>(t) * a.k * a.d + col;
@@ -609,27 +654,24 @@ LayerKernel layer_kernel(int group, int modes) {
                        : layer_kernel_of<128>(modes);
 }
 
-constexpr size_t kFewDynamicSmem = kFewSmemMax - 6144;  // the rest: FewShared
-static_assert(sizeof(FewShared) <= 6144, "FewShared must fit beside the ring");
+constexpr size_t kFewDynamicSmem = kFewSmemMax - 4096;  // the rest: FewShared
+static_assert(sizeof(FewShared) <= 4096, "FewShared must fit beside the ring");
 // the scores of 16 tokens fit in the ring
-static_assert(kFewMaxTokens * kMaxE * 8 <= kI4SlotBytes && kFewMaxTokens * kMaxE * 8 <= kBf16SlotBytes, "scores must fit in the ring");
+static_assert(kFewMaxTokens * kMaxE * 9 <= 2 * kI4SlotBytes && kFewMaxTokens * kMaxE * 9 <= 2 * kBf16SlotBytes,
+              "scores and slots must fit in the ring");
+
+
+constexpr int kRtSmemMax = kFewSmemMax - 1024;
 
 }  // namespace
 
 cudaError_t launch_few_router(const FewRouterArgs& a, cudaStream_t s) {
-  const dim3 grid(a.E / kRtExperts);
-  if (a.T <= 1)
-    few_router_kernel<1><<<grid, kRtThreads, 0, s>>>(a);
-  else if (a.T <= 2)
-    few_router_kernel<2><<<grid, kRtThreads, 0, s>>>(a);
-  else if (a.T <= 4)
-    few_router_kernel<4><<<grid, kRtThreads, 0, s>>>(a);
-  else if (a.T <= 8)
-    few_router_kernel<8><<<grid, kRtThreads, 0, s>>>(a);
-  else
-    few_router_kernel<16><<<grid, kRtThreads, 0, s>>>(a);
+  const size_t smem = static_cast<size_t>(kRtExperts) * a.d * 4 + static_cast<size_t>(a.T) * a.d * 2;
+  few_router_kernel<<<a.E / kRtExperts, kRtThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
+
+int few_router_tokens(int d) { return (kRtSmemMax - kRtExperts * d * 4) / (d * 2); }
 
 cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
@@ -638,27 +680,34 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   a.slot_bytes = group ? kI4SlotBytes : kBf16SlotBytes;
   a.k1 = make_ksplit(a.d / unit, a.slot_bytes, unit_bytes);
   a.k2 = make_ksplit(a.I / unit, a.slot_bytes, unit_bytes);
+  const int most = (a.d > a.I ? a.d : a.I) / unit;  // of a warp's K slice
+  a.stage_bytes = stage_bytes((most + kFewWarps - 1) / kFewWarps * unit, group != 0);
   const size_t red = static_cast<size_t>(group ? kFewRed : kBf16Red) * kFewWarps * 512 +
-                     (group ? static_cast<size_t>(kFewWarps) * kI4SplitBytes : 0);
+                     static_cast<size_t>(kFewWarps) * a.stage_bytes;
   a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);
   if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
   // no more CTAs than gate|up items can exist
-  const int64_t most = static_cast<int64_t>(a.T) * a.k * (a.I / 8);
-  const int grid = most < sms ? static_cast<int>(most) : sms;
+  const int64_t items = static_cast<int64_t>(a.T) * a.k * (a.I / 8);
+  const int grid = items < sms ? static_cast<int>(items) : sms;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kFewThreads);
   cfg.dynamicSmemBytes = a.stages * static_cast<size_t>(a.slot_bytes) + red;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, layer_kernel(group, i4_mode(a.T < a.entry_max ? a.T : a.entry_max)), a);
 }
 
 cudaError_t prepare_few_kernels() {
+  const cudaError_t r = cudaFuncSetAttribute(few_router_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kRtSmemMax);
+  if (r != cudaSuccess) return r;
   for (int group : {0, 32, 64, 128})
     for (int modes : {1, 2, 3}) {
       const cudaError_t e = cudaFuncSetAttribute(layer_kernel(group, modes),

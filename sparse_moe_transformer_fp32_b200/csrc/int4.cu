@@ -179,13 +179,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   __shared__ __align__(8) uint64_t red_full[kFewRed], red_empty[kFewRed];
   __shared__ __align__(8) uint64_t recv_full[kLinRecv], recv_free[kLinMaxCluster][kLinRecv];
   __shared__ int abort_sh;
+  __shared__ __align__(16) uint8_t zeros_sh[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t C = a.cluster, rank = C > 1 ? cluster_rank() : 0;
   const uint32_t ring = smem_u32(smem);
   const uint32_t red = ring + a.stages * a.slot_bytes;
   const uint32_t recv = red + kFewRed * kFewWarps * kRedBytes;
   [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kRedBytes +
-                         (a.cluster > 1 ? a.recv * a.cluster * kRedBytes : 0) + (threadIdx.x >> 5) * kI4SplitBytes;
+                         (a.cluster > 1 ? a.recv * a.cluster * kRedBytes : 0) + (threadIdx.x >> 5) * a.stage_bytes;
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       for (int r = 0; r < kLinMaxCluster; ++r) mbar_init(smem_u32(&recv_free[r][i]), 1);
     }
     abort_sh = 0;
+    *reinterpret_cast<uint4*>(zeros_sh) = make_uint4(0u, 0u, 0u, 0u);
     fence_mbarrier_init();
   }
   pdl_launch();
@@ -228,11 +230,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     pdl_wait();
     const __nv_bfloat16* x0 = a.x + static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit;
     auto row = [&](int t) { return x0 + static_cast<size_t>(t) * a.K; };
-    [[maybe_unused]] TokenRow src;
+    [[maybe_unused]] TokenSource src;
     if constexpr (MODE == 4)
       i4_load_tokens16<kUnits * 4>(b, row, a.T, units, lane);
     else
-      i4_load_tokens<MODE>(b, factor, src, row, a.T, units, split, lane);
+      i4_load_tokens<MODE>(b, factor, src, row, a.T, units, split, zeros_sh, lane);
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
     bool ok = true;
@@ -493,12 +495,13 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   }
   if (!best) return cudaErrorInvalidConfiguration;
   a.cluster = best;
+  const int per = (units + best - 1) / best;
+  a.stage_bytes = mode == 4 ? 0 : stage_bytes((per + kFewWarps - 1) / kFewWarps * kI4Unit, true);
   a.recv = kLinRecvBytes / (best * 512 * lin_sets(mode));
   if (a.recv > kLinRecv) a.recv = kLinRecv;
   const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * lin_sets(mode) +
                       (best > 1 ? static_cast<size_t>(a.recv) * best * 512 * lin_sets(mode) : 0) +
-                      static_cast<size_t>(kFewWarps) * kI4SplitBytes;
-  const int per = (units + best - 1) / best;
+                      static_cast<size_t>(kFewWarps) * a.stage_bytes;
   // a whole tile to a slot where it fits
   const KSplit ks = make_ksplit(per, kI4SlotBytes, unit_bytes);
   a.cw = ks.cw;
