@@ -9,13 +9,13 @@
 //
 //  - one persistent CTA per SM: a producer warp moves weights into a shared-memory ring of
 //    about 190 KB with bulk copies (4 us of one SM's share of the HBM bandwidth in flight, so
-//    synchronisation between phases does not stop the stream), 8 consumer warps multiply, one
-//    warp finishes outputs;
+//    synchronisation between phases does not stop the stream), 8 consumer warps multiply, three
+//    finish outputs;
 //  - a tile is 16 weight rows by the whole K range of the CTA; the 8 consumer warps split K.
 //    Each keeps its K slice of the token rows in registers, as B fragments of
 //    mma.sync.m16n8k16 (weights are the 16-row A operand, tokens the 8 columns), for as long as
 //    the CTA stays with the same tokens, so that shared memory carries weights only;
-//  - the 16 partial tiles go through a small shared-memory buffer to the finishing warp, which
+//  - the 16 partial tiles go through a small shared-memory buffer to a finishing warp, which
 //    adds them in warp order (results do not depend on timing).
 //
 // tcgen05 is not used here: its smallest tile is 128 weight rows by 8 tokens with both operands
@@ -31,8 +31,8 @@ constexpr int kFewCols = 8;           // tokens of one entry (an expert's produc
 constexpr int kFewMaxK = 8192;        // K of one tile: 8 warps x 1024 elements (128 B registers)
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;  // (token, expert) slots = most entries
 constexpr int kFewWarps = 8;          // consumer warps
-// Consumers, then a warp group of producer, two finishing warps and one that only keeps it whole:
-// register budgets are given per warp group.  Launched with 168 registers a thread; while the roles run,
+// Consumers, then a warp group of the producer and three finishing warps: register budgets are given
+// per warp group.  Launched with 168 registers a thread; while the roles run,
 // consumers hold 216 and the others 72 (256 * 216 + 128 * 72 = 384 * 168).
 constexpr int kFewThreads = (kFewWarps + 4) * 32;
 constexpr int kFewRegsLaunch = 168, kFewRegsConsumer = 216, kFewRegsOther = 72;
@@ -222,6 +222,15 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
   bool ok = mbar_test_wait(bar, parity);
   if (!ok) ok = mbar_wait_slow(bar, parity, abort_flag, limit_ns, status, where);
   return __all_sync(0xffffffffu, ok);
+}
+
+// The same, where `seen` is an earlier mbar_test_wait of the phase by each lane.  A test takes about 100
+// clocks to answer; asked before the work that precedes the wait, it costs none.
+__device__ __forceinline__ bool mbar_wait_seen(bool seen, uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, uint64_t limit_ns,
+                                               uint32_t* status, uint32_t where) {
+  if (__all_sync(0xffffffffu, seen)) return true;
+  return mbar_wait_warp(bar, parity, abort_flag, limit_ns, status, where);
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {

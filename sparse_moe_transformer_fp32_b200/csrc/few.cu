@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
     };
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
-    bool ok = true;
+    bool ok = true, seen = false;  // seen: the current slot's phase
     // Phase -1 is the selection, with the loading of all tokens if they stay; as a turn of the same
     // loop so that there is one copy of the loading code.
 #pragma unroll 1
@@ -416,13 +416,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           continue;
         }
         float4 part = make_float4(0.f, 0.f, 0.f, 0.f);  // rows g, g of two tokens, then g + 8
+        const bool red_seen = mbar_test_wait(smem_u32(&sh.red_empty[rb]), rpar);
         // every warp passes every chunk in order: a phase may only be waited for by who has seen
         // the slot's phase before
 #pragma unroll 1
         for (int ch = 0; ch < chunks; ++ch) {
-          ok = mbar_wait_warp(smem_u32(&sh.full_bar[slot]), par, abort_flag, a.wait_limit_ns, a.status,
+          ok = mbar_wait_seen(seen, smem_u32(&sh.full_bar[slot]), par, abort_flag, a.wait_limit_ns, a.status,
                               kWhereFew + 2);
           if (!ok) break;
+          const int next = slot + 1 == a.stages ? 0 : slot + 1;
+          if (next == 0) par ^= 1;
+          seen = mbar_test_wait(smem_u32(&sh.full_bar[next]), par);
           if (ch == mine) {
             const uint32_t base = ring + slot * a.slot_bytes + off;
             if constexpr (kI4) {
@@ -445,13 +449,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.empty_bar[slot]));
-          if (++slot == a.stages) {
-            slot = 0;
-            par ^= 1;
-          }
+          slot = next;
         }
         if (!ok) break;
-        ok = mbar_wait_warp(smem_u32(&sh.red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
+        ok = mbar_wait_seen(red_seen, smem_u32(&sh.red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
                             kWhereFew + 3);
         if (!ok) break;
         if (units > 0)
@@ -537,21 +538,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
         mbar_wait_bounded(smem_u32(&sh.full_bar[i % a.stages]), (i / a.stages) & 1, &never,
                           2000000000ull, nullptr, 0);
     }
-  } else if (warp <= kFewWarps + 2) {
-    // ---- finishing warps, tiles in turn
+  } else {
+    // ---- finishing warps, tiles in turn: at most as many as there are buffers, so that who waits for a
+    // buffer has seen its phase before (or a later tile's)
+    constexpr int kFinishers = kRed < 3 ? kRed : 3;
+    const bool idle = warp > kFewWarps + kFinishers;
     const int g = lane >> 2, c = lane & 3;
     int rb = 0;
-    uint32_t rpar = 0, turn = warp - kFewWarps - 1;
+    uint32_t rpar = 0;
+    int turn = warp - kFewWarps - 1;  // tiles until this warp's next
     bool ok = true;
 #pragma unroll 1
-    for (int ph = 0; ph < 2 && ok; ++ph) {
+    for (int ph = 0; ph < 2 && ok && !idle; ++ph) {
       const KSplit ks = ph ? a.k2 : a.k1;
       const int per = ph ? n_dn : n_gu;
       const int first = ph ? i2 : i1, last = ph ? j2 : j1;
       const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
       int entry = first / per, tile = first % per;
 #pragma unroll 1
-      for (int it = first; it < last; ++it, turn ^= 1) {
+      for (int it = first; it < last; ++it, --turn) {
         if (turn) {
           if (++rb == kRed) {
             rb = 0;
@@ -563,12 +568,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           }
           continue;
         }
+        turn = kFinishers;
         ok = mbar_wait_warp(smem_u32(&sh.red_full[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
                             kWhereFew + 4);
         if (!ok) break;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int w = 0; w < active; ++w) {
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+          if (w >= active) break;
           const uint4 p = lds128(red + (rb * kFewWarps + w) * 512 + lane * 16);
           v.x += __uint_as_float(p.x);
           v.y += __uint_as_float(p.y);

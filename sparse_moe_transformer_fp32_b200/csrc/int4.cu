@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const Int4QuantArgs 
 constexpr int kLinRecv = 8;             // receive buffers for a tile's partial results, at most
 constexpr int kLinRecvBytes = 16384;    // all of them
 constexpr int kLinMaxCluster = 8;
+constexpr int kLinSlotBytes = 46080;  // ring slot: a tile of K = 5120, any group
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -238,14 +239,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
     bool ok = true;
+    bool seen = false;  // of the current slot's phase
     for (int tile = tile0; tile < tile1; ++tile) {
       float4 part[kSets];
+      const bool red_seen = mbar_test_wait(smem_u32(&red_empty[rb]), rpar);
       // every warp passes every chunk in order: a phase may only be waited for by who has seen the
       // slot's phase before
 #pragma unroll 1
       for (int ch = 0; ch < chunks; ++ch) {
-        ok = mbar_wait_warp(smem_u32(&full_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
+        ok = mbar_wait_seen(seen, smem_u32(&full_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
         if (!ok) break;
+        const int next = slot + 1 == a.stages ? 0 : slot + 1;
+        if (next == 0) par ^= 1;
+        seen = mbar_test_wait(smem_u32(&full_bar[next]), par);
         if (ch == mine) {
           const uint32_t base = ring + slot * a.slot_bytes + off;
           if constexpr (MODE == 4) {
@@ -261,13 +267,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&empty_bar[slot]));
-        if (++slot == a.stages) {
-          slot = 0;
-          par ^= 1;
-        }
+        slot = next;
       }
       if (!ok) break;
-      if (!mbar_wait_warp(smem_u32(&red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0)) break;
+      if (!mbar_wait_seen(red_seen, smem_u32(&red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0))
+        break;
       if (units > 0) {
 #pragma unroll
         for (int i = 0; i < kSets; ++i)
@@ -315,17 +319,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         mbar_wait_bounded(smem_u32(&full_bar[i % a.stages]), (i / a.stages) & 1, &never,
                           2000000000ull, nullptr, 0);
     }
-  } else if (warp == kFewWarps + 1 || (warp == kFewWarps + 2 && C > 1)) {
-    // ---- finishing warps: the first adds the consumers' partial tiles, and stores the result of a
-    // tile that is whole (C = 1) or sends it to the tile's owner; the second adds what an owner got
+  } else {
+    // ---- finishing warps (one alone took 0.7 us a tile).  Three in turn add the consumers' partial
+    // tiles and store the result of a tile that is whole (C = 1); or two in turn add them and send them
+    // to the tile's owner, and the third adds what an owner got
     const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
     const int g = lane >> 2, c = lane & 3;
-    const bool receiver = warp == kFewWarps + 2;
-    int rb = 0;
-    uint32_t rpar = 0;
+    const bool receiver = warp == kFewWarps + 3 && C > 1;
+    const int finishers = C > 1 ? 2 : 3, mine = warp - kFewWarps - 1;
     bool ok = true;
     pdl_wait();
-    for (int i = receiver ? rank : 0; i < tile1 - tile0; i += receiver ? C : 1) {
+    for (int i = receiver ? rank : mine; i < tile1 - tile0; i += receiver ? C : finishers) {
       float4 v[kSets];  // rows g, g of tokens 2 c, 2 c + 1, then rows g + 8
 #pragma unroll
       for (int s = 0; s < kSets; ++s) v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -345,20 +349,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
           if (lane < static_cast<int>(C)) remote_arrive(map_rank(smem_u32(&recv_free[rank][slot]), lane));
         }
       } else {
-        if (ok) ok = mbar_wait_warp(smem_u32(&red_full[rb]), rpar, abort_flag, a.wait_limit_ns, nullptr, 0);
+        const int rb = i % kFewRed;
+        if (ok)
+          ok = mbar_wait_warp(smem_u32(&red_full[rb]), (i / kFewRed) & 1, abort_flag, a.wait_limit_ns,
+                              nullptr, 0);
         if (ok) {
-#pragma unroll 4
-          for (int w = 0; w < active; ++w) {
+#pragma unroll
+          for (int w = 0; w < kFewWarps; ++w) {
+            if (w >= active) break;
 #pragma unroll
             for (int s = 0; s < kSets; ++s)
               v[s] = add4(v[s], lds_f4(red + (rb * kFewWarps + w) * kRedBytes + s * 512 + lane * 16));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&red_empty[rb]));
-          if (++rb == kFewRed) {
-            rb = 0;
-            rpar ^= 1;
-          }
         }
         if (C > 1) {
           if (ok && use > 0)
@@ -502,8 +506,8 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * lin_sets(mode) +
                       (best > 1 ? static_cast<size_t>(a.recv) * best * 512 * lin_sets(mode) : 0) +
                       static_cast<size_t>(kFewWarps) * a.stage_bytes;
-  // a whole tile to a slot where it fits
-  const KSplit ks = make_ksplit(per, kI4SlotBytes, unit_bytes);
+  // a whole tile to a slot where four of them fit
+  const KSplit ks = make_ksplit(per, kLinSlotBytes, unit_bytes);
   a.cw = ks.cw;
   a.slot_bytes = chunk_bytes(ks, unit_bytes);
   a.stages = static_cast<int>((kLinDynamicSmem - rest) / a.slot_bytes);
