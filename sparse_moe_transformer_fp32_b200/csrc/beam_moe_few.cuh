@@ -465,40 +465,41 @@ __host__ __device__ constexpr int i4_mode_runs(int mode) { return mode == 1 ? 32
 
 __host__ __device__ constexpr int i4_mode(int tokens) { return tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3; }
 
-// E of a K slice from its largest magnitude's FP32 bits, and 2^(21 - E) as two normal factors.
+// E of a K slice from its largest magnitude's FP32 bits, at least -105 (2^(21 - E) has to be a normal
+// number; smaller tokens keep an absolute accuracy of 2^-127), and 2^(21 - E).
 struct I4Scale {
   int E;
-  float f1, f2;
+  float f;
 };
 __device__ __forceinline__ I4Scale i4_scale(uint32_t top) {
-  I4Scale s;
-  s.E = max(static_cast<int>(top >> 23), 1) - 127;
-  const int e1 = (21 - s.E) / 2, e2 = 21 - s.E - e1;
-  s.f1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
-  s.f2 = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-  return s;
+  const int E = max(static_cast<int>(top >> 23) - 127, -105);
+  return {E, __uint_as_float(static_cast<uint32_t>(127 + 21 - E) << 23)};
+}
+// Digits of 4 elements (two words of BF16 pairs), a byte each: d[p] holds digit p.  The addition of
+// 1.5 2^23 rounds x 2^(21 - E) to an integer i, and leaves it in the low bits; the bytes of i +
+// 0x808080 are the balanced digits plus 128.
+__device__ __forceinline__ void i4_digits(uint32_t (&d)[3], uint32_t w0, uint32_t w1, float f) {
+  uint32_t x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = j < 2 ? w0 : w1;
+    x[j] = __float_as_uint(fmaf((j & 1) ? bf16_hi(u) : bf16_lo(u), f, kI4SumStartF)) + 0x00408080u;
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const uint32_t at = 0x0040u + 0x0011u * (2 - p);  // byte 2 - p of both
+    d[p] = __byte_perm(__byte_perm(x[0], x[1], at), __byte_perm(x[2], x[3], at), 0x5410) ^ 0x80808080u;
+  }
 }
 // Splits a staged slice (n elements, a multiple of 128) into its digits, n bytes each.
-__device__ __forceinline__ void i4_split(const uint8_t* raw, uint8_t* digits, int n, const I4Scale& s,
-                                         int lane) {
+__device__ __forceinline__ void i4_split(const uint8_t* raw, uint8_t* digits, int n, float f, int lane) {
 #pragma unroll 1
   for (int k = lane * 4; k < n; k += 128) {
     const uint2 w = *reinterpret_cast<const uint2*>(raw + k * 2);
-    uint32_t x[3][4];
+    uint32_t d[3];
+    i4_digits(d, w.x, w.y, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t u = j < 2 ? w.x : w.y;
-      const float f = (j & 1) ? bf16_hi(u) : bf16_lo(u);
-      // rounded to an integer by the addition of 1.5 2^23
-      const uint32_t i = __float_as_uint(fmaf(f * s.f1, s.f2, kI4SumStartF)) - kI4SumStart;
-      x[2][j] = i;
-      x[1][j] = static_cast<uint32_t>(static_cast<int>(i + 128) >> 8);
-      x[0][j] = static_cast<uint32_t>(static_cast<int>(x[1][j] + 128) >> 8);
-    }
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint32_t*>(digits + p * n + k) =
-          __byte_perm(__byte_perm(x[p][0], x[p][1], 0x0040), __byte_perm(x[p][2], x[p][3], 0x0040), 0x5410);
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t*>(digits + p * n + k) = d[p];
   }
 }
 
@@ -514,9 +515,30 @@ __device__ __forceinline__ I4Factor i4_factor(int E) {
           __uint_as_float(static_cast<uint32_t>(127 + r - r / 2) << 23)};
 }
 
+// Returns when all rows are written: fetch_row and settle without staging.
+template <class Row>
+__device__ __forceinline__ void await_rows(TokenSource& src, Row row, int tokens, int n, int lane) {
+#pragma unroll 1
+  for (int t = 0; t < tokens; ++t) {
+    uint4 v[kRowLoads];
+    const __nv_bfloat16* from = row(t);
+    fetch_row(v, from, n, lane);
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i) {
+      const int k = (i * 32 + lane) * 8;
+      if (k < n) src.settle(v[i], from + k);
+    }
+  }
+  __syncwarp();
+}
+
 // B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
-// row(t): the slice's first element of token t, or null.  factor[h]: of the token of the lane's
-// result column h.
+// row(t): the slice's first element of token t, or (MODE 1) null.  factor[h]: of the token of the
+// lane's result column h.
+//
+// MODE 1 splits a token at a time with the whole warp, through shared memory: a lane's share of the
+// work is 1/32 of the slice, and the code is short.  With more tokens each lane converts the elements
+// of its own column's token, in the registers that take the digits.
 template <int MODE, int REGS, class Row>
 __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&factor)[2], TokenSource& src,
                                                Row row, int tokens, int units, uint8_t* raw,
@@ -524,45 +546,86 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
   constexpr int kRuns = i4_mode_runs(MODE);
   static_assert(kRuns * 2 * MODE <= REGS, "the fragments must fit");
   const int g = lane >> 2, c = lane & 3, n = units * kI4Unit;
-  uint8_t* const digits = raw + 2 * n;
-  const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of result column 0
   int E[2] = {0, 0};
-  uint4 v[kRowLoads];
-  const __nv_bfloat16* next = row(0);
-  fetch_row(v, next, n, lane);
-#pragma unroll 1
-  for (int t = 0; t < tokens; ++t) {
-    const __nv_bfloat16* from = next;
-    uint32_t top = 0;
-    if (from != nullptr) top = stage_row(v, src, from, n, raw, lane);
-    top = __reduce_max_sync(0xffffffffu, top);
-    next = t + 1 < tokens ? row(t + 1) : nullptr;
+  if constexpr (MODE == 1) {
+    uint8_t* const digits = raw + 2 * n;
+    uint4 v[kRowLoads];
+    const __nv_bfloat16* next = row(0);
     fetch_row(v, next, n, lane);
-    const I4Scale s = i4_scale(top);
-    if (from != nullptr) i4_split(raw, digits, n, s, lane);
-    __syncwarp();
-    const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
-    if (t == first) E[0] = e;
-    if (t == first + 1) E[1] = e;
-#pragma unroll
-    for (int nt = 0; nt < MODE; ++nt) {
-      const int token = MODE == 1 ? (g & 1) : MODE == 2 ? (g & 3) : g;
-      const int digit = MODE == 1 ? (g >> 1) : MODE == 2 ? (nt ? 2 + (g >> 2) : (g >> 2)) : nt;
-      const bool mine = token == t && digit < 3 && from != nullptr;
+#pragma unroll 1
+    for (int t = 0; t < tokens; ++t) {
+      const __nv_bfloat16* from = next;
+      uint32_t top = 0;
+      if (from != nullptr) top = stage_row(v, src, from, n, raw, lane);
+      top = __reduce_max_sync(0xffffffffu, top);
+      next = t + 1 < tokens ? row(t + 1) : nullptr;
+      fetch_row(v, next, n, lane);
+      const I4Scale s = i4_scale(top);
+      if (from != nullptr) i4_split(raw, digits, n, s.f, lane);
+      __syncwarp();
+      const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
+      E[0] = t == 0 ? e : E[0];
+      E[1] = t == 1 ? e : E[1];
+      const bool mine = (g & 1) == t && g < 6 && from != nullptr;
       if (mine || t == 0) {  // the first token also clears the other columns
-        const uint8_t* p = mine ? digits + digit * n + c * 8 : zeros;
+        const uint8_t* p = mine ? digits + (g >> 1) * n + c * 8 : zeros;
         const int step = mine ? 32 : 0;
 #pragma unroll
         for (int j = 0; j < kRuns; ++j) {
           if (j < units * 4) {
             const uint2 w = *reinterpret_cast<const uint2*>(p + j * step);
-            b[(j * MODE + nt) * 2] = w.x;
-            b[(j * MODE + nt) * 2 + 1] = w.y;
+            b[j * 2] = w.x;
+            b[j * 2 + 1] = w.y;
           }
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
+  } else {
+    if (src.polled) await_rows(src, row, tokens, n, lane);
+    const int t = MODE == 2 ? (g & 3) : g;
+    const __nv_bfloat16* p = t < tokens ? row(t) + c * 8 : nullptr;
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (p != nullptr && j < units * 4) v = ld_relaxed(p + j * 32);
+      b[j * 2 * MODE] = v.x;
+      b[j * 2 * MODE + 1] = v.y;
+      b[j * 2 * MODE + 2] = v.z;
+      b[j * 2 * MODE + 3] = v.w;
+    }
+    uint32_t w = 0;  // magnitudes, two at a time
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w = __vmaxu2(w, b[j * 2 * MODE + i] & 0x7fff7fffu);
+    uint32_t top = max(w << 16, w & 0xffff0000u);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const I4Scale s = i4_scale(top);
+    const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
+    // result column h of lane column c: token 2 (c % 2) + h or 2 c + h, in lane 4 token
+    const int first = MODE == 2 ? 2 * (c & 1) : 2 * c;
+    E[0] = __shfl_sync(0xffffffffu, e, first * 4);
+    E[1] = __shfl_sync(0xffffffffu, e, first * 4 + 4);
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {
+      uint32_t lo[3], hi[3];
+      i4_digits(lo, b[j * 2 * MODE], b[j * 2 * MODE + 1], s.f);
+      i4_digits(hi, b[j * 2 * MODE + 2], b[j * 2 * MODE + 3], s.f);
+      if constexpr (MODE == 2) {
+        b[j * 4] = g < 4 ? lo[0] : lo[1];
+        b[j * 4 + 1] = g < 4 ? hi[0] : hi[1];
+        b[j * 4 + 2] = g < 4 ? lo[2] : 0u;
+        b[j * 4 + 3] = g < 4 ? hi[2] : 0u;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          b[j * 6 + q * 2] = lo[q];
+          b[j * 6 + q * 2 + 1] = hi[q];
+        }
+      }
+    }
   }
   factor[0] = i4_factor(E[0]);
   factor[1] = i4_factor(E[1]);
