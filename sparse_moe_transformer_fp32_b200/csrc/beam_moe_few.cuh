@@ -38,15 +38,16 @@ constexpr int kFewThreads = (kFewWarps + 4) * 32;
 constexpr int kFewRegsLaunch = 168, kFewRegsConsumer = 216, kFewRegsOther = 72;
 static_assert(kFewWarps == 8 && kFewWarps * kFewRegsConsumer + 4 * kFewRegsOther ==
                                     (kFewWarps + 4) * kFewRegsLaunch, "register budgets must add up");
-// Ring slot, 4-bit weights: a tile of K = 2560 (any group), half a tile of K = 5120.  A slot takes its
-// consumption and a round trip to HBM (about 2 us) to be ready again, so there have to be eight.
-constexpr int kI4SlotBytes = 23040;
+// Ring slot, 4-bit weights, at most: two tiles of K = 2560 or halves of two of K = 5120, any group.  A
+// warp's waits, hand-over and branches take about 1100 clocks a slot, its products 400 clocks a tile of
+// K = 2560, and a tile of that size arrives every 900: with one tile to a slot a layer of one token took
+// 46.7 us and one of 8 tokens 268, with two 41.6 and 212 (d = 5120, I = 2560, 64 experts, 8 chosen).
+constexpr int kI4SlotBytes = 46080;
 // Ring slot, BF16 weights: 16 rows x (2560 + 64) bytes.  Each row of a slot is a bulk copy, and one
 // SM starts a copy about every 39 ns whatever its size: segments of 640, 1280 and 2560 bytes
 // stream at 2.4, 4.8 and 7.4 TB/s over the GPU.
 constexpr int kBf16SlotBytes = 41984;
-constexpr int kFewRed = 4;            // partial-tile buffers, at most
-constexpr int kBf16Red = 2;           // with BF16 weights, whose tiles take four times as long
+constexpr int kFewRed = 2;            // buffers of partial tiles, each with a finishing warp
 constexpr int kFewMaxStages = 16;
 constexpr int kFewSmemMax = 232448;   // 227 KB
 constexpr int kBf16Unit = 32;         // K elements of the smallest BF16 slice of a warp
@@ -638,60 +639,85 @@ struct I4Acc {
   float v[MODE][4] = {};
 };
 
-// acc += 16 rows of 4-bit weights (`base`: the warp's first superblock) times the token digits, over
-// UNITS superblocks.  Each group is summed unscaled; its
-// scale multiplies the sum in FP32.
-template <int MODE, int GROUP, int UNITS, int REGS>
-__device__ __forceinline__ void i4_slice_of(I4Acc<MODE>& acc, const uint32_t (&b)[REGS], uint32_t base,
-                                            int lane) {
+// (a0, a1) += s * ((d0, d1) - kI4SumStartF), each rounded as by single instructions
+__device__ __forceinline__ void i4_scale2(float& a0, float& a1, float s, int d0, int d1) {
+  constexpr float kNeg = -kI4SumStartF;
+  asm("{\n\t.reg .b64 a, s, d, n;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 d, {%3, %4};\n\tmov.b64 n, {%5, %5};\n\t"
+      "add.rn.f32x2 d, d, n;\n\tfma.rn.f32x2 a, s, d, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(s), "r"(d0), "r"(d1), "f"(kNeg));
+}
+
+// acc[r] += 16 rows of 4-bit weights (`base` + r * apart: the warp's first superblock of tile r) times the
+// token digits, over UNITS superblocks.  Each group is summed unscaled; its scale multiplies the sum in
+// FP32.
+template <int MODE, int GROUP, int UNITS, int R, int REGS>
+__device__ __forceinline__ void i4_slice_of(I4Acc<MODE> (&acc)[R], const uint32_t (&b)[REGS], uint32_t base,
+                                            uint32_t apart, int lane) {
   constexpr int kUnitBytes = i4_unit_bytes(GROUP);
   constexpr uint32_t kMask = 0xf0f0f0f0u;
-  const uint32_t codes = base + lane * 16, scales = base + 1024 + (lane >> 2) * 4;
-  int d[MODE][4];
-  uint4 q;
+  uint32_t codes[R], scales[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    codes[r] = base + r * apart + lane * 16;
+    scales[r] = base + r * apart + 1024 + (lane >> 2) * 4;
+  }
+  int d[R][MODE][4];
+  uint4 q[R];
 #pragma unroll
   for (int j = 0; j < UNITS * 4; ++j) {  // runs of 32
     const int u = j / 4, run = j % 4;
-    if (run % 2 == 0) q = lds128(codes + u * kUnitBytes + (run / 2) * 512);
-    const uint32_t lo = run % 2 ? q.z : q.x, hi = run % 2 ? q.w : q.y;
-    const uint32_t a0 = lo & kMask, a1 = (lo << 4) & kMask, a2 = hi & kMask, a3 = (hi << 4) & kMask;
     constexpr int kRunsPerGroup = GROUP / 32;
     const bool first = j % kRunsPerGroup == 0, last = j % kRunsPerGroup == kRunsPerGroup - 1;
+    if (run % 2 == 0) {
 #pragma unroll
-    for (int nt = 0; nt < MODE; ++nt) {
-      const uint32_t b0 = b[(j * MODE + nt) * 2], b1 = b[(j * MODE + nt) * 2 + 1];
-      if (first)
-        mma_s8_first(d[nt], a0, a1, a2, a3, b0, b1, kI4SumStart);
-      else
-        mma_s8(d[nt], a0, a1, a2, a3, b0, b1);
+      for (int r = 0; r < R; ++r) q[r] = lds128(codes[r] + u * kUnitBytes + (run / 2) * 512);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t lo = run % 2 ? q[r].z : q[r].x, hi = run % 2 ? q[r].w : q[r].y;
+      const uint32_t a0 = lo & kMask, a1 = (lo << 4) & kMask, a2 = hi & kMask, a3 = (hi << 4) & kMask;
+#pragma unroll
+      for (int nt = 0; nt < MODE; ++nt) {
+        const uint32_t b0 = b[(j * MODE + nt) * 2], b1 = b[(j * MODE + nt) * 2 + 1];
+        if (first)
+          mma_s8_first(d[r][nt], a0, a1, a2, a3, b0, b1, kI4SumStart);
+        else
+          mma_s8(d[r][nt], a0, a1, a2, a3, b0, b1);
+      }
     }
     if (last) {
-      const uint32_t s = lds32(scales + u * kUnitBytes + (run / kRunsPerGroup) * 32);
-      const float sc[2] = {bf16_lo(s), bf16_hi(s)};
 #pragma unroll
-      for (int nt = 0; nt < MODE; ++nt)
+      for (int r = 0; r < R; ++r) {
+        const uint32_t s = lds32(scales[r] + u * kUnitBytes + (run / kRunsPerGroup) * 32);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc.v[nt][i] = fmaf(sc[i >> 1], __int_as_float(d[nt][i]) - kI4SumStartF, acc.v[nt][i]);
+        for (int nt = 0; nt < MODE; ++nt) {
+          float* v = acc[r].v[nt];
+          const int* e = d[r][nt];
+          i4_scale2(v[0], v[1], bf16_lo(s), e[0], e[1]);
+          i4_scale2(v[2], v[3], bf16_hi(s), e[2], e[3]);
+        }
+      }
     }
   }
 }
 
 // One straight run of code for each number of superblocks: with a branch after every superblock
 // the loads and products of two of them do not overlap (a fifth slower).
-template <int GROUP, int MODE, int REGS>
-__device__ __forceinline__ void i4_slice(I4Acc<MODE>& acc, const uint32_t (&b)[REGS], uint32_t base,
-                                         int units, int lane) {
+template <int GROUP, int MODE, int R, int REGS>
+__device__ __forceinline__ void i4_slice(I4Acc<MODE> (&acc)[R], const uint32_t (&b)[REGS], uint32_t base,
+                                         uint32_t apart, int units, int lane) {
   constexpr int kMax = i4_mode_runs(MODE) / 4;
   switch (units) {
-    case 1: i4_slice_of<MODE, GROUP, 1>(acc, b, base, lane); break;
-    case 2: i4_slice_of<MODE, GROUP, 2>(acc, b, base, lane); break;
-    case 3: i4_slice_of<MODE, GROUP, 3>(acc, b, base, lane); break;
-    case 4: i4_slice_of<MODE, GROUP, 4>(acc, b, base, lane); break;
-    case 5: if constexpr (kMax >= 5) i4_slice_of<MODE, GROUP, 5>(acc, b, base, lane); break;
-    case 6: if constexpr (kMax >= 6) i4_slice_of<MODE, GROUP, 6>(acc, b, base, lane); break;
-    case 7: if constexpr (kMax >= 7) i4_slice_of<MODE, GROUP, 7>(acc, b, base, lane); break;
-    case 8: if constexpr (kMax >= 8) i4_slice_of<MODE, GROUP, 8>(acc, b, base, lane); break;
+    case 1: i4_slice_of<MODE, GROUP, 1>(acc, b, base, apart, lane); break;
+    case 2: i4_slice_of<MODE, GROUP, 2>(acc, b, base, apart, lane); break;
+    case 3: i4_slice_of<MODE, GROUP, 3>(acc, b, base, apart, lane); break;
+    case 4: i4_slice_of<MODE, GROUP, 4>(acc, b, base, apart, lane); break;
+    case 5: if constexpr (kMax >= 5) i4_slice_of<MODE, GROUP, 5>(acc, b, base, apart, lane); break;
+    case 6: if constexpr (kMax >= 6) i4_slice_of<MODE, GROUP, 6>(acc, b, base, apart, lane); break;
+    case 7: if constexpr (kMax >= 7) i4_slice_of<MODE, GROUP, 7>(acc, b, base, apart, lane); break;
+    case 8: if constexpr (kMax >= 8) i4_slice_of<MODE, GROUP, 8>(acc, b, base, apart, lane); break;
     default: break;
   }
 }

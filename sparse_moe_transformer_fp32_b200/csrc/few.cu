@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
   constexpr int kUnit = kI4 ? kI4Unit : kBf16Unit;                       // K elements
   constexpr int kUnitBytes = kI4 ? i4_unit_bytes(kI4 ? GROUP : 128) : 0;  // packed bytes
   constexpr int kRuns = kFewMaxK / kFewWarps / 32;                       // runs of 32 per warp
-  constexpr int kRed = kI4 ? kFewRed : kBf16Red;
+  constexpr int kStep = kI4 ? 2 : 1;  // tiles of one step, which share a ring slot, waits and hand-over
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       mbar_init(smem_u32(&sh.full_bar[i]), 1);
       mbar_init(smem_u32(&sh.empty_bar[i]), kFewWarps);
     }
-    for (int i = 0; i < kRed; ++i) {
+    for (int i = 0; i < kFewRed; ++i) {
       mbar_init(smem_u32(&sh.red_full[i]), kFewWarps);
       mbar_init(smem_u32(&sh.red_empty[i]), 1);
     }
@@ -351,13 +351,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
     j2 = __shfl_sync(0xffffffffu, v, 3);
   };
 
+  // tiles of the next step, of one entry
+  auto step_len = [](int left, int of_entry) {
+    const int n = left < of_entry ? left : of_entry;
+    return n < kStep ? n : kStep;
+  };
+
   if (warp < kFewWarps) {
     more_registers<kFewRegsConsumer>();
     // ---- consumers
     // token fragments: BF16 4 registers a run of 32; INT8 digits 2, 4 or 6 (4 and 6: up to 20 runs)
     uint32_t b[!kI4 ? 128 : MODES == 1 ? 64 : MODES == 2 ? 80 : 120];
     [[maybe_unused]] I4Factor factor[2];
-    uint8_t* const raw = smem + a.stages * a.slot_bytes + kRed * kFewWarps * 512 + warp * a.stage_bytes;
+    uint8_t* const raw = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kStep * 512 + warp * a.stage_bytes;
     int n_tok = 0;
     auto load = [&](int ph, int entry) {  // entry < 0: all tokens
       const KSplit ks = ph ? a.k2 : a.k1;
@@ -399,8 +405,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       const uint32_t off = kI4 ? uoff * kUnitBytes : uoff * 64;
       const int stride = bf16_row_stride(cunits);
       int entry = first / per, tile = first % per, loaded = -1;
+      int len = 1;
 #pragma unroll 1
-      for (int it = first; it < last; ++it) {
+      for (int it = first; it < last; it += len) {
         if (ph < 0 ? by_token : entry != loaded && !(ph == 0 && by_token)) {
           loaded = entry;
           ok = load(ph > 0 ? 1 : 0, ph < 0 ? -1 : entry);
@@ -415,8 +422,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           cut();
           continue;
         }
-        float4 part = make_float4(0.f, 0.f, 0.f, 0.f);  // rows g, g of two tokens, then g + 8
-        const bool red_seen = mbar_test_wait(smem_u32(&sh.red_empty[rb]), rpar);
+        len = step_len(last - it, per - tile);
+        float4 part[kStep] = {};  // of each tile: rows g, g of two tokens, then g + 8
+        bool red_seen = false;
+        if (!kI4) red_seen = mbar_test_wait(smem_u32(&sh.red_empty[rb]), rpar);
         // every warp passes every chunk in order: a phase may only be waited for by who has seen
         // the slot's phase before
 #pragma unroll 1
@@ -426,14 +435,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           if (!ok) break;
           const int next = slot + 1 == a.stages ? 0 : slot + 1;
           if (next == 0) par ^= 1;
-          seen = mbar_test_wait(smem_u32(&sh.full_bar[next]), par);
+          // 4-bit weights: the tests of barriers come after the slice's loads from shared memory, which
+          // wait for the answer of a test ahead of them.
+          auto test = [&] {
+            seen = mbar_test_wait(smem_u32(&sh.full_bar[next]), par);
+            if (kI4 && ch + 1 == chunks) red_seen = mbar_test_wait(smem_u32(&sh.red_empty[rb]), rpar);
+          };
+          if (!kI4 || ch != mine) test();
           if (ch == mine) {
             const uint32_t base = ring + slot * a.slot_bytes + off;
             if constexpr (kI4) {
               constexpr std::integral_constant<int, kI4 ? GROUP : 128> kG{};
-              auto product = [&](auto acc) {
-                i4_slice<kG.value>(acc, b, base, units, lane);
-                part = i4_result(acc, factor, lane);
+              // Both tiles are multiplied even where the step has one: the second is then what the slot
+              // held before, and its sums are not stored.
+              auto product = [&](auto acc0) {
+                decltype(acc0) acc[2] = {};
+                i4_slice<kG.value>(acc, b, base, cunits * kUnitBytes, units, lane);
+                test();
+#pragma unroll
+                for (int r = 0; r < kStep; ++r) part[r] = i4_result(acc[r], factor, lane);
               };
               if (MODES == 1 || n_tok <= 2)
                 product(I4Acc<1>{});
@@ -444,7 +464,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
             } else {
               float acc[4] = {};
               bf16_slice<kRuns>(acc, b, base, stride, units, lane);
-              part = make_float4(acc[0], acc[1], acc[2], acc[3]);
+              part[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
             }
           }
           __syncwarp();
@@ -455,15 +475,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
         ok = mbar_wait_seen(red_seen, smem_u32(&sh.red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
                             kWhereFew + 3);
         if (!ok) break;
-        if (units > 0)
-          sts128(red + (rb * kFewWarps + warp) * 512 + lane * 16, part);
+        if (units > 0) {
+#pragma unroll
+          for (int r = 0; r < kStep; ++r)
+            sts128(red + ((rb * kFewWarps + warp) * kStep + r) * 512 + lane * 16, part[r]);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.red_full[rb]));
-        if (++rb == kRed) {
+        if (++rb == kFewRed) {
           rb = 0;
           rpar ^= 1;
         }
-        if (++tile == per) {
+        if ((tile += len) == per) {
           tile = 0;
           ++entry;
         }
@@ -490,8 +513,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       const KSplit ks = ph ? a.k2 : a.k1;
       const int per = ph ? n_dn : n_gu, K = ph ? a.I : a.d;
       int entry = (ph ? i2 : i1) / per, tile = (ph ? i2 : i1) % per;
+      const int last = ph ? j2 : j1;
+      int len;
 #pragma unroll 1
-      for (int it = ph ? i2 : i1; it < (ph ? j2 : j1) && ok; ++it) {
+      for (int it = ph ? i2 : i1; it < last && ok; it += len) {
+        len = step_len(last - it, per - tile);
         const int e = sh.entry_e[entry];
         const uint8_t* src;
         if (kI4) {
@@ -511,11 +537,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           const int s = ks.start(w), n = ks.start(w + ks.cw) - s;
           const uint32_t bar = smem_u32(&sh.full_bar[slot]);
           const uint32_t dst = ring + slot * a.slot_bytes;
-          if (lane == 0) mbar_arrive_expect_tx(bar, kI4 ? n * kUnitBytes : 16 * n * 64);
+          if (lane == 0) mbar_arrive_expect_tx(bar, kI4 ? len * n * kUnitBytes : 16 * n * 64);
           __syncwarp();
           if (kI4) {
-            if (lane == 0)
-              bulk_load(dst, src + static_cast<size_t>(s) * kUnitBytes, n * kUnitBytes, bar);
+            if (lane < len)  // lane r copies the chunk of tile r
+              bulk_load(dst + lane * n * kUnitBytes, src + static_cast<size_t>(lane * ks.n + s) * kUnitBytes,
+                        n * kUnitBytes, bar);
           } else if (lane < 16 && n > 0) {
             bulk_load(dst + lane * bf16_row_stride(n), src + static_cast<size_t>(s) * 64, n * 64, bar);
           }
@@ -525,7 +552,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
             par ^= 1;
           }
         }
-        if (++tile == per) {
+        if ((tile += len) == per) {
           tile = 0;
           ++entry;
         }
@@ -539,14 +566,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
                           2000000000ull, nullptr, 0);
     }
   } else {
-    // ---- finishing warps, tiles in turn: at most as many as there are buffers, so that who waits for a
-    // buffer has seen its phase before (or a later tile's)
-    constexpr int kFinishers = kRed < 3 ? kRed : 3;
-    const bool idle = warp > kFewWarps + kFinishers;
+    // ---- finishing warps, steps in turn: no more warps than buffers, so that who waits for a buffer
+    // has seen its phase before (or a later step's)
+    const int mine = warp - kFewWarps - 1;
+    const bool idle = mine >= kFewRed;
     const int g = lane >> 2, c = lane & 3;
     int rb = 0;
     uint32_t rpar = 0;
-    int turn = warp - kFewWarps - 1;  // tiles until this warp's next
     bool ok = true;
 #pragma unroll 1
     for (int ph = 0; ph < 2 && ok && !idle; ++ph) {
@@ -554,57 +580,55 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       const int per = ph ? n_dn : n_gu;
       const int first = ph ? i2 : i1, last = ph ? j2 : j1;
       const int active = ks.n < kFewWarps ? ks.n : kFewWarps;
-      int entry = first / per, tile = first % per;
+      int entry = first / per, tile = first % per, len;
 #pragma unroll 1
-      for (int it = first; it < last; ++it, --turn) {
-        if (turn) {
-          if (++rb == kRed) {
-            rb = 0;
-            rpar ^= 1;
-          }
-          if (++tile == per) {
-            tile = 0;
-            ++entry;
-          }
-          continue;
-        }
-        turn = kFinishers;
-        ok = mbar_wait_warp(smem_u32(&sh.red_full[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
-                            kWhereFew + 4);
-        if (!ok) break;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int it = first; it < last; it += len) {
+        len = step_len(last - it, per - tile);
+        if (rb == mine) {  // a buffer to each finishing warp
+          ok = mbar_wait_warp(smem_u32(&sh.red_full[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
+                              kWhereFew + 4);
+          if (!ok) break;
+          float4 v[kStep] = {};
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-          if (w >= active) break;
-          const uint4 p = lds128(red + (rb * kFewWarps + w) * 512 + lane * 16);
-          v.x += __uint_as_float(p.x);
-          v.y += __uint_as_float(p.y);
-          v.z += __uint_as_float(p.z);
-          v.w += __uint_as_float(p.w);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.red_empty[rb]));
-        if (++rb == kRed) {
-          rb = 0;
-          rpar ^= 1;
-        }
-        const int n = sh.entry_n[entry];
-        const float lo[2] = {v.x, v.y}, hi[2] = {v.z, v.w};
+          for (int w = 0; w < kFewWarps; ++w) {
+            if (w >= active) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = c * 2 + h;
-          if (col < n && sh.entry_slot[entry][col] != kNoSlot) {
-            const size_t s = sh.entry_slot[entry][col];
-            if (ph == 0) {
-              st_relaxed16(a.act + s * a.I + tile * 8 + g, __float2bfloat16_rn(swiglu(lo[h], hi[h])));
-            } else {
-              float* y = a.y + s * a.d + tile * 16 + g;
-              st_relaxed32(y, lo[h]);
-              st_relaxed32(y + 8, hi[h]);
+            for (int r = 0; r < kStep; ++r) {
+              const float4 p = lds_f4(red + ((rb * kFewWarps + w) * kStep + r) * 512 + lane * 16);
+              v[r].x += p.x;
+              v[r].y += p.y;
+              v[r].z += p.z;
+              v[r].w += p.w;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.red_empty[rb]));
+          const int n = sh.entry_n[entry];
+#pragma unroll
+          for (int r = 0; r < kStep; ++r) {
+            if (r >= len) break;
+            const float lo[2] = {v[r].x, v[r].y}, hi[2] = {v[r].z, v[r].w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int col = c * 2 + h;
+              if (col < n && sh.entry_slot[entry][col] != kNoSlot) {
+                const size_t s = sh.entry_slot[entry][col];
+                if (ph == 0) {
+                  st_relaxed16(a.act + s * a.I + (tile + r) * 8 + g, __float2bfloat16_rn(swiglu(lo[h], hi[h])));
+                } else {
+                  float* y = a.y + s * a.d + (tile + r) * 16 + g;
+                  st_relaxed32(y, lo[h]);
+                  st_relaxed32(y + 8, hi[h]);
+                }
+              }
             }
           }
         }
-        if (++tile == per) {
+        if (++rb == kFewRed) {
+          rb = 0;
+          rpar ^= 1;
+        }
+        if ((tile += len) == per) {
           tile = 0;
           ++entry;
         }
@@ -684,12 +708,14 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
   // the digits of 3 to 8 tokens fit in a warp's registers up to K = 5120, those of 2 up to 8192
   a.entry_max = group && (a.d > 5120 || a.I > 5120) ? 2 : kFewCols;
-  a.slot_bytes = group ? kI4SlotBytes : kBf16SlotBytes;
-  a.k1 = make_ksplit(a.d / unit, a.slot_bytes, unit_bytes);
-  a.k2 = make_ksplit(a.I / unit, a.slot_bytes, unit_bytes);
+  const int step = group ? 2 : 1;  // tiles
+  a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
+  a.k2 = make_ksplit(a.I / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
+  const int c1 = chunk_bytes(a.k1, step * unit_bytes), c2 = chunk_bytes(a.k2, step * unit_bytes);
+  a.slot_bytes = c1 > c2 ? c1 : c2;
   const int most = (a.d > a.I ? a.d : a.I) / unit;  // of a warp's K slice
   a.stage_bytes = stage_bytes((most + kFewWarps - 1) / kFewWarps * unit, group != 0);
-  const size_t red = static_cast<size_t>(group ? kFewRed : kBf16Red) * kFewWarps * 512 +
+  const size_t red = static_cast<size_t>(kFewRed) * kFewWarps * step * 512 +
                      static_cast<size_t>(kFewWarps) * a.stage_bytes;
   a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);
   if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;

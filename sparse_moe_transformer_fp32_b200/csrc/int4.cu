@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const Int4QuantArgs 
 constexpr int kLinRecv = 8;             // receive buffers for a tile's partial results, at most
 constexpr int kLinRecvBytes = 16384;    // all of them
 constexpr int kLinMaxCluster = 8;
+constexpr int kLinRed = 4;          // buffers of partial tiles
 constexpr int kLinSlotBytes = 46080;  // ring slot: a tile of K = 5120, any group
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   constexpr int kRedBytes = 512 * kSets;   // one partial tile
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[kFewMaxStages], empty_bar[kFewMaxStages];
-  __shared__ __align__(8) uint64_t red_full[kFewRed], red_empty[kFewRed];
+  __shared__ __align__(8) uint64_t red_full[kLinRed], red_empty[kLinRed];
   __shared__ __align__(8) uint64_t recv_full[kLinRecv], recv_free[kLinMaxCluster][kLinRecv];
   __shared__ int abort_sh;
   __shared__ __align__(16) uint8_t zeros_sh[16];
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   const uint32_t C = a.cluster, rank = C > 1 ? cluster_rank() : 0;
   const uint32_t ring = smem_u32(smem);
   const uint32_t red = ring + a.stages * a.slot_bytes;
-  const uint32_t recv = red + kFewRed * kFewWarps * kRedBytes;
-  [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kRedBytes +
+  const uint32_t recv = red + kLinRed * kFewWarps * kRedBytes;
+  [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kLinRed * kFewWarps * kRedBytes +
                          (a.cluster > 1 ? a.recv * a.cluster * kRedBytes : 0) + (threadIdx.x >> 5) * a.stage_bytes;
   volatile int* abort_flag = &abort_sh;
 
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       mbar_init(smem_u32(&full_bar[i]), 1);
       mbar_init(smem_u32(&empty_bar[i]), kFewWarps);
     }
-    for (int i = 0; i < kFewRed; ++i) {
+    for (int i = 0; i < kLinRed; ++i) {
       mbar_init(smem_u32(&red_full[i]), kFewWarps);
       mbar_init(smem_u32(&red_empty[i]), 1);
     }
@@ -260,9 +261,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
 #pragma unroll
             for (int i = 0; i < 2; ++i) part[i] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
           } else {
-            I4Acc<MODE> acc;
-            i4_slice<GROUP>(acc, b, base, units, lane);
-            part[0] = i4_result(acc, factor, lane);
+            I4Acc<MODE> acc[1] = {};
+            i4_slice<GROUP>(acc, b, base, 0, units, lane);
+            part[0] = i4_result(acc[0], factor, lane);
           }
         }
         __syncwarp();
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&red_full[rb]));
-      if (++rb == kFewRed) {
+      if (++rb == kLinRed) {
         rb = 0;
         rpar ^= 1;
       }
@@ -349,9 +350,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
           if (lane < static_cast<int>(C)) remote_arrive(map_rank(smem_u32(&recv_free[rank][slot]), lane));
         }
       } else {
-        const int rb = i % kFewRed;
+        const int rb = i % kLinRed;
         if (ok)
-          ok = mbar_wait_warp(smem_u32(&red_full[rb]), (i / kFewRed) & 1, abort_flag, a.wait_limit_ns,
+          ok = mbar_wait_warp(smem_u32(&red_full[rb]), (i / kLinRed) & 1, abort_flag, a.wait_limit_ns,
                               nullptr, 0);
         if (ok) {
 #pragma unroll
@@ -503,7 +504,7 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   a.stage_bytes = mode == 4 ? 0 : stage_bytes((per + kFewWarps - 1) / kFewWarps * kI4Unit, true);
   a.recv = kLinRecvBytes / (best * 512 * lin_sets(mode));
   if (a.recv > kLinRecv) a.recv = kLinRecv;
-  const size_t rest = static_cast<size_t>(kFewRed) * kFewWarps * 512 * lin_sets(mode) +
+  const size_t rest = static_cast<size_t>(kLinRed) * kFewWarps * 512 * lin_sets(mode) +
                       (best > 1 ? static_cast<size_t>(a.recv) * best * 512 * lin_sets(mode) : 0) +
                       static_cast<size_t>(kFewWarps) * a.stage_bytes;
   // a whole tile to a slot where four of them fit
