@@ -270,6 +270,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with D = A * B.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // D (16 x 8, INT32) += A (16 x 32, INT8) * B (32 x 8, INT8).
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                        uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -463,6 +472,7 @@ constexpr int kI4NonFinite = 1 << 20;           // in the place of an exponent
 
 // Runs of 32 of a warp's K slice at most: 64, 80 or 120 registers of fragments.
 __host__ __device__ constexpr int i4_mode_runs(int mode) { return mode == 1 ? 32 : 20; }
+__host__ __device__ constexpr int i4_mode_regs(int mode) { return i4_mode_runs(mode) * 2 * mode; }
 
 __host__ __device__ constexpr int i4_mode(int tokens) { return tokens <= 2 ? 1 : tokens <= 4 ? 2 : 3; }
 
@@ -516,30 +526,14 @@ __device__ __forceinline__ I4Factor i4_factor(int E) {
           __uint_as_float(static_cast<uint32_t>(127 + r - r / 2) << 23)};
 }
 
-// Returns when all rows are written: fetch_row and settle without staging.
-template <class Row>
-__device__ __forceinline__ void await_rows(TokenSource& src, Row row, int tokens, int n, int lane) {
-#pragma unroll 1
-  for (int t = 0; t < tokens; ++t) {
-    uint4 v[kRowLoads];
-    const __nv_bfloat16* from = row(t);
-    fetch_row(v, from, n, lane);
-#pragma unroll
-    for (int i = 0; i < kRowLoads; ++i) {
-      const int k = (i * 32 + lane) * 8;
-      if (k < n) src.settle(v[i], from + k);
-    }
-  }
-  __syncwarp();
-}
-
 // B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
-// row(t): the slice's first element of token t, or (MODE 1) null.  factor[h]: of the token of the
-// lane's result column h.
+// row(t): the slice's first element of token t, or null.  factor[h]: of the token of the lane's result
+// column h.
 //
-// MODE 1 splits a token at a time with the whole warp, through shared memory: a lane's share of the
-// work is 1/32 of the slice, and the code is short.  With more tokens each lane converts the elements
-// of its own column's token, in the registers that take the digits.
+// MODE 1 and 2 split a token at a time with the whole warp, through shared memory: a lane's share of the
+// work is 1/32 of the slice, the code is short, and few registers are held beside the fragments.  At 8
+// tokens that takes 13 us: with MODE 3 each lane converts the elements of its own column's token, in the
+// registers that take the digits.
 template <int MODE, int REGS, class Row>
 __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&factor)[2], TokenSource& src,
                                                Row row, int tokens, int units, uint8_t* raw,
@@ -547,49 +541,54 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
   constexpr int kRuns = i4_mode_runs(MODE);
   static_assert(kRuns * 2 * MODE <= REGS, "the fragments must fit");
   const int g = lane >> 2, c = lane & 3, n = units * kI4Unit;
+  const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of the lane's result column 0
   int E[2] = {0, 0};
-  if constexpr (MODE == 1) {
-    uint8_t* const digits = raw + 2 * n;
-    uint4 v[kRowLoads];
-    const __nv_bfloat16* next = row(0);
-    fetch_row(v, next, n, lane);
+  if constexpr (MODE < 3) {
+  uint8_t* const digits = raw + 2 * n;
+  const int token = MODE == 1 ? (g < 6 ? g & 1 : -1) : g & 3;  // of B column g
+  uint4 v[kRowLoads];
+  const __nv_bfloat16* next = row(0);
+  fetch_row(v, next, n, lane);
 #pragma unroll 1
-    for (int t = 0; t < tokens; ++t) {
-      const __nv_bfloat16* from = next;
-      uint32_t top = 0;
-      if (from != nullptr) top = stage_row(v, src, from, n, raw, lane);
-      top = __reduce_max_sync(0xffffffffu, top);
-      next = t + 1 < tokens ? row(t + 1) : nullptr;
-      fetch_row(v, next, n, lane);
-      const I4Scale s = i4_scale(top);
-      if (from != nullptr) i4_split(raw, digits, n, s.f, lane);
-      __syncwarp();
-      const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
-      E[0] = t == 0 ? e : E[0];
-      E[1] = t == 1 ? e : E[1];
-      const bool mine = (g & 1) == t && g < 6 && from != nullptr;
-      if (mine || t == 0) {  // the first token also clears the other columns
-        const uint8_t* p = mine ? digits + (g >> 1) * n + c * 8 : zeros;
-        const int step = mine ? 32 : 0;
+  for (int t = 0; t < tokens; ++t) {
+    const __nv_bfloat16* from = next;
+    uint32_t top = 0;
+    if (from != nullptr) top = stage_row(v, src, from, n, raw, lane);
+    top = __reduce_max_sync(0xffffffffu, top);
+    next = t + 1 < tokens ? row(t + 1) : nullptr;
+    fetch_row(v, next, n, lane);
+    const I4Scale s = i4_scale(top);
+    if (from != nullptr) i4_split(raw, digits, n, s.f, lane);
+    __syncwarp();
+    const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
+    E[0] = t == first ? e : E[0];
+    E[1] = t == first + 1 ? e : E[1];
+    const bool mine = token == t && from != nullptr;
+    if (mine || t == 0) {  // the first token also clears the other columns
+#pragma unroll
+      for (int q = 0; q < MODE; ++q) {
+        const int digit = MODE == 1 ? g >> 1 : q == 0 ? g >> 2 : 2;  // of column g in MMA q
+        const bool any = mine && (q == 0 || g < 4);
+        const uint8_t* p = any ? digits + digit * n + c * 8 : zeros;
+        const int step = any ? 32 : 0;
 #pragma unroll
         for (int j = 0; j < kRuns; ++j) {
           if (j < units * 4) {
             const uint2 w = *reinterpret_cast<const uint2*>(p + j * step);
-            b[j * 2] = w.x;
-            b[j * 2 + 1] = w.y;
+            b[(j * MODE + q) * 2] = w.x;
+            b[(j * MODE + q) * 2 + 1] = w.y;
           }
         }
       }
-      __syncwarp();
     }
+    __syncwarp();
+  }
   } else {
-    if (src.polled) await_rows(src, row, tokens, n, lane);
-    const int t = MODE == 2 ? (g & 3) : g;
-    const __nv_bfloat16* p = t < tokens ? row(t) + c * 8 : nullptr;
+    const __nv_bfloat16* p = g < tokens ? row(g) + c * 8 : nullptr;
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (p != nullptr && j < units * 4) v = ld_relaxed(p + j * 32);
+      if (p != nullptr && j < units * 4) v = __ldcg(reinterpret_cast<const uint4*>(p + j * 32));
       b[j * 2 * MODE] = v.x;
       b[j * 2 * MODE + 1] = v.y;
       b[j * 2 * MODE + 2] = v.z;
@@ -605,8 +604,6 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const I4Scale s = i4_scale(top);
     const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
-    // result column h of lane column c: token 2 (c % 2) + h or 2 c + h, in lane 4 token
-    const int first = MODE == 2 ? 2 * (c & 1) : 2 * c;
     E[0] = __shfl_sync(0xffffffffu, e, first * 4);
     E[1] = __shfl_sync(0xffffffffu, e, first * 4 + 4);
 #pragma unroll
@@ -614,17 +611,10 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
       uint32_t lo[3], hi[3];
       i4_digits(lo, b[j * 2 * MODE], b[j * 2 * MODE + 1], s.f);
       i4_digits(hi, b[j * 2 * MODE + 2], b[j * 2 * MODE + 3], s.f);
-      if constexpr (MODE == 2) {
-        b[j * 4] = g < 4 ? lo[0] : lo[1];
-        b[j * 4 + 1] = g < 4 ? hi[0] : hi[1];
-        b[j * 4 + 2] = g < 4 ? lo[2] : 0u;
-        b[j * 4 + 3] = g < 4 ? hi[2] : 0u;
-      } else {
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          b[j * 6 + q * 2] = lo[q];
-          b[j * 6 + q * 2 + 1] = hi[q];
-        }
+      for (int q = 0; q < 3; ++q) {
+        b[j * 6 + q * 2] = lo[q];
+        b[j * 6 + q * 2 + 1] = hi[q];
       }
     }
   }
@@ -779,52 +769,66 @@ __device__ __forceinline__ void i4_load_tokens16(uint32_t (&b)[RUNS * 8], Row ro
   }
 }
 
-template <int GROUP, int UNITS, int REGS>
-__device__ __forceinline__ void i4_slice16_of(float (&acc)[2][4], const uint32_t (&b)[REGS], uint32_t base,
-                                              int lane) {
+template <int GROUP, int UNITS, int R, int REGS>
+__device__ __forceinline__ void i4_slice16_of(float (&acc)[R][2][4], const uint32_t (&b)[REGS], uint32_t base,
+                                              uint32_t apart, int lane) {
   constexpr int kUnitBytes = i4_unit_bytes(GROUP);
-  const uint32_t codes = base + lane * 16, scales = base + 1024 + (lane >> 2) * 4;
-  float d[2][4];
-  uint4 q;
+  uint32_t codes[R], scales[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    codes[r] = base + r * apart + lane * 16;
+    scales[r] = base + r * apart + 1024 + (lane >> 2) * 4;
+  }
+  float d[R][2][4];
+  uint4 q[R];
 #pragma unroll
   for (int j = 0; j < UNITS * 4; ++j) {  // runs of 32
     const int u = j / 4, run = j % 4;
-    if (run % 2 == 0) q = lds128(codes + u * kUnitBytes + (run / 2) * 512);
     constexpr int kRunsPerGroup = GROUP / 32;
     const bool first = j % kRunsPerGroup == 0, last = j % kRunsPerGroup == kRunsPerGroup - 1;
+    if (run % 2 == 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w = run % 2 ? (h ? q.w : q.z) : (h ? q.y : q.x);
-      const uint32_t a0 = i4_pair(w >> 4), a1 = i4_pair(w), a2 = i4_pair(w >> 12), a3 = i4_pair(w >> 8);
+      for (int r = 0; r < R; ++r) q[r] = lds128(codes[r] + u * kUnitBytes + (run / 2) * 512);
+    }
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        if (first && h == 0) {
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[nt][i] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = run % 2 ? (h ? q[r].w : q[r].z) : (h ? q[r].y : q[r].x);
+        const uint32_t a0 = i4_pair(w >> 4), a1 = i4_pair(w), a2 = i4_pair(w >> 12), a3 = i4_pair(w >> 8);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const uint32_t b0 = b[(j * 2 + nt) * 4 + h * 2], b1 = b[(j * 2 + nt) * 4 + h * 2 + 1];
+          if (first && h == 0)
+            mma_bf16_first(d[r][nt], a0, a1, a2, a3, b0, b1);
+          else
+            mma_bf16(d[r][nt], a0, a1, a2, a3, b0, b1);
         }
-        mma_bf16(d[nt], a0, a1, a2, a3, b[(j * 2 + nt) * 4 + h * 2], b[(j * 2 + nt) * 4 + h * 2 + 1]);
       }
     }
     if (last) {
-      const uint32_t s = lds32(scales + u * kUnitBytes + (run / kRunsPerGroup) * 32);
-      const float sc[2] = {bf16_lo(s), bf16_hi(s)};
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int r = 0; r < R; ++r) {
+        const uint32_t s = lds32(scales[r] + u * kUnitBytes + (run / kRunsPerGroup) * 32);
+        const float sc[2] = {bf16_lo(s), bf16_hi(s)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][i] = fmaf(sc[i >> 1], d[nt][i], acc[nt][i]);
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][nt][i] = fmaf(sc[i >> 1], d[r][nt][i], acc[r][nt][i]);
+      }
     }
   }
 }
 
-template <int GROUP, int REGS>
-__device__ __forceinline__ void i4_slice16(float (&acc)[2][4], const uint32_t (&b)[REGS], uint32_t base,
-                                           int units, int lane) {
+template <int GROUP, int R, int REGS>
+__device__ __forceinline__ void i4_slice16(float (&acc)[R][2][4], const uint32_t (&b)[REGS], uint32_t base,
+                                           uint32_t apart, int units, int lane) {
   static_assert(REGS == 128, "four superblocks");
   switch (units) {
-    case 1: i4_slice16_of<GROUP, 1>(acc, b, base, lane); break;
-    case 2: i4_slice16_of<GROUP, 2>(acc, b, base, lane); break;
-    case 3: i4_slice16_of<GROUP, 3>(acc, b, base, lane); break;
-    case 4: i4_slice16_of<GROUP, 4>(acc, b, base, lane); break;
+    case 1: i4_slice16_of<GROUP, 1>(acc, b, base, apart, lane); break;
+    case 2: i4_slice16_of<GROUP, 2>(acc, b, base, apart, lane); break;
+    case 3: i4_slice16_of<GROUP, 3>(acc, b, base, apart, lane); break;
+    case 4: i4_slice16_of<GROUP, 4>(acc, b, base, apart, lane); break;
     default: break;
   }
 }

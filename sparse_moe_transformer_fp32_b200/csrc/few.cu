@@ -241,7 +241,7 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
   const int e = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kFewWarps * 32 == kMaxE, "a thread to an expert");
   uint32_t m = e < a.E ? sh.mask[e] : 0u;
-  const int shift = a.entry_max == 2 ? 1 : 3;
+  const int shift = 31 - __clz(a.entry_max);  // 2, 4 or 8
   const int need = by_token ? m != 0u : (__popc(m) + a.entry_max - 1) >> shift;
   int incl = need;
 #pragma unroll
@@ -283,8 +283,8 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
 // Each CTA takes one contiguous run of items of either phase, cut so that both runs together are
 // the same number of weight bytes for every CTA; its producer goes from the first into the second
 // without waiting for anything but ring space, so the weights keep streaming while activations
-// cross the GPU.  GROUP = 0: BF16 weights.  MODES: the largest i4_mode of an entry.  HBM-bound on the touched experts' bytes.
-template <int GROUP, int MODES>
+// cross the GPU.  GROUP = 0: BF16 weights.  MODE: see i4_mode (1 or 2; 0 for BF16).  HBM-bound on the touched experts' bytes.
+template <int GROUP, int MODE>
 __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLayerArgs a) {
   constexpr bool kI4 = GROUP != 0;
   constexpr int kUnit = kI4 ? kI4Unit : kBf16Unit;                       // K elements
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
   uint8_t* slot_of = smem + kSlotTable;
   // With few enough tokens the columns of every entry are the tokens: the fragments of gate|up are
   // loaded once, while other warps select.
-  const bool by_token = a.T <= (kI4 ? 2 : kFewCols);
+  const bool by_token = a.T <= a.entry_max;
   auto select = [&](int first, int step) {
     for (int t = first; t < a.T; t += step) few_select(a, sc + t * a.E, slot_of, sh, t, lane);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic accesses before bulk writes
@@ -360,32 +360,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
   if (warp < kFewWarps) {
     more_registers<kFewRegsConsumer>();
     // ---- consumers
-    // token fragments: BF16 4 registers a run of 32; INT8 digits 2, 4 or 6 (4 and 6: up to 20 runs)
-    uint32_t b[!kI4 ? 128 : MODES == 1 ? 64 : MODES == 2 ? 80 : 120];
+    // token fragments: BF16 4 registers a run of 32; INT8 digits 2 or 4 (4: up to 20 runs)
+    uint32_t b[kI4 ? i4_mode_regs(kI4 ? MODE : 1) : 128];
     [[maybe_unused]] I4Factor factor[2];
     uint8_t* const raw = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kStep * 512 + warp * a.stage_bytes;
-    int n_tok = 0;
     auto load = [&](int ph, int entry) {  // entry < 0: all tokens
-      const KSplit ks = ph ? a.k2 : a.k1;
-      const int K = ph ? a.I : a.d, units = ks.count(warp);
-      const __nv_bfloat16* from = (ph ? a.act : a.h) + ks.start(warp) * kUnit;
-      TokenSource src{ph != 0, abort_flag, a.wait_limit_ns, a.status, kWhereFew + 1};
+      const KSplit ks = ph > 0 ? a.k2 : a.k1;
+      const int K = ph > 0 ? a.I : a.d, units = ks.count(warp);
+      const __nv_bfloat16* from = (ph > 0 ? a.act : a.h) + ks.start(warp) * kUnit;
+      TokenSource src{ph > 0, abort_flag, a.wait_limit_ns, a.status, kWhereFew + 1};
       auto row = [&](int col) -> const __nv_bfloat16* {
         if (entry < 0) return from + static_cast<size_t>(col) * K;
         const int s = sh.entry_slot[entry][col];
-        return s == kNoSlot ? nullptr : from + static_cast<size_t>(ph ? s : s / a.k) * K;
+        return s == kNoSlot ? nullptr : from + static_cast<size_t>(ph > 0 ? s : s / a.k) * K;
       };
-      n_tok = entry < 0 ? a.T : sh.entry_n[entry];
-      if constexpr (kI4) {
-        if (MODES == 1 || n_tok <= 2)
-          i4_load_tokens<1>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
-        else if (MODES == 2 || n_tok <= 4)
-          i4_load_tokens<(MODES > 1 ? 2 : 1)>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
-        else
-          i4_load_tokens<MODES>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
-      } else {
+      const int n_tok = entry < 0 ? a.T : sh.entry_n[entry];
+      if constexpr (kI4)
+        i4_load_tokens<(kI4 ? MODE : 1)>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
+      else
         load_tokens<kRuns>(b, src, row, n_tok, units * kUnit, raw, sh.zeros, lane);
-      }
       return __all_sync(0xffffffffu, src.ok) != 0;
     };
     int slot = 0, rb = 0;
@@ -404,13 +397,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       const int uoff = ks.start(warp) - cstart;
       const uint32_t off = kI4 ? uoff * kUnitBytes : uoff * 64;
       const int stride = bf16_row_stride(cunits);
-      int entry = first / per, tile = first % per, loaded = -1;
-      int len = 1;
+      int entry = first / per, tile = first % per, loaded = -1, len = 1;
 #pragma unroll 1
       for (int it = first; it < last; it += len) {
         if (ph < 0 ? by_token : entry != loaded && !(ph == 0 && by_token)) {
           loaded = entry;
-          ok = load(ph > 0 ? 1 : 0, ph < 0 ? -1 : entry);
+          ok = load(ph, ph < 0 ? -1 : entry);
           if (!ok) break;
         }
         if (ph < 0) {
@@ -445,22 +437,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           if (ch == mine) {
             const uint32_t base = ring + slot * a.slot_bytes + off;
             if constexpr (kI4) {
-              constexpr std::integral_constant<int, kI4 ? GROUP : 128> kG{};
               // Both tiles are multiplied even where the step has one: the second is then what the slot
               // held before, and its sums are not stored.
-              auto product = [&](auto acc0) {
-                decltype(acc0) acc[2] = {};
-                i4_slice<kG.value>(acc, b, base, cunits * kUnitBytes, units, lane);
-                test();
+              I4Acc<(kI4 ? MODE : 1)> acc[kStep] = {};
+              i4_slice<(kI4 ? GROUP : 128)>(acc, b, base, cunits * kUnitBytes, units, lane);
+              test();
 #pragma unroll
-                for (int r = 0; r < kStep; ++r) part[r] = i4_result(acc[r], factor, lane);
-              };
-              if (MODES == 1 || n_tok <= 2)
-                product(I4Acc<1>{});
-              else if (MODES == 2 || n_tok <= 4)
-                product(I4Acc<(MODES > 1 ? 2 : 1)>{});
-              else
-                product(I4Acc<MODES>{});
+              for (int r = 0; r < kStep; ++r) part[r] = i4_result(acc[r], factor, lane);
             } else {
               float acc[4] = {};
               bf16_slice<kRuns>(acc, b, base, stride, units, lane);
@@ -674,15 +657,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
 
 using LayerKernel = void (*)(FewLayerArgs);
 template <int GROUP>
-LayerKernel layer_kernel_of(int modes) {
-  return modes == 1 ? few_layer_kernel<GROUP, 1> : modes == 2 ? few_layer_kernel<GROUP, 2>
-                                                              : few_layer_kernel<GROUP, 3>;
+LayerKernel layer_kernel_of(int mode) {
+  return mode == 1 ? few_layer_kernel<GROUP, 1> : few_layer_kernel<GROUP, 2>;
 }
-LayerKernel layer_kernel(int group, int modes) {
+LayerKernel layer_kernel(int group, int mode) {
   return group == 0    ? few_layer_kernel<0, 0>
-         : group == 32 ? layer_kernel_of<32>(modes)
-         : group == 64 ? layer_kernel_of<64>(modes)
-                       : layer_kernel_of<128>(modes);
+         : group == 32 ? layer_kernel_of<32>(mode)
+         : group == 64 ? layer_kernel_of<64>(mode)
+                       : layer_kernel_of<128>(mode);
 }
 
 constexpr size_t kFewDynamicSmem = kFewSmemMax - 4096;  // the rest: FewShared
@@ -706,8 +688,10 @@ int few_router_tokens(int d) { return (kRtSmemMax - kRtExperts * d * 4) / (d * 2
 
 cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
-  // the digits of 3 to 8 tokens fit in a warp's registers up to K = 5120, those of 2 up to 8192
-  a.entry_max = group && (a.d > 5120 || a.I > 5120) ? 2 : kFewCols;
+  // Tokens of an entry: with 4-bit weights 4 (2 alone, or where the digits of 4 do not fit in a warp's
+  // registers).  8 to an entry read the weights of an expert of 5 to 8 tokens once, but every product
+  // then takes three MMAs instead of two: 16 tokens over 64 experts 267 us, with 4 to an entry 249.
+  a.entry_max = !group ? kFewCols : a.T <= 2 || a.d > 5120 || a.I > 5120 ? 2 : 4;
   const int step = group ? 2 : 1;  // tiles
   a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
   a.k2 = make_ksplit(a.I / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
@@ -734,7 +718,7 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, layer_kernel(group, i4_mode(a.T < a.entry_max ? a.T : a.entry_max)), a);
+  return cudaLaunchKernelEx(&cfg, layer_kernel(group, i4_mode(a.entry_max)), a);
 }
 
 cudaError_t prepare_few_kernels() {
@@ -742,8 +726,8 @@ cudaError_t prepare_few_kernels() {
                                              kRtSmemMax);
   if (r != cudaSuccess) return r;
   for (int group : {0, 32, 64, 128})
-    for (int modes : {1, 2, 3}) {
-      const cudaError_t e = cudaFuncSetAttribute(layer_kernel(group, modes),
+    for (int mode : {1, 2}) {
+      const cudaError_t e = cudaFuncSetAttribute(layer_kernel(group, mode),
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(kFewDynamicSmem));
       if (e != cudaSuccess) return e;

@@ -98,7 +98,6 @@ __global__ void __launch_bounds__(256) int4_quantize_kernel(const Int4QuantArgs 
 constexpr int kLinRecv = 8;             // receive buffers for a tile's partial results, at most
 constexpr int kLinRecvBytes = 16384;    // all of them
 constexpr int kLinMaxCluster = 8;
-constexpr int kLinRed = 4;          // buffers of partial tiles
 constexpr int kLinSlotBytes = 46080;  // ring slot: a tile of K = 5120, any group
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -170,15 +169,25 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
 __host__ __device__ constexpr int lin_units(int mode) { return mode == 4 ? 4 : i4_mode_runs(mode) / 4; }
 __host__ __device__ constexpr int lin_sets(int mode) { return mode == 4 ? 2 : 1; }  // of 8 tokens
 
-template <int MODE, int GROUP>
+// Buffers of the partial tiles of a step: a finishing warp has to have seen a buffer's last phase, or a
+// later tile's, when it waits; three of them in turn, so that the tile before is two steps back at most.
+__host__ __device__ constexpr int lin_red(int step) { return 4 / step; }
+// Tiles of a CTA from which on a step is two tiles, for up to 4 tokens: half the waits, but twice the code
+// to fetch for a first tile (1 x 1280 x 2560 with one tile to a CTA: 3.4 us, with steps of two 3.7; 1 x 40960
+// x 5120 with 18: 20.3 and 20.0; 4 x 40960 x 5120: 25.1 and 23.8).  Beyond 4 tokens the products of a tile
+// take longer than the waits, and two at a time nothing off.
+constexpr int kLinStepTiles = 4;
+
+template <int MODE, int GROUP, int STEP>
 __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4LinearArgs a) {
   constexpr int kUnits = lin_units(MODE);
   constexpr int kSets = lin_sets(MODE);
   constexpr int kUnitBytes = i4_unit_bytes(GROUP);
   constexpr int kRedBytes = 512 * kSets;   // one partial tile
+  constexpr int kRed = lin_red(STEP);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[kFewMaxStages], empty_bar[kFewMaxStages];
-  __shared__ __align__(8) uint64_t red_full[kLinRed], red_empty[kLinRed];
+  __shared__ __align__(8) uint64_t red_full[kRed], red_empty[kRed];
   __shared__ __align__(8) uint64_t recv_full[kLinRecv], recv_free[kLinMaxCluster][kLinRecv];
   __shared__ int abort_sh;
   __shared__ __align__(16) uint8_t zeros_sh[16];
@@ -186,8 +195,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
   const uint32_t C = a.cluster, rank = C > 1 ? cluster_rank() : 0;
   const uint32_t ring = smem_u32(smem);
   const uint32_t red = ring + a.stages * a.slot_bytes;
-  const uint32_t recv = red + kLinRed * kFewWarps * kRedBytes;
-  [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kLinRed * kFewWarps * kRedBytes +
+  const uint32_t recv = red + kRed * kFewWarps * STEP * kRedBytes;
+  [[maybe_unused]] uint8_t* const split = smem + a.stages * a.slot_bytes + kRed * kFewWarps * STEP * kRedBytes +
                          (a.cluster > 1 ? a.recv * a.cluster * kRedBytes : 0) + (threadIdx.x >> 5) * a.stage_bytes;
   volatile int* abort_flag = &abort_sh;
 
@@ -196,9 +205,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
       mbar_init(smem_u32(&full_bar[i]), 1);
       mbar_init(smem_u32(&empty_bar[i]), kFewWarps);
     }
-    for (int i = 0; i < kLinRed; ++i) {
+    for (int i = 0; i < kRed; ++i) {
       mbar_init(smem_u32(&red_full[i]), kFewWarps);
-      mbar_init(smem_u32(&red_empty[i]), 1);
+      mbar_init(smem_u32(&red_empty[i]), STEP);
     }
     for (int i = 0; i < kLinRecv; ++i) {
       mbar_init(smem_u32(&recv_full[i]), 2);  // the receiver, and this CTA's own part
@@ -226,7 +235,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     more_registers<kFewRegsConsumer>();
     // ---- consumers
     const int units = ks.count(warp), mine = warp / ks.cw, chunks = ks.chunks();
-    const uint32_t off = (ks.start(warp) - ks.start(mine * ks.cw)) * kUnitBytes;
+    const int cstart = ks.start(mine * ks.cw);
+    const uint32_t off = (ks.start(warp) - cstart) * kUnitBytes;
+    const uint32_t apart = (ks.start((mine + 1) * ks.cw) - cstart) * kUnitBytes;  // tiles in a slot
     uint32_t b[kUnits * 8 * MODE];
     [[maybe_unused]] I4Factor factor[2];
     pdl_wait();
@@ -241,9 +252,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     uint32_t par = 0, rpar = 1;
     bool ok = true;
     bool seen = false;  // of the current slot's phase
-    for (int tile = tile0; tile < tile1; ++tile) {
-      float4 part[kSets];
-      const bool red_seen = mbar_test_wait(smem_u32(&red_empty[rb]), rpar);
+    for (int tile = tile0; tile < tile1; tile += STEP) {
+      float4 part[STEP * kSets] = {};
+      bool red_seen = false;
       // every warp passes every chunk in order: a phase may only be waited for by who has seen the
       // slot's phase before
 #pragma unroll 1
@@ -252,18 +263,32 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         if (!ok) break;
         const int next = slot + 1 == a.stages ? 0 : slot + 1;
         if (next == 0) par ^= 1;
-        seen = mbar_test_wait(smem_u32(&full_bar[next]), par);
+        // Steps of two tiles: the tests of barriers come after the slice's loads from shared memory, which
+        // wait for the answer of a test ahead of them.  With one tile that is 4 % slower.
+        auto test = [&] {
+          seen = mbar_test_wait(smem_u32(&full_bar[next]), par);
+          if (ch + 1 == chunks) red_seen = mbar_test_wait(smem_u32(&red_empty[rb]), rpar);
+        };
+        if (STEP == 1 || ch != mine) test();
         if (ch == mine) {
+          // Every tile of a step is multiplied even where the last step has fewer: the others are then
+          // what the slot held before, and their sums are not stored.
           const uint32_t base = ring + slot * a.slot_bytes + off;
           if constexpr (MODE == 4) {
-            float acc[2][4] = {};
-            i4_slice16<GROUP>(acc, b, base, units, lane);
+            float acc[STEP][2][4] = {};
+            i4_slice16<GROUP>(acc, b, base, apart, units, lane);
+            if (STEP > 1) test();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) part[i] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            for (int i = 0; i < STEP * 2; ++i) {
+              const float* v = acc[i / 2][i % 2];
+              part[i] = make_float4(v[0], v[1], v[2], v[3]);
+            }
           } else {
-            I4Acc<MODE> acc[1] = {};
-            i4_slice<GROUP>(acc, b, base, 0, units, lane);
-            part[0] = i4_result(acc[0], factor, lane);
+            I4Acc<MODE> acc[STEP] = {};
+            i4_slice<GROUP>(acc, b, base, apart, units, lane);
+            if (STEP > 1) test();
+#pragma unroll
+            for (int r = 0; r < STEP; ++r) part[r] = i4_result(acc[r], factor, lane);
           }
         }
         __syncwarp();
@@ -275,12 +300,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         break;
       if (units > 0) {
 #pragma unroll
-        for (int i = 0; i < kSets; ++i)
-          sts128(red + (rb * kFewWarps + warp) * kRedBytes + i * 512 + lane * 16, part[i]);
+        for (int i = 0; i < STEP * kSets; ++i)
+          sts128(red + (rb * kFewWarps + warp) * STEP * kRedBytes + i * 512 + lane * 16, part[i]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&red_full[rb]));
-      if (++rb == kLinRed) {
+      if (++rb == kRed) {
         rb = 0;
         rpar ^= 1;
       }
@@ -294,18 +319,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     int slot = 0;
     uint32_t par = 1, issued = 0;
     bool ok = true;
-    for (int tile = tile0; tile < tile1 && ok; ++tile) {
+    for (int tile = tile0; tile < tile1 && ok; tile += STEP) {
+      const int len = tile1 - tile < STEP ? tile1 - tile : STEP;
       const uint8_t* src = a.w + (static_cast<size_t>(tile) * units_all + u0) * kUnitBytes;
       for (int w = 0; w < kFewWarps; w += ks.cw) {
         ok = mbar_wait_warp(smem_u32(&empty_bar[slot]), par, abort_flag, a.wait_limit_ns, nullptr, 0);
         if (!ok) break;
-        if (lane == 0) {
-          const int s = ks.start(w), n = ks.start(w + ks.cw) - s;
-          const uint32_t bar = smem_u32(&full_bar[slot]);
-          mbar_arrive_expect_tx(bar, n * kUnitBytes);
-          bulk_load(ring + slot * a.slot_bytes, src + static_cast<size_t>(s) * kUnitBytes,
-                    n * kUnitBytes, bar);
-        }
+        const int s = ks.start(w), n = ks.start(w + ks.cw) - s;
+        const uint32_t bar = smem_u32(&full_bar[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, len * n * kUnitBytes);
+        __syncwarp();
+        if (lane < len)  // lane r copies the chunk of tile r
+          bulk_load(ring + slot * a.slot_bytes + lane * n * kUnitBytes,
+                    src + static_cast<size_t>(lane * units_all + s) * kUnitBytes, n * kUnitBytes, bar);
         ++issued;
         if (++slot == a.stages) {
           slot = 0;
@@ -350,9 +376,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
           if (lane < static_cast<int>(C)) remote_arrive(map_rank(smem_u32(&recv_free[rank][slot]), lane));
         }
       } else {
-        const int rb = i % kLinRed;
+        const int rb = i / STEP % kRed;
         if (ok)
-          ok = mbar_wait_warp(smem_u32(&red_full[rb]), (i / kLinRed) & 1, abort_flag, a.wait_limit_ns,
+          ok = mbar_wait_warp(smem_u32(&red_full[rb]), (i / (STEP * kRed)) & 1, abort_flag, a.wait_limit_ns,
                               nullptr, 0);
         if (ok) {
 #pragma unroll
@@ -360,7 +386,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
             if (w >= active) break;
 #pragma unroll
             for (int s = 0; s < kSets; ++s)
-              v[s] = add4(v[s], lds_f4(red + (rb * kFewWarps + w) * kRedBytes + s * 512 + lane * 16));
+              v[s] = add4(v[s], lds_f4(red + ((rb * kFewWarps + w) * STEP + i % STEP) * kRedBytes +
+                                         s * 512 + lane * 16));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&red_empty[rb]));
@@ -431,16 +458,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
 }
 
 using LinearKernel = void (*)(Int4LinearArgs);
-template <int MODE>
+template <int MODE, int STEP>
 LinearKernel linear_kernel_of(int group) {
-  return group == 32 ? int4_linear_kernel<MODE, 32> : group == 64 ? int4_linear_kernel<MODE, 64>
-                                                                  : int4_linear_kernel<MODE, 128>;
+  return group == 32   ? int4_linear_kernel<MODE, 32, STEP>
+         : group == 64 ? int4_linear_kernel<MODE, 64, STEP>
+                       : int4_linear_kernel<MODE, 128, STEP>;
 }
-LinearKernel linear_kernel(int mode, int group) {
-  return mode == 1   ? linear_kernel_of<1>(group)
-         : mode == 2 ? linear_kernel_of<2>(group)
-         : mode == 3 ? linear_kernel_of<3>(group)
-                     : linear_kernel_of<4>(group);
+LinearKernel linear_kernel(int mode, int group, int step) {
+  return mode == 1   ? (step == 2 ? linear_kernel_of<1, 2>(group) : linear_kernel_of<1, 1>(group))
+         : mode == 2 ? (step == 2 ? linear_kernel_of<2, 2>(group) : linear_kernel_of<2, 1>(group))
+         : mode == 3 ? linear_kernel_of<3, 1>(group)
+                     : linear_kernel_of<4, 1>(group);
 }
 
 // Co-resident clusters of C CTAs on this device, by log2 C (filled by prepare_int4_kernels; one
@@ -504,34 +532,35 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   a.stage_bytes = mode == 4 ? 0 : stage_bytes((per + kFewWarps - 1) / kFewWarps * kI4Unit, true);
   a.recv = kLinRecvBytes / (best * 512 * lin_sets(mode));
   if (a.recv > kLinRecv) a.recv = kLinRecv;
-  const size_t rest = static_cast<size_t>(kLinRed) * kFewWarps * 512 * lin_sets(mode) +
+  const int step = mode <= 2 && (a.tiles + best_clus - 1) / best_clus >= kLinStepTiles ? 2 : 1;
+  const size_t rest = static_cast<size_t>(lin_red(step)) * kFewWarps * step * 512 * lin_sets(mode) +
                       (best > 1 ? static_cast<size_t>(a.recv) * best * 512 * lin_sets(mode) : 0) +
                       static_cast<size_t>(kFewWarps) * a.stage_bytes;
-  // a whole tile to a slot where four of them fit
-  const KSplit ks = make_ksplit(per, kLinSlotBytes, unit_bytes);
+  const KSplit ks = make_ksplit(per, kLinSlotBytes, step * unit_bytes);
   a.cw = ks.cw;
-  a.slot_bytes = chunk_bytes(ks, unit_bytes);
+  a.slot_bytes = chunk_bytes(ks, step * unit_bytes);
   a.stages = static_cast<int>((kLinDynamicSmem - rest) / a.slot_bytes);
   if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg =
       linear_config(best * best_clus, a.stages * static_cast<size_t>(a.slot_bytes) + rest, s, best, attr);
-  return cudaLaunchKernelEx(&cfg, linear_kernel(mode, group), a);
+  return cudaLaunchKernelEx(&cfg, linear_kernel(mode, group, step), a);
 }
 
 cudaError_t prepare_int4_kernels() {
   for (int mode : {1, 2, 3, 4})
-    for (int group : {32, 64, 128}) {
-      const cudaError_t e = cudaFuncSetAttribute(linear_kernel(mode, group),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(kLinDynamicSmem));
-      if (e != cudaSuccess) return e;
-    }
+    for (int group : {32, 64, 128})
+      for (int step : {1, 2}) {
+        const cudaError_t e = cudaFuncSetAttribute(linear_kernel(mode, group, step),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kLinDynamicSmem));
+        if (e != cudaSuccess) return e;
+      }
   for (int lc = 1; lc < 4; ++lc) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = linear_config(1 << lc, kLinDynamicSmem, nullptr, 1 << lc, attr);
     int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, linear_kernel(1, 128), &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, linear_kernel(1, 128, 1), &cfg);
     if (e != cudaSuccess) return e;
     g_max_clusters[lc] = n;
   }
