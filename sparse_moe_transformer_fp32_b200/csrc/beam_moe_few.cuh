@@ -12,10 +12,12 @@
 //    synchronisation between phases does not stop the stream), 8 consumer warps multiply, three
 //    finish outputs;
 //  - a tile is 16 weight rows by the whole K range of the CTA; the 8 consumer warps split K.
-//    Each keeps its K slice of the token rows in registers, as B fragments of
-//    mma.sync.m16n8k16 (weights are the 16-row A operand, tokens the 8 columns), for as long as
-//    the CTA stays with the same tokens, so that shared memory carries weights only;
-//  - the 16 partial tiles go through a small shared-memory buffer to a finishing warp, which
+//    Each keeps its K slice of the token rows in registers, as B fragments of mma.sync (weights are
+//    the 16-row A operand, tokens the 8 columns), for as long as the CTA stays with the same
+//    tokens, so that shared memory carries weights only;
+//  - with 4-bit weights a step is two tiles where there are enough of them: waits, hand-over and
+//    branches cost a warp about as much as its products of a tile;
+//  - the 8 partial tiles go through a small shared-memory buffer to a finishing warp, which
 //    adds them in warp order (results do not depend on timing).
 //
 // tcgen05 is not used here: its smallest tile is 128 weight rows by 8 tokens with both operands
@@ -449,7 +451,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 // columns takes 22 clocks of an SM to arrive (528 bytes at 6.5 TB/s over the GPU), and expanding it
 // to BF16 for m16n8k16 measured 20 whatever the number of warps: 28 shifts and masks, 16
 // subtractions and 4 MMAs of 2 clocks.  As 8-bit operands the codes take 12 shifts and masks and 2
-// MMAs of 2 clocks for each 8 columns of tokens, 9 clocks in all.  (E4M3 MMAs would take the codes
+// MMAs of 4 clocks for each 8 columns of tokens, 9 clocks in all.  (E4M3 MMAs would take the codes
 // as they lie, but mma.sync expands E4M3 operands with ALU operations: 18.5 clocks.)
 //
 // The token is a 23-bit integer per element, in three signed 8-bit digits:
@@ -737,7 +739,8 @@ __device__ __forceinline__ float4 i4_result(const I4Acc<MODE>& acc, const I4Fact
   return make_float4(o[0], o[1], o[2], o[3]);
 }
 
-// ---- 9 to 16 tokens: BF16 MMAs, two sets of 8 columns
+// ---- 9 to 16 tokens: BF16 MMAs, two sets of 8 columns (six INT8 MMAs of 4 clocks a run are slower:
+// 16 x 40960 x 5120 in 55 us, with these 42)
 
 // Two codes (two's complement, bits 0..3 and 16..19 of v) as exact BF16: with the sign bit inverted
 // a code is q + 8, 0x4300 | (q + 8) is the BF16 value 136 + q.

@@ -132,6 +132,7 @@ __device__ __forceinline__ uint32_t score_key(float v) {
 constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..24
 
 constexpr uint8_t kNoSlot = 255;
+constexpr int kI4EntryMax = 4;  // tokens of an entry with 4-bit weights
 constexpr int kSlotTable = kFewMaxTokens * kMaxE * 8;  // offset in the ring, behind the scores
 
 struct FewShared {
@@ -283,7 +284,12 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
 // Each CTA takes one contiguous run of items of either phase, cut so that both runs together are
 // the same number of weight bytes for every CTA; its producer goes from the first into the second
 // without waiting for anything but ring space, so the weights keep streaming while activations
-// cross the GPU.  GROUP = 0: BF16 weights.  MODE: see i4_mode (1 or 2; 0 for BF16).  HBM-bound on the touched experts' bytes.
+// cross the GPU.  GROUP = 0: BF16 weights.  MODE: the arrangement of digits, 1 or 2 (0 for BF16).
+//
+// Bound by HBM, the bytes of the touched experts.  d = 5120, I = 2560, 64 experts, 8 chosen: BF16 1 token
+// 107 us and 16 tokens 680 (6.0 and 6.5 TB/s), 4-bit weights 8 tokens 167.  4-bit, 1 token, 41.6 us: 26 of
+// them the bytes, 6 the selection and the first copies, 4 the exchange of the activations (the ring holds
+// 4 us of weights, and the slowest CTA's last rows take that long to reach everyone), 4 the combine.
 template <int GROUP, int MODE>
 __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLayerArgs a) {
   constexpr bool kI4 = GROUP != 0;
@@ -669,10 +675,15 @@ LayerKernel layer_kernel(int group, int mode) {
 
 constexpr size_t kFewDynamicSmem = kFewSmemMax - 4096;  // the rest: FewShared
 static_assert(sizeof(FewShared) <= 4096, "FewShared must fit beside the ring");
-// the scores of 16 tokens fit in the ring
-static_assert(kFewMaxTokens * kMaxE * 9 <= 2 * kI4SlotBytes && kFewMaxTokens * kMaxE * 9 <= 2 * kBf16SlotBytes,
-              "scores and slots must fit in the ring");
-
+// Scores and slots lie in the ring while tokens are selected.  The smallest slot is two tiles of one
+// superblock (or one tile of four BF16 units), and there are kFewMaxStages of them.  Only the scores of
+// calls whose columns are not the tokens may reach into the partial-tile buffers behind: nothing uses
+// those before the selection is done.
+constexpr int kSmallestRing = kFewMaxStages * 2 * i4_unit_bytes(128);
+static_assert(16 * bf16_row_stride(4) >= 4 * i4_unit_bytes(128), "BF16 rings are twice as large at least");
+static_assert(kSlotTable + kI4EntryMax * kMaxE <= kSmallestRing && 2 * kSmallestRing > kSlotTable + kFewCols * kMaxE, "scores and slots must fit in the ring");
+static_assert(kFewMaxTokens * kMaxE * 9 <= kSmallestRing + kFewRed * kFewWarps * 512,
+              "scores and slots must fit in the ring and the partial-tile buffers");
 
 constexpr int kRtSmemMax = kFewSmemMax - 1024;
 
@@ -691,7 +702,7 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   // Tokens of an entry: with 4-bit weights 4 (2 alone, or where the digits of 4 do not fit in a warp's
   // registers).  8 to an entry read the weights of an expert of 5 to 8 tokens once, but every product
   // then takes three MMAs instead of two: 16 tokens over 64 experts 267 us, with 4 to an entry 249.
-  a.entry_max = !group ? kFewCols : a.T <= 2 || a.d > 5120 || a.I > 5120 ? 2 : 4;
+  a.entry_max = !group ? kFewCols : a.T <= 2 || a.d > 5120 || a.I > 5120 ? 2 : kI4EntryMax;
   const int step = group ? 2 : 1;  // tiles
   a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
   a.k2 = make_ksplit(a.I / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);

@@ -154,17 +154,22 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
   return __all_sync(0xffffffffu, ok);
 }
 
-// y = x W^T; MODE 1, 2, 3: up to 2, 4, 8 tokens on INT8 MMAs, 4: up to 16 on BF16 MMAs.  A tile is 16 rows of W; a cluster of C CTAs shares a tile, each
-// taking a K range, and the CTA whose turn it is (tile index mod C) receives the partial tiles of
-// all in its shared memory and adds them in rank order.  One warp sends and another receives, several
-// tiles apart: with one warp for both a tile took the exchange's 1.5 us.  C > 1 is for matrices with few tiles
-// (the spread over 148 SMs would be uneven) and for K ranges whose token fragments do not fit in
-// registers.  HBM-bound on N K (1/2 + 2 / group) bytes.
+// y = x W^T; MODE 1, 2, 3: up to 2, 4, 8 tokens on INT8 MMAs, 4: up to 16 on BF16 MMAs.  A tile is 16
+// rows of W; a cluster of C CTAs shares a tile, each taking a K range, and the CTA whose turn it is
+// (tile index mod C) receives the partial tiles of all in its shared memory and adds them in rank order.
+// One warp sends and another receives, several tiles apart: with one warp for both a tile took the
+// exchange's 1.5 us.  C > 1 is for matrices with few tiles (the spread over 148 SMs would be uneven) and
+// for K ranges whose token fragments do not fit in registers.
+//
+// Bound by HBM, N K (1/2 + 2 / group) bytes, for up to 4 tokens (1 x 151936 x 5120, groups of 128: 61 us,
+// 6.6 TB/s).  From 5 tokens on by the consumers: at 8 the three MMAs of a run alone take the time in which
+// its weights arrive (84 us), at 16 the expansion to BF16 and the waits between (133 us).
 //
 // Launched with programmatic stream serialisation: the producer starts on the weights while the
 // previous kernel of the stream drains; tokens are read, and outputs written, after
 // griddepcontrol.wait.  (Weights written by the previous kernel are safe: only kernels of this
 // kind let their successor start early, and they write no weights.)
+
 // Superblocks per warp at most: 64 to 128 registers of token fragments.
 __host__ __device__ constexpr int lin_units(int mode) { return mode == 4 ? 4 : i4_mode_runs(mode) / 4; }
 __host__ __device__ constexpr int lin_sets(int mode) { return mode == 4 ? 2 : 1; }  // of 8 tokens

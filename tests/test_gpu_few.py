@@ -184,6 +184,40 @@ def test_a_nan_token_stays_alone(group):
     m.check(h[rest], out[rest], idx[rest], w[rest])
 
 
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("T", [2, 3, 4])
+def test_a_nan_token_stays_alone_where_columns_are_the_tokens(T, group):
+    m = Layer(512, 16, 4, 2, 4, 256, group)
+    h = normal(4, T, 512)
+    h[1, 9] = float("nan")
+    out, idx, w, _ = m.run(h)
+    assert torch.isnan(out[1]).all()
+    rest = [t for t in range(T) if t != 1]
+    m.check(h[rest], out[rest], idx[rest], w[rest])
+
+
+@pytest.mark.parametrize("T,d,I", [(3, 5376, 256), (5, 5376, 256), (4, 512, 6144), (16, 512, 6144)])
+def test_wide_layers_hold_two_tokens_to_an_entry(T, d, I):
+    m = Layer(d, 8, 2, 2, 3, I, 64)
+    h = normal(8, T, d)
+    out, idx, w, _ = m.run(h)
+    m.check(h, out, idx, w)
+
+
+@pytest.mark.parametrize("T", [5, 8, 13])
+def test_rows_do_not_depend_on_how_entries_are_cut(T):
+    """All tokens on the same experts: entries of four tokens and a rest, and each token alone."""
+    bias = torch.zeros(32, device="cuda")
+    bias[[3, 4, 9, 30]] = 5.0
+    m = Layer(512, 32, 4, 4, 4, 256, 64, bias=bias)
+    h = normal(13, T, 512)
+    out = m.run(h)[0]
+    for t in range(T):
+        one = torch.empty_like(out[:1])
+        m.call(h[t:t + 1].clone(), one)
+        assert torch.equal(one[0], out[t])
+
+
 @pytest.mark.parametrize("group", [0, 64])
 def test_same_bits_every_time_and_without_optional_outputs(group):
     m = Layer(2560, 64, 8, 4, 8, 1280, group)

@@ -157,6 +157,25 @@ def test_linear_token_rows_do_not_depend_on_the_batch():
         assert torch.equal(one[0], out[t])
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N,K,fp32", [
+    (1, 20011, 640, True), (2, 16000, 1408, False), (3, 20483, 256, True), (4, 11000, 5120, False),
+    (8, 20011, 640, True), (16, 11000, 1408, False)])
+def test_linear_with_many_tiles_to_a_cta(T, N, K, fp32, group):
+    """Steps of two tiles, even and odd numbers of tiles to a CTA."""
+    x, w, _, out = run_linear(T, N, K, group, fp32)
+    ref, bound = R.linear_ref(x, w[0], group, fp32)
+    R.assert_within(out, ref, bound, f"T={T} N={N} K={K} g={group}")
+
+
+def test_linear_rows_of_steps_of_two_tiles_have_the_same_bits():
+    x, w, packed, out = run_linear(8, 20011, 1280, 64, True)
+    for first, n in ((0, 1), (3, 2), (4, 4), (1, 5)):
+        part = torch.empty(n, 20011, device="cuda")
+        bm.beam_int4_linear(bm.int4_shape(n, 20011, 1280, 64), x[first:first + n].clone(), packed, part)
+        assert torch.equal(part, out[first:first + n])
+
+
 def test_linear_chain_back_to_back():
     """Each product reads what the one before wrote, without a wait between them; and weights
     converted right before their first use."""
