@@ -340,14 +340,14 @@ BEAM_API beam_status beam_moe_bias_update(const beam_moe_shape* shape, const voi
  * layer is bound by its weights' bytes, read once each, and by launches.
  *
  * 4-bit weights are integer codes with a BF16 scale per row and group of group_size (32, 64 or
- * 128) consecutive elements of the row; activations stay BF16:
+ * 128) consecutive elements of the row; inputs and outputs stay BF16:
  *   s = bf16(fl32(amax / 7)),  q = clamp(rne(fl32(x / s)), -8, 7),  value = s * q
  * with amax the group's largest magnitude; a group with s = 0 has zero codes.  A product sums each
  * group's codes times activations exactly or in FP32, multiplies by the scale and adds the groups in
- * FP32.  (For up to 8 tokens the activations enter as 23-bit integers with a common power of two per
- * token and K slice: exactly their BF16 values, unless an element is below 2^-14 of the slice's
- * largest, when it is off by at most 2^-22 of that.  There a token with a non-finite element has NaN
- * outputs.)
+ * FP32.  (For up to 8 tokens, and in the MoE layer for any number, the activations enter as 23-bit integers with a common
+ * power of two per token and K slice: exactly their BF16 values, unless an element is below 2^-14 of
+ * the slice's largest, when it is off by at most 2^-22 of that.  There a token with a non-finite
+ * element has NaN outputs.)
  *
  * Packed storage (what the kernels stream): tiles of 16 rows; in a tile, superblocks of 128
  * columns in order; a superblock is two 512-byte code blocks of 64 columns, then for each of its
@@ -397,9 +397,10 @@ BEAM_API beam_status beam_int4_linear(const beam_int4_shape* shape, const void* 
 BEAM_API size_t beam_dense_int4_workspace_size(const beam_dense_shape* shape);
 
 /* beam_dense_forward with 4-bit weights, T <= BEAM_FEW_MAX_TOKENS, I <= BEAM_INT4_MAX_K: gate_up
- * packed from (w_gate, w_up) [1, I, d], down from w_down [1, d, I], both with group_size.  ws holds
- * the activation only: beam_moe_sync_status does not apply to it (errors as in beam_int4_linear:
- * NaN outputs). */
+ * packed from (w_gate, w_up) [1, I, d], down from w_down [1, d, I], both with group_size.  Two
+ * launches.  The activation between the products is FP32 for up to 8 tokens, BF16 beyond (as in
+ * beam_dense_forward).  ws holds the activation only: beam_moe_sync_status does not apply to it
+ * (errors as in beam_int4_linear: NaN outputs). */
 BEAM_API beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int32_t group_size,
                                              const void* hidden, const void* gate_up,
                                              const void* down, void* out, void* ws,
@@ -409,12 +410,13 @@ BEAM_API beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int3
  * shape: T <= BEAM_FEW_MAX_TOKENS and I <= 8192 besides the layer's shape rules). */
 BEAM_API size_t beam_moe_few_workspace_size(const beam_moe_shape* shape);
 
-/* beam_moe_forward for 1 to BEAM_FEW_MAX_TOKENS tokens in two launches: the same arguments and
- * definition, with ws sized by beam_moe_few_workspace_size.  The router's sums run in FP64 and are
- * rounded once to FP32, so topk_idx is the definition's also on near ties; expert outputs stay FP32
- * until the combine's sum is rounded to BF16 (the activation between the expert's two products is
- * BF16, as in beam_moe_forward).  Results do not depend on timing.  The second launch is
- * cooperative: it needs every SM for itself and runs when they are free. */
+/* beam_moe_forward for 1 to BEAM_FEW_MAX_TOKENS tokens in two launches (three for more than 10 tokens
+ * where d > 5632): the same arguments and definition, with ws sized by beam_moe_few_workspace_size.  The
+ * router's sums run in FP64 and are rounded once to FP32, so topk_idx is the definition's also on near
+ * ties.  Activations between an expert's two products and expert outputs stay FP32 (the activations
+ * enter the second product as two BF16 pieces) until the combine's sum is rounded to BF16: closer to
+ * the definition than beam_moe_forward, which rounds both to BF16.  Results do not depend on timing.
+ * The second launch is cooperative: it needs every SM for itself and runs when they are free. */
 BEAM_API beam_status beam_moe_forward_few(const beam_moe_shape* shape, const void* hidden,
                                           const float* router_w, const float* bias,
                                           const void* w_gate, const void* w_up,

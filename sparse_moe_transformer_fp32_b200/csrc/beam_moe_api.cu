@@ -1194,9 +1194,10 @@ beam_status check_int4_linear(const beam_int4_shape* s) {
 }
 
 beam_status run_int4_linear(const DeviceInfo& dev, const beam_int4_shape& s, const void* x,
-                            const void* w, void* out, Int4Out kind, cudaStream_t st) {
+                            const void* w, void* out, Int4Out kind, cudaStream_t st,
+                            bool wide = false) {
   Int4LinearArgs la{};
-  la.x = static_cast<const __nv_bfloat16*>(x);
+  la.x = x;
   la.w = static_cast<const uint8_t*>(w);
   la.out = out;
   la.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
@@ -1205,6 +1206,7 @@ beam_status run_int4_linear(const DeviceInfo& dev, const beam_int4_shape& s, con
   la.K = s.K;
   la.tiles = static_cast<int>(ceil_div(s.N, 16));
   la.out_kind = kind;
+  la.wide = wide;
   BEAM_LAUNCH(kKInt4Linear, st, launch_int4_linear(la, s.group_size, dev.sms, st));
   return BEAM_OK;
 }
@@ -1243,7 +1245,7 @@ FewLayout plan_few(const beam_moe_shape& s) {
   const size_t R = static_cast<size_t>(s.T) * s.top_k;
   L.status = take(256);
   L.sc = take(sizeof(float2) * s.T * s.E);
-  L.act = take(sizeof(__nv_bfloat16) * R * s.I);
+  L.act = take(sizeof(float) * R * s.I);
   L.y = take(sizeof(float) * R * s.d);
   L.total = o;
   return L;
@@ -1277,7 +1279,7 @@ beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void
   ra.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   ra.d = shape->d;
   ra.E = shape->E;
-  // one launch up to d = 5120 (and up to 10 tokens at any d)
+  // one launch up to d = 5632 (and up to 10 tokens at any d)
   const int per = few_router_tokens(shape->d);
   for (int t = 0; t < shape->T; t += per) {
     ra.T = shape->T - t < per ? shape->T - t : per;
@@ -1291,7 +1293,7 @@ beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void
   la.w_gate = w_gate;
   la.w_up = w_up;
   la.w_down = w_down;
-  la.act = at<__nv_bfloat16>(ws, L.act);
+  la.act = at<float>(ws, L.act);
   la.y = at<float>(ws, L.y);
   la.out = static_cast<__nv_bfloat16*>(out);
   la.idx = topk_idx;
@@ -1369,7 +1371,7 @@ beam_status beam_int4_linear(const beam_int4_shape* shape, const void* x, const 
 
 size_t beam_dense_int4_workspace_size(const beam_dense_shape* shape) {
   if (check_dense_int4(shape, 128) != BEAM_OK) return 0;
-  return align_up(sizeof(__nv_bfloat16) * static_cast<size_t>(shape->T ? shape->T : 1) * shape->I, 1024);
+  return align_up(sizeof(float) * static_cast<size_t>(shape->T ? shape->T : 1) * shape->I, 1024);
 }
 
 beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int32_t group_size,
@@ -1387,8 +1389,11 @@ beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int32_t group
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const beam_int4_shape up{shape->T, 2 * shape->I, shape->d, group_size};
   const beam_int4_shape dn{shape->T, shape->d, shape->I, group_size};
-  if ((b = run_int4_linear(*dev, up, hidden, gate_up, ws, kI4OutSwiglu, st)) != BEAM_OK) return b;
-  return run_int4_linear(*dev, dn, ws, down, out, kI4OutBf16, st);
+  // the products of 9 to 16 tokens take BF16 operands: the activation is rounded as in beam_dense_forward
+  const bool wide = shape->T <= kFewCols;
+  b = run_int4_linear(*dev, up, hidden, gate_up, ws, wide ? kI4OutSwigluF32 : kI4OutSwigluBf16, st);
+  if (b != BEAM_OK) return b;
+  return run_int4_linear(*dev, dn, ws, down, out, kI4OutBf16, st, wide);
 }
 
 size_t beam_moe_few_workspace_size(const beam_moe_shape* shape) {

@@ -24,6 +24,8 @@
 // in shared memory, which would need the 4-bit codes expanded to BF16 in shared memory (four
 // times the bytes) and gives 320 m-tiles of 16 rows only 40 tiles to spread over 148 SMs.
 #pragma once
+#include <type_traits>
+
 #include "beam_moe_internal.cuh"
 
 namespace beam {
@@ -112,15 +114,16 @@ struct Int4QuantArgs {
   int group;
 };
 
-enum Int4Out { kI4OutBf16 = 0, kI4OutF32 = 1, kI4OutSwiglu = 2 };
+enum Int4Out { kI4OutBf16 = 0, kI4OutF32 = 1, kI4OutSwigluBf16 = 2, kI4OutSwigluF32 = 3 };
 
 struct Int4LinearArgs {
-  const __nv_bfloat16* x;  // [T, K]
+  const void* x;           // [T, K], BF16, or FP32 with wide
   const uint8_t* w;        // packed [tiles, K / 128, superblock]
-  void* out;               // [T, N] (SwiGLU: [T, N / 2] BF16)
+  void* out;               // [T, N] (SwiGLU: [T, N / 2], FP32 or BF16)
   uint64_t wait_limit_ns;
   int T, N, K, tiles;
   int out_kind;            // Int4Out
+  int wide;                // T <= 8
   int cluster;             // CTAs that split K
   int recv;                // receive buffers of partial tiles (cluster > 1)
   int cw;                  // KSplit::cw of the largest K range
@@ -145,7 +148,7 @@ struct FewLayerArgs {
   const void* w_gate;      // BF16 [E, I, d], or packed gate|up
   const void* w_up;        // BF16 [E, I, d], or null
   const void* w_down;      // BF16 [E, d, I], or packed
-  __nv_bfloat16* act;      // [T * k, I], all ones on entry
+  float* act;              // [T * k, I], all ones on entry
   float* y;                // [T * k, d], all ones on entry
   __nv_bfloat16* out;      // [T, d]
   int32_t* idx;            // [T, k] out, or null
@@ -315,17 +318,16 @@ __device__ __forceinline__ uint4 ld_relaxed(const void* p) {
   return v;
 }
 
-// Rows that other CTAs of the kernel are writing.  Every element was set to kUnwritten16 (a NaN that
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+constexpr float kInfinity = __builtin_huge_valf();
+
+// FP32 rows that other CTAs of the kernel are writing.  Every element was set to kUnwritten32 (a NaN that
 // no computation produces) before the kernel, so an element tells by itself whether it is there:
 // no flag has to follow the data through a fence and an atomic, which take 2 us together.
-constexpr uint32_t kUnwritten16 = 0xffffu;
 constexpr uint32_t kUnwritten32 = 0xffffffffu;
-__device__ __forceinline__ bool has_unwritten16(uint4 v) {
-  const uint32_t w[4] = {~v.x, ~v.y, ~v.z, ~v.w};
-  uint32_t z = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) z |= (w[i] - 0x00010001u) & ~w[i];  // a zero half sets its top bit
-  return (z & 0x80008000u) != 0u;
+__device__ __forceinline__ bool has_unwritten32(uint4 v) {
+  return max(max(v.x, v.y), max(v.z, v.w)) == kUnwritten32;
 }
 
 struct TokenSource {
@@ -335,8 +337,11 @@ struct TokenSource {
   uint32_t* status = nullptr;
   uint32_t where = 0;
   bool ok = true;
-  // Whether to look again; gives up after limit_ns, or when another wait did.
+  uint32_t looks = 0;
+  // Whether to look again; gives up after limit_ns, or when another wait did.  The timer and the status
+  // are read every eighth time: that takes as long as a look.
   __device__ bool again(uint64_t& t0) {
+    if (looks++ % 8 && limit_ns) return ok;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
     uint32_t other;
@@ -350,64 +355,112 @@ struct TokenSource {
     }
     return ok;
   }
-  __device__ __forceinline__ void settle(uint4& v, const __nv_bfloat16* p) {
-    if (!polled) return;
-    uint64_t t0 = 0;
-    while (has_unwritten16(v) && ok && again(t0)) v = ld_relaxed(p);
-  }
 };
 
 // The K slice of a token row is brought in by the whole warp, 16 bytes a lane and load, and staged in
 // shared memory, from where each lane picks its fragments.  Everything that runs once per entry
 // is kept short and in loops: code that is not in the instruction cache costs about 10 ns an
 // instruction, more than its execution.
-constexpr int kRowLoads = kFewMaxK / kFewWarps / 256;
-__device__ __forceinline__ void fetch_row(uint4 (&v)[kRowLoads], const __nv_bfloat16* row, int n, int lane) {
+//
+// Rows are BF16, or (wide) FP32: the activations between an expert's two products.  Rounding those to
+// BF16 would add an error as large as the rounding of the output.  One copy of the code for both: with
+// two, fragments were moved between the registers of either.
+constexpr int kRowLoads = kFewMaxK / kFewWarps / 128;
+__device__ __forceinline__ void fetch_row(uint4 (&v)[kRowLoads], const void* row, int bytes, int lane) {
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
-    const int k = (i * 32 + lane) * 8;
-    if (row != nullptr && k < n) v[i] = ld_relaxed(row + k);
+    if (row != nullptr && (i * 32 + lane) * 16 < bytes)
+      v[i] = ld_relaxed(static_cast<const uint4*>(row) + i * 32 + lane);
   }
 }
-// Stages what fetch_row brought; returns the largest magnitude bits of the lane's elements.
-__device__ __forceinline__ uint32_t stage_row(uint4 (&v)[kRowLoads], TokenSource& src,
-                                              const __nv_bfloat16* row, int n, uint8_t* raw, int lane) {
+// Waits until what fetch_row brought is there; all loads of the row at a time, one round trip.
+__device__ __forceinline__ void settle_row(uint4 (&v)[kRowLoads], TokenSource& src, const void* row, int bytes,
+                                           int lane) {
+  if (!src.polled) return;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (true) {
+    bool missing = false;
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i)
+      missing |= (i * 32 + lane) * 16 < bytes && has_unwritten32(v[i]);
+    if (!missing || !src.ok || !src.again(t0)) return;
+    fetch_row(v, row, bytes, lane);
+  }
+}
+// Stages a row; returns the largest magnitude bits of the lane's elements, as FP32 (NaN and infinity are
+// the largest).
+__device__ __forceinline__ uint32_t stage_row(const uint4 (&v)[kRowLoads], bool wide, int bytes, uint8_t* raw,
+                                              int lane) {
   uint32_t top = 0;
+  const uint32_t mask = wide ? 0x7fffffffu : 0x7fff7fffu;
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
-    const int k = (i * 32 + lane) * 8;
-    if (k < n) {
-      src.settle(v[i], row + k);
-      *reinterpret_cast<uint4*>(raw + k * 2) = v[i];
-      // magnitudes, two at a time; NaN and infinity are the largest
-      const uint32_t w = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                  __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
-      top = max(top, max(w << 16, w & 0xffff0000u));
+    if ((i * 32 + lane) * 16 < bytes) {
+      *reinterpret_cast<uint4*>(raw + (i * 32 + lane) * 16) = v[i];
+      const uint32_t x = v[i].x & mask, y = v[i].y & mask, z = v[i].z & mask, w = v[i].w & mask;
+      if (wide) {
+        top = max(top, max(max(x, y), max(z, w)));
+      } else {  // magnitudes, two at a time
+        const uint32_t m = __vmaxu2(__vmaxu2(x, y), __vmaxu2(z, w));
+        top = max(top, max(m << 16, m & 0xffff0000u));
+      }
     }
   }
   return top;
 }
+// Stages an FP32 row of n elements as two BF16 pieces (16 bits: off by at most 2^-17; beyond BF16's range
+// the second is zero), the second ones n elements on.
+__device__ __forceinline__ void stage_pieces(const uint4 (&v)[kRowLoads], int n, uint8_t* raw, int lane) {
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = (i * 32 + lane) * 4;
+    if (k < n) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x = __uint_as_float(w[j * 2]), y = __uint_as_float(w[j * 2 + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        hi[j] = *reinterpret_cast<const uint32_t*>(&h);
+        const float hx = bf16_lo(hi[j]), hy = bf16_hi(hi[j]);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(fabsf(hx) < kInfinity ? x - hx : 0.f,
+                                                       fabsf(hy) < kInfinity ? y - hy : 0.f);
+        lo[j] = *reinterpret_cast<const uint32_t*>(&l);
+      }
+      *reinterpret_cast<uint2*>(raw + k * 2) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(raw + (n + k) * 2) = make_uint2(lo[0], lo[1]);
+    }
+  }
+}
 
-// B fragments of the K slices of up to 8 BF16 tokens (n elements), 4 registers per 32 elements: column
-// t is token t.  row(t): the slice's first element of token t, or null (a column of zeros).
+// B fragments of the K slices of BF16 tokens (n elements), 4 registers per 32 elements.  Column t is
+// token t, up to 8; wide: up to 4 FP32 tokens, columns t and 4 + t their two pieces.  row(t): the
+// slice's first element of token t, or null (a column of zeros).
 template <int RUNS, int REGS, class Row>
-__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& src, Row row, int tokens,
+__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& src, Row row, bool wide, int tokens,
                                             int n, uint8_t* raw, const uint8_t* zeros, int lane) {
   static_assert(RUNS * 4 <= REGS, "the fragments must fit");
-  const int g = lane >> 2, c = lane & 3;
+  const int g = lane >> 2, c = lane & 3, bytes = n * (wide ? 4 : 2);
   uint4 v[kRowLoads];
-  const __nv_bfloat16* next = row(0);
-  fetch_row(v, next, n, lane);
+  const void* next = row(0);
+  fetch_row(v, next, bytes, lane);
 #pragma unroll 1
   for (int t = 0; t < tokens; ++t) {
-    const __nv_bfloat16* from = next;
-    if (from != nullptr) stage_row(v, src, from, n, raw, lane);
+    const void* from = next;
+    if (from != nullptr) {
+      settle_row(v, src, from, bytes, lane);
+      if (wide)
+        stage_pieces(v, n, raw, lane);
+      else
+        stage_row(v, false, bytes, raw, lane);
+    }
     __syncwarp();
     next = t + 1 < tokens ? row(t + 1) : nullptr;
-    fetch_row(v, next, n, lane);
-    const bool mine = g == t && from != nullptr;
+    fetch_row(v, next, bytes, lane);
+    const bool mine = (wide ? g & 3 : g) == t && from != nullptr;
     if (mine || t == 0) {  // the first token also clears the other columns
-      const uint8_t* p = mine ? raw + c * 16 : zeros;
+      const uint8_t* p = mine ? raw + (wide ? (g >> 2) * n * 2 : 0) + c * 16 : zeros;
       const int step = mine ? 64 : 0;
 #pragma unroll
       for (int j = 0; j < RUNS; ++j) {
@@ -444,8 +497,6 @@ __device__ __forceinline__ void bf16_slice(float (&acc)[4], const uint32_t (&b)[
   for (int i = 0; i < 4; ++i) acc[i] += d0[i] + d1[i];
 }
 
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // Products with 4-bit weights run on INT8 MMAs for up to 8 tokens.  A code block of 16 rows x 64
 // columns takes 22 clocks of an SM to arrive (528 bytes at 6.5 TB/s over the GPU), and expanding it
@@ -468,8 +519,10 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 constexpr int kI4SumStart = 0x4b400000;
 constexpr float kI4SumStartF = 12582912.f;
 constexpr int kI4SliceMax = kFewMaxK / kFewWarps;
-// A warp's buffer for one token of n elements: BF16, and for 4-bit weights three bytes of digits.
-__host__ __device__ constexpr int stage_bytes(int n, bool i4) { return i4 ? 5 * n : 2 * n; }
+// A warp's buffer for one token of n elements: the row, and for 4-bit weights three bytes of digits.
+__host__ __device__ constexpr int stage_bytes(int n, bool i4, bool wide) {
+  return n * ((wide ? 4 : 2) + (i4 ? 3 : 0));
+}
 constexpr int kI4NonFinite = 1 << 20;           // in the place of an exponent
 
 // Runs of 32 of a warp's K slice at most: 64, 80 or 120 registers of fragments.
@@ -488,29 +541,40 @@ __device__ __forceinline__ I4Scale i4_scale(uint32_t top) {
   const int E = max(static_cast<int>(top >> 23) - 127, -105);
   return {E, __uint_as_float(static_cast<uint32_t>(127 + 21 - E) << 23)};
 }
-// Digits of 4 elements (two words of BF16 pairs), a byte each: d[p] holds digit p.  The addition of
-// 1.5 2^23 rounds x 2^(21 - E) to an integer i, and leaves it in the low bits; the bytes of i +
-// 0x808080 are the balanced digits plus 128.
-__device__ __forceinline__ void i4_digits(uint32_t (&d)[3], uint32_t w0, uint32_t w1, float f) {
+// Digits of 4 elements, a byte each: d[p] holds digit p.  The addition of 1.5 2^23 rounds x 2^(21 - E) to
+// an integer i, and leaves it in the low bits; the bytes of i + 0x808080 are the balanced digits plus 128.
+__device__ __forceinline__ void i4_digits(uint32_t (&d)[3], const float (&e)[4], float f) {
   uint32_t x[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t u = j < 2 ? w0 : w1;
-    x[j] = __float_as_uint(fmaf((j & 1) ? bf16_hi(u) : bf16_lo(u), f, kI4SumStartF)) + 0x00408080u;
-  }
+  for (int j = 0; j < 4; ++j) x[j] = __float_as_uint(fmaf(e[j], f, kI4SumStartF)) + 0x00408080u;
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     const uint32_t at = 0x0040u + 0x0011u * (2 - p);  // byte 2 - p of both
     d[p] = __byte_perm(__byte_perm(x[0], x[1], at), __byte_perm(x[2], x[3], at), 0x5410) ^ 0x80808080u;
   }
 }
+// The same of two words of BF16 pairs.
+__device__ __forceinline__ void i4_digits(uint32_t (&d)[3], uint32_t w0, uint32_t w1, float f) {
+  const float e[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
+  i4_digits(d, e, f);
+}
+__device__ __forceinline__ void i4_digits(uint32_t (&d)[3], uint4 w, float f) {  // four FP32
+  const float e[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+  i4_digits(d, e, f);
+}
 // Splits a staged slice (n elements, a multiple of 128) into its digits, n bytes each.
-__device__ __forceinline__ void i4_split(const uint8_t* raw, uint8_t* digits, int n, float f, int lane) {
+__device__ __forceinline__ void i4_split(const uint8_t* raw, bool wide, uint8_t* digits, int n, float f, int lane) {
 #pragma unroll 1
   for (int k = lane * 4; k < n; k += 128) {
-    const uint2 w = *reinterpret_cast<const uint2*>(raw + k * 2);
+    uint4 w;  // as FP32
+    if (wide) {
+      w = *reinterpret_cast<const uint4*>(raw + k * 4);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(raw + k * 2);
+      w = make_uint4(u.x << 16, u.x & 0xffff0000u, u.y << 16, u.y & 0xffff0000u);
+    }
     uint32_t d[3];
-    i4_digits(d, w.x, w.y, f);
+    i4_digits(d, w, f);
 #pragma unroll
     for (int p = 0; p < 3; ++p) *reinterpret_cast<uint32_t*>(digits + p * n + k) = d[p];
   }
@@ -529,7 +593,7 @@ __device__ __forceinline__ I4Factor i4_factor(int E) {
 }
 
 // B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
-// row(t): the slice's first element of token t, or null.  factor[h]: of the token of the lane's result
+// row(t): the slice's first element of token t (BF16, or FP32 with wide), or null.  factor[h]: of the token of the lane's result
 // column h.
 //
 // MODE 1 and 2 split a token at a time with the whole warp, through shared memory: a lane's share of the
@@ -538,7 +602,7 @@ __device__ __forceinline__ I4Factor i4_factor(int E) {
 // registers that take the digits.
 template <int MODE, int REGS, class Row>
 __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&factor)[2], TokenSource& src,
-                                               Row row, int tokens, int units, uint8_t* raw,
+                                               Row row, bool wide, int tokens, int units, uint8_t* raw,
                                                const uint8_t* zeros, int lane) {
   constexpr int kRuns = i4_mode_runs(MODE);
   static_assert(kRuns * 2 * MODE <= REGS, "the fragments must fit");
@@ -546,21 +610,25 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
   const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of the lane's result column 0
   int E[2] = {0, 0};
   if constexpr (MODE < 3) {
-  uint8_t* const digits = raw + 2 * n;
+  const int bytes = n * (wide ? 4 : 2);
+  uint8_t* const digits = raw + bytes;
   const int token = MODE == 1 ? (g < 6 ? g & 1 : -1) : g & 3;  // of B column g
   uint4 v[kRowLoads];
-  const __nv_bfloat16* next = row(0);
-  fetch_row(v, next, n, lane);
+  const void* next = row(0);
+  fetch_row(v, next, bytes, lane);
 #pragma unroll 1
   for (int t = 0; t < tokens; ++t) {
-    const __nv_bfloat16* from = next;
+    const void* from = next;
     uint32_t top = 0;
-    if (from != nullptr) top = stage_row(v, src, from, n, raw, lane);
+    if (from != nullptr) {
+      settle_row(v, src, from, bytes, lane);
+      top = stage_row(v, wide, bytes, raw, lane);
+    }
     top = __reduce_max_sync(0xffffffffu, top);
     next = t + 1 < tokens ? row(t + 1) : nullptr;
-    fetch_row(v, next, n, lane);
+    fetch_row(v, next, bytes, lane);
     const I4Scale s = i4_scale(top);
-    if (from != nullptr) i4_split(raw, digits, n, s.f, lane);
+    if (from != nullptr) i4_split(raw, wide, digits, n, s.f, lane);
     __syncwarp();
     const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
     E[0] = t == first ? e : E[0];
@@ -586,22 +654,37 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
     __syncwarp();
   }
   } else {
-    const __nv_bfloat16* p = g < tokens ? row(g) + c * 8 : nullptr;
+    auto convert = [&](auto is_wide) {
+    constexpr bool kWide = decltype(is_wide)::value;
+    // a lane's 8 elements of run j; of FP32 rows the second half comes 16 bytes on
+    const uint4* p = g < tokens ? reinterpret_cast<const uint4*>(row(g)) + c * (kWide ? 2 : 1) : nullptr;
+    auto part = [&](int j, int half) {
+      if (p == nullptr || j >= units * 4) return make_uint4(0u, 0u, 0u, 0u);
+      return __ldcg(p + j * (kWide ? 8 : 4) + half);
+    };
+    uint32_t top = 0;
+    if constexpr (kWide) {  // read twice: 8 words of a run do not fit where its 6 of digits go
 #pragma unroll
-    for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (p != nullptr && j < units * 4) v = __ldcg(reinterpret_cast<const uint4*>(p + j * 32));
-      b[j * 2 * MODE] = v.x;
-      b[j * 2 * MODE + 1] = v.y;
-      b[j * 2 * MODE + 2] = v.z;
-      b[j * 2 * MODE + 3] = v.w;
+      for (int j = 0; j < kRuns * 2; ++j) {
+        const uint4 v = part(j / 2, j % 2);
+        top = max(top, max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
+        const uint4 v = part(j, 0);
+        b[j * 6] = v.x;
+        b[j * 6 + 1] = v.y;
+        b[j * 6 + 2] = v.z;
+        b[j * 6 + 3] = v.w;
+      }
+      uint32_t w = 0;  // magnitudes, two at a time
+#pragma unroll
+      for (int j = 0; j < kRuns; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w = __vmaxu2(w, b[j * 6 + i] & 0x7fff7fffu);
+      top = max(w << 16, w & 0xffff0000u);
     }
-    uint32_t w = 0;  // magnitudes, two at a time
-#pragma unroll
-    for (int j = 0; j < kRuns; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w = __vmaxu2(w, b[j * 2 * MODE + i] & 0x7fff7fffu);
-    uint32_t top = max(w << 16, w & 0xffff0000u);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const I4Scale s = i4_scale(top);
@@ -611,14 +694,24 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
       uint32_t lo[3], hi[3];
-      i4_digits(lo, b[j * 2 * MODE], b[j * 2 * MODE + 1], s.f);
-      i4_digits(hi, b[j * 2 * MODE + 2], b[j * 2 * MODE + 3], s.f);
+      if constexpr (kWide) {
+        i4_digits(lo, part(j, 0), s.f);
+        i4_digits(hi, part(j, 1), s.f);
+      } else {
+        i4_digits(lo, b[j * 6], b[j * 6 + 1], s.f);
+        i4_digits(hi, b[j * 6 + 2], b[j * 6 + 3], s.f);
+      }
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
         b[j * 6 + q * 2] = lo[q];
         b[j * 6 + q * 2 + 1] = hi[q];
       }
     }
+    };
+    if (wide)
+      convert(std::true_type{});
+    else
+      convert(std::false_type{});
   }
   factor[0] = i4_factor(E[0]);
   factor[1] = i4_factor(E[1]);

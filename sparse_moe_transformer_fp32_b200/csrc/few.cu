@@ -110,12 +110,7 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
 
 // ------------------------------------------------------------------ the layer
 
-// Stores of what other CTAs poll for.  A NaN is stored as the one that is not kUnwritten.
-__device__ __forceinline__ void st_relaxed16(__nv_bfloat16* p, __nv_bfloat16 v) {
-  unsigned short u = __bfloat16_as_ushort(v);
-  if (u == kUnwritten16) u = 0x7fff;
-  asm volatile("st.relaxed.gpu.global.u16 [%0], %1;" ::"l"(p), "h"(u) : "memory");
-}
+// A store of what other CTAs poll for.  A NaN is stored as the one that is not kUnwritten32.
 __device__ __forceinline__ void st_relaxed32(float* p, float v) {
   uint32_t u = __float_as_uint(v);
   if (u == kUnwritten32) u = 0x7fffffffu;
@@ -132,7 +127,8 @@ __device__ __forceinline__ uint32_t score_key(float v) {
 constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..24
 
 constexpr uint8_t kNoSlot = 255;
-constexpr int kI4EntryMax = 4;  // tokens of an entry with 4-bit weights
+constexpr int kEntryMax = 4;  // tokens of an entry, at most
+static_assert(kEntryMax * 2 == kFewCols, "both BF16 pieces of an entry's activations are columns");
 constexpr int kSlotTable = kFewMaxTokens * kMaxE * 8;  // offset in the ring, behind the scores
 
 struct FewShared {
@@ -275,8 +271,8 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
 // Everything after the router scores, in one cooperative persistent kernel:
 //   selection        every CTA for itself (E scores per token; no exchange needed)
 //   gate|up          items (entry, 8 intermediate rows): a 16-row tile holds 8 gate rows and the
-//                    same 8 up rows, so one lane ends up with both and applies SwiGLU; BF16
-//                    activations, the down product's MMA operand, as the layer defines them
+//                    same 8 up rows, so one lane ends up with both and applies SwiGLU;
+//                    FP32 activations
 //   down             items (entry, 16 output rows): the entry's activations, polled for; FP32
 //                    partial outputs per slot
 //   combine          every CTA an even share of the output columns: each token's k slots, polled
@@ -372,19 +368,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
     uint8_t* const raw = smem + a.stages * a.slot_bytes + kFewRed * kFewWarps * kStep * 512 + warp * a.stage_bytes;
     auto load = [&](int ph, int entry) {  // entry < 0: all tokens
       const KSplit ks = ph > 0 ? a.k2 : a.k1;
-      const int K = ph > 0 ? a.I : a.d, units = ks.count(warp);
-      const __nv_bfloat16* from = (ph > 0 ? a.act : a.h) + ks.start(warp) * kUnit;
+      const int units = ks.count(warp), n = entry < 0 ? a.T : sh.entry_n[entry];
+      const size_t k0 = ks.start(warp) * kUnit;
       TokenSource src{ph > 0, abort_flag, a.wait_limit_ns, a.status, kWhereFew + 1};
-      auto row = [&](int col) -> const __nv_bfloat16* {
-        if (entry < 0) return from + static_cast<size_t>(col) * K;
+      auto row = [&](int col) -> const void* {
+        if (entry < 0) return a.h + static_cast<size_t>(col) * a.d + k0;
         const int s = sh.entry_slot[entry][col];
-        return s == kNoSlot ? nullptr : from + static_cast<size_t>(ph > 0 ? s : s / a.k) * K;
+        if (s == kNoSlot) return nullptr;
+        if (ph > 0) return a.act + static_cast<size_t>(s) * a.I + k0;
+        return a.h + static_cast<size_t>(s / a.k) * a.d + k0;
       };
-      const int n_tok = entry < 0 ? a.T : sh.entry_n[entry];
       if constexpr (kI4)
-        i4_load_tokens<(kI4 ? MODE : 1)>(b, factor, src, row, n_tok, units, raw, sh.zeros, lane);
+        i4_load_tokens<(kI4 ? MODE : 1)>(b, factor, src, row, ph > 0, n, units, raw, sh.zeros, lane);
       else
-        load_tokens<kRuns>(b, src, row, n_tok, units * kUnit, raw, sh.zeros, lane);
+        load_tokens<kRuns>(b, src, row, ph > 0, n, units * kUnit, raw, sh.zeros, lane);
       return __all_sync(0xffffffffu, src.ok) != 0;
     };
     int slot = 0, rb = 0;
@@ -593,6 +590,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.red_empty[rb]));
           const int n = sh.entry_n[entry];
+          if (!kI4 && ph > 0) {  // the products of the second pieces are two lanes on
+            v[0].x += __shfl_xor_sync(0xffffffffu, v[0].x, 2);
+            v[0].y += __shfl_xor_sync(0xffffffffu, v[0].y, 2);
+            v[0].z += __shfl_xor_sync(0xffffffffu, v[0].z, 2);
+            v[0].w += __shfl_xor_sync(0xffffffffu, v[0].w, 2);
+          }
 #pragma unroll
           for (int r = 0; r < kStep; ++r) {
             if (r >= len) break;
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
               if (col < n && sh.entry_slot[entry][col] != kNoSlot) {
                 const size_t s = sh.entry_slot[entry][col];
                 if (ph == 0) {
-                  st_relaxed16(a.act + s * a.I + (tile + r) * 8 + g, __float2bfloat16_rn(swiglu(lo[h], hi[h])));
+                  st_relaxed32(a.act + s * a.I + (tile + r) * 8 + g, swiglu(lo[h], hi[h]));
                 } else {
                   float* y = a.y + s * a.d + (tile + r) * 16 + g;
                   st_relaxed32(y, lo[h]);
@@ -681,7 +684,7 @@ static_assert(sizeof(FewShared) <= 4096, "FewShared must fit beside the ring");
 // those before the selection is done.
 constexpr int kSmallestRing = kFewMaxStages * 2 * i4_unit_bytes(128);
 static_assert(16 * bf16_row_stride(4) >= 4 * i4_unit_bytes(128), "BF16 rings are twice as large at least");
-static_assert(kSlotTable + kI4EntryMax * kMaxE <= kSmallestRing && 2 * kSmallestRing > kSlotTable + kFewCols * kMaxE, "scores and slots must fit in the ring");
+static_assert(kSlotTable + kEntryMax * kMaxE <= kSmallestRing && 2 * kSmallestRing > kSlotTable + kFewCols * kMaxE, "scores and slots must fit in the ring");
 static_assert(kFewMaxTokens * kMaxE * 9 <= kSmallestRing + kFewRed * kFewWarps * 512,
               "scores and slots must fit in the ring and the partial-tile buffers");
 
@@ -702,14 +705,15 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   // Tokens of an entry: with 4-bit weights 4 (2 alone, or where the digits of 4 do not fit in a warp's
   // registers).  8 to an entry read the weights of an expert of 5 to 8 tokens once, but every product
   // then takes three MMAs instead of two: 16 tokens over 64 experts 267 us, with 4 to an entry 249.
-  a.entry_max = !group ? kFewCols : a.T <= 2 || a.d > 5120 || a.I > 5120 ? 2 : kI4EntryMax;
+  a.entry_max = group && (a.T <= 2 || a.d > 5120 || a.I > 5120) ? 2 : kEntryMax;
   const int step = group ? 2 : 1;  // tiles
   a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
   a.k2 = make_ksplit(a.I / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
   const int c1 = chunk_bytes(a.k1, step * unit_bytes), c2 = chunk_bytes(a.k2, step * unit_bytes);
   a.slot_bytes = c1 > c2 ? c1 : c2;
-  const int most = (a.d > a.I ? a.d : a.I) / unit;  // of a warp's K slice
-  a.stage_bytes = stage_bytes((most + kFewWarps - 1) / kFewWarps * unit, group != 0);
+  const int b1 = stage_bytes((a.d / unit + kFewWarps - 1) / kFewWarps * unit, group != 0, false);
+  const int b2 = stage_bytes((a.I / unit + kFewWarps - 1) / kFewWarps * unit, group != 0, true);
+  a.stage_bytes = b1 > b2 ? b1 : b2;
   const size_t red = static_cast<size_t>(kFewRed) * kFewWarps * step * 512 +
                      static_cast<size_t>(kFewWarps) * a.stage_bytes;
   a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);

@@ -246,13 +246,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     uint32_t b[kUnits * 8 * MODE];
     [[maybe_unused]] I4Factor factor[2];
     pdl_wait();
-    const __nv_bfloat16* x0 = a.x + static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit;
-    auto row = [&](int t) { return x0 + static_cast<size_t>(t) * a.K; };
+    const size_t k0 = static_cast<size_t>(u0 + ks.start(warp)) * kI4Unit;
+    auto row = [&](int t) -> const void* {
+      const size_t k = static_cast<size_t>(t) * a.K + k0;
+      return static_cast<const uint8_t*>(a.x) + (a.wide ? k * 4 : k * 2);
+    };
     [[maybe_unused]] TokenSource src;
     if constexpr (MODE == 4)
-      i4_load_tokens16<kUnits * 4>(b, row, a.T, units, lane);
+      i4_load_tokens16<kUnits * 4>(
+          b, [&](int t) { return static_cast<const __nv_bfloat16*>(a.x) + static_cast<size_t>(t) * a.K + k0; },
+          a.T, units, lane);
     else
-      i4_load_tokens<MODE>(b, factor, src, row, a.T, units, split, zeros_sh, lane);
+      i4_load_tokens<MODE>(b, factor, src, row, a.wide, a.T, units, split, zeros_sh, lane);
     int slot = 0, rb = 0;
     uint32_t par = 0, rpar = 1;
     bool ok = true;
@@ -429,11 +434,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         for (int h = 0; h < 2; ++h) {
           const int t = s * kFewCols + c * 2 + h;
           if (t >= a.T) continue;
-          if (a.out_kind == kI4OutSwiglu) {  // row g: gate, row g + 8: up
+          if (a.out_kind >= kI4OutSwigluBf16) {  // row g: gate, row g + 8: up
             const int n = tile * 8 + g;
-            if (n < a.N / 2)
-              static_cast<__nv_bfloat16*>(a.out)[static_cast<size_t>(t) * (a.N / 2) + n] =
-                  __float2bfloat16_rn(swiglu(lo[h], hi[h]));
+            const size_t o = static_cast<size_t>(t) * (a.N / 2) + n;
+            const float v = swiglu(lo[h], hi[h]);
+            if (n < a.N / 2) {
+              if (a.out_kind == kI4OutSwigluF32)
+                static_cast<float*>(a.out)[o] = v;
+              else
+                static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+            }
           } else {
             const int n = tile * 16 + g;
             const size_t o = static_cast<size_t>(t) * a.N + n;
@@ -534,7 +544,7 @@ cudaError_t launch_int4_linear(Int4LinearArgs a, int group, int sms, cudaStream_
   if (!best) return cudaErrorInvalidConfiguration;
   a.cluster = best;
   const int per = (units + best - 1) / best;
-  a.stage_bytes = mode == 4 ? 0 : stage_bytes((per + kFewWarps - 1) / kFewWarps * kI4Unit, true);
+  a.stage_bytes = mode > 2 ? 0 : stage_bytes((per + kFewWarps - 1) / kFewWarps * kI4Unit, true, a.wide);
   a.recv = kLinRecvBytes / (best * 512 * lin_sets(mode));
   if (a.recv > kLinRecv) a.recv = kLinRecv;
   const int step = mode <= 2 && (a.tiles + best_clus - 1) / best_clus >= kLinStepTiles ? 2 : 1;
