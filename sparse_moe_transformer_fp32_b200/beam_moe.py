@@ -420,6 +420,27 @@ def _one_device(stream, *tensors):
     return _stream(stream)
 
 
+def _launch(stream, *specs):
+    """(stream to launch on, data pointers) of checked (tensor, dtype, name, shape or None) entries; a
+    fifth item, True, allows None.  The checks of _ptr and _one_device, in a form that takes a third
+    of their time: a small call is over in the time that ten of those take."""
+    dev, same, ptrs = -1, True, []
+    for spec in specs:
+        t, dtype, _, shape = spec[:4]
+        if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
+                and (shape is None or t.shape == shape) and t.is_contiguous()):
+            d = t.get_device()
+            same = same and dev in (-1, d)
+            dev = d
+            ptrs.append(t.data_ptr())
+        else:
+            ptrs.append(_ptr(*spec))  # says what is wrong
+    if not same or dev != torch.cuda.current_device():
+        _one_device(0, *(spec[0] for spec in specs))
+    # the raw handle of torch.cuda.current_stream, without the object around it
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream), ptrs
+
+
 def int4_shape(T, N, K, group_size=128) -> beam_int4_shape:
     return beam_int4_shape(T, N, K, group_size)
 
@@ -439,30 +460,30 @@ def beam_int4_quantize(a, b=None, group_size=128, out=None, stream=None):
         raise BeamError(BEAM_ERR_UNSUPPORTED, "beam_int4_packed_size")
     if out is None:
         out = torch.empty((groups, n), dtype=torch.uint8, device=a.device)
-    args = [_ptr(a, torch.bfloat16, "a", tuple(a.shape)),
-            _ptr(b, torch.bfloat16, "b", tuple(a.shape), optional=True),
-            groups, rows, cols, group_size, _ptr(out, torch.uint8, "out", (groups, n))]
-    _check(lib().beam_int4_quantize(*args, _one_device(stream, a, b, out)), "beam_int4_quantize")
+    st, (pa, pb, po) = _launch(stream, (a, torch.bfloat16, "a", a.shape),
+                               (b, torch.bfloat16, "b", a.shape, True),
+                               (out, torch.uint8, "out", (groups, n)))
+    _check(lib().beam_int4_quantize(pa, pb, groups, rows, cols, group_size, po, st), "beam_int4_quantize")
     return out
 
 
 def _packed(t, name, groups, rows, cols, group_size):
-    """Pointer of packed weights, whose size must be that of [groups, rows, cols]."""
-    p = _ptr(t, torch.uint8, name)
-    if t.numel() != beam_int4_packed_size(groups, rows, cols, group_size):
+    """Entry of _launch for packed weights, whose size must be that of [groups, rows, cols]."""
+    if isinstance(t, torch.Tensor) and t.numel() != beam_int4_packed_size(groups, rows, cols, group_size):
+        _ptr(t, torch.uint8, name)
         raise ValueError(f"{name} must hold {groups} x {rows} x {cols} weights in groups of {group_size} "
                          f"(got {t.numel()} bytes)")
-    return p
+    return t, torch.uint8, name, None
 
 
 def beam_int4_linear(shape, x, packed, out, stream=None):
     """out [T, N] (bfloat16 or float32) = x [T, K] BF16 times packed 4-bit weights [N, K]."""
     T, N, K = shape.T, shape.N, shape.K
     fp32 = isinstance(out, torch.Tensor) and out.dtype == torch.float32
-    args = [_ptr(x, torch.bfloat16, "x", (T, K)),
-            _packed(packed, "packed", 1, N, K, shape.group_size),
-            _ptr(out, torch.float32 if fp32 else torch.bfloat16, "out", (T, N)), 1 if fp32 else 0]
-    _check(lib().beam_int4_linear(ctypes.byref(shape), *args, _one_device(stream, x, packed, out)),
+    st, (px, pw, po) = _launch(stream, (x, torch.bfloat16, "x", (T, K)),
+                               _packed(packed, "packed", 1, N, K, shape.group_size),
+                               (out, torch.float32 if fp32 else torch.bfloat16, "out", (T, N)))
+    _check(lib().beam_int4_linear(ctypes.byref(shape), px, pw, po, 1 if fp32 else 0, st),
            "beam_int4_linear")
 
 
@@ -477,16 +498,14 @@ def beam_dense_forward_int4(shape, group_size, hidden, gate_up, down, out, ws=No
     """beam_dense_forward for at most 16 tokens with 4-bit weights: gate_up =
     beam_int4_quantize(w_gate[None], w_up[None]), down = beam_int4_quantize(w_down[None])."""
     T, d, I = shape.T, shape.d, shape.I
-    args = [_ptr(hidden, torch.bfloat16, "hidden", (T, d)),
-            _packed(gate_up, "gate_up", 1, 2 * I, d, group_size),
-            _packed(down, "down", 1, d, I, group_size),
-            _ptr(out, torch.bfloat16, "out", (T, d))]
     if ws is None:
+        _ptr(hidden, torch.bfloat16, "hidden", (T, d))
         ws = dense_int4_workspace(shape, hidden.device)
-    _ptr(ws, torch.uint8, "ws")
-    _check(lib().beam_dense_forward_int4(ctypes.byref(shape), group_size, *args, ws.data_ptr(),
-                                         ws.numel(),
-                                         _one_device(stream, hidden, gate_up, down, out, ws)),
+    st, ptrs = _launch(stream, (hidden, torch.bfloat16, "hidden", (T, d)),
+                       _packed(gate_up, "gate_up", 1, 2 * I, d, group_size),
+                       _packed(down, "down", 1, d, I, group_size),
+                       (out, torch.bfloat16, "out", (T, d)), (ws, torch.uint8, "ws", None))
+    _check(lib().beam_dense_forward_int4(ctypes.byref(shape), group_size, *ptrs, ws.numel(), st),
            "beam_dense_forward_int4")
     return ws
 
@@ -503,20 +522,19 @@ def beam_moe_forward_few(shape, hidden, router_w, bias, w_gate, w_up, w_down, ou
                          topk_w=None, ws=None, stream=None):
     """beam_moe_forward for at most 16 tokens, in two launches."""
     T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
-    args = [_ptr(hidden, torch.bfloat16, "hidden", (T, d)),
-            _ptr(router_w, torch.float32, "router_w", (E, d)),
-            _ptr(bias, torch.float32, "bias", (E,)),
-            _ptr(w_gate, torch.bfloat16, "w_gate", (E, I, d)),
-            _ptr(w_up, torch.bfloat16, "w_up", (E, I, d)),
-            _ptr(w_down, torch.bfloat16, "w_down", (E, d, I)),
-            _ptr(out, torch.bfloat16, "out", (T, d)),
-            _ptr(topk_idx, torch.int32, "topk_idx", (T, k), optional=True),
-            _ptr(topk_w, torch.float32, "topk_w", (T, k), optional=True)]
     if ws is None:
+        _ptr(hidden, torch.bfloat16, "hidden", (T, d))
         ws = few_workspace(shape, hidden.device)
-    _ptr(ws, torch.uint8, "ws")
-    st = _one_device(stream, hidden, router_w, bias, w_gate, w_up, w_down, out, topk_idx, topk_w, ws)
-    _check(lib().beam_moe_forward_few(ctypes.byref(shape), *args, ws.data_ptr(), ws.numel(), st),
+    st, ptrs = _launch(stream, (hidden, torch.bfloat16, "hidden", (T, d)),
+                       (router_w, torch.float32, "router_w", (E, d)),
+                       (bias, torch.float32, "bias", (E,)),
+                       (w_gate, torch.bfloat16, "w_gate", (E, I, d)),
+                       (w_up, torch.bfloat16, "w_up", (E, I, d)),
+                       (w_down, torch.bfloat16, "w_down", (E, d, I)),
+                       (out, torch.bfloat16, "out", (T, d)),
+                       (topk_idx, torch.int32, "topk_idx", (T, k), True),
+                       (topk_w, torch.float32, "topk_w", (T, k), True), (ws, torch.uint8, "ws", None))
+    _check(lib().beam_moe_forward_few(ctypes.byref(shape), *ptrs, ws.numel(), st),
            "beam_moe_forward_few")
     return ws
 
@@ -526,20 +544,19 @@ def beam_moe_forward_few_int4(shape, group_size, hidden, router_w, bias, gate_up
     """beam_moe_forward_few with 4-bit experts: gate_up = beam_int4_quantize(w_gate, w_up, group_size),
     down = beam_int4_quantize(w_down, group_size=group_size)."""
     T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
-    args = [_ptr(hidden, torch.bfloat16, "hidden", (T, d)),
-            _ptr(router_w, torch.float32, "router_w", (E, d)),
-            _ptr(bias, torch.float32, "bias", (E,)),
-            _packed(gate_up, "gate_up", E, 2 * I, d, group_size),
-            _packed(down, "down", E, d, I, group_size),
-            _ptr(out, torch.bfloat16, "out", (T, d)),
-            _ptr(topk_idx, torch.int32, "topk_idx", (T, k), optional=True),
-            _ptr(topk_w, torch.float32, "topk_w", (T, k), optional=True)]
     if ws is None:
+        _ptr(hidden, torch.bfloat16, "hidden", (T, d))
         ws = few_workspace(shape, hidden.device)
-    _ptr(ws, torch.uint8, "ws")
-    st = _one_device(stream, hidden, router_w, bias, gate_up, down, out, topk_idx, topk_w, ws)
-    _check(lib().beam_moe_forward_few_int4(ctypes.byref(shape), group_size, *args, ws.data_ptr(),
-                                           ws.numel(), st), "beam_moe_forward_few_int4")
+    st, ptrs = _launch(stream, (hidden, torch.bfloat16, "hidden", (T, d)),
+                       (router_w, torch.float32, "router_w", (E, d)),
+                       (bias, torch.float32, "bias", (E,)),
+                       _packed(gate_up, "gate_up", E, 2 * I, d, group_size),
+                       _packed(down, "down", E, d, I, group_size),
+                       (out, torch.bfloat16, "out", (T, d)),
+                       (topk_idx, torch.int32, "topk_idx", (T, k), True),
+                       (topk_w, torch.float32, "topk_w", (T, k), True), (ws, torch.uint8, "ws", None))
+    _check(lib().beam_moe_forward_few_int4(ctypes.byref(shape), group_size, *ptrs, ws.numel(), st),
+           "beam_moe_forward_few_int4")
     return ws
 
 
