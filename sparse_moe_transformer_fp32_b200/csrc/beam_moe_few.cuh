@@ -3,7 +3,7 @@
 // kernels share.
 //
 // Every one of these operators is a product of a large weight matrix with a handful of token rows:
-// each weight is read once and used for at most 8 tokens (16 in the linear product), far below the
+// each weight is read once and used for at most 4 tokens (16 in the linear product), far below the
 // arithmetic intensity at which the tensor cores bound anything, so the design is about streaming
 // weights without a pause:
 //
@@ -31,7 +31,7 @@
 namespace beam {
 
 constexpr int kFewMaxTokens = 16;     // tokens per call
-constexpr int kFewCols = 8;           // tokens of one entry (an expert's product in the layer kernel)
+constexpr int kFewCols = 8;           // token columns of an MMA
 constexpr int kFewMaxK = 8192;        // K of one tile: 8 warps x 1024 elements (128 B registers)
 constexpr int kFewMaxSlots = kFewMaxTokens * kMaxTopK;  // (token, expert) slots = most entries
 constexpr int kFewWarps = 8;          // consumer warps
@@ -518,7 +518,6 @@ __device__ __forceinline__ void bf16_slice(float (&acc)[4], const uint32_t (&b)[
 // pattern of 1.5 2^23, so that it is read as a float without a conversion.
 constexpr int kI4SumStart = 0x4b400000;
 constexpr float kI4SumStartF = 12582912.f;
-constexpr int kI4SliceMax = kFewMaxK / kFewWarps;
 // A warp's buffer for one token of n elements: the row, and for 4-bit weights three bytes of digits.
 __host__ __device__ constexpr int stage_bytes(int n, bool i4, bool wide) {
   return n * ((wide ? 4 : 2) + (i4 ? 3 : 0));
@@ -563,7 +562,8 @@ __device__ __forceinline__ void i4_digits(uint32_t (&d)[3], uint4 w, float f) { 
   i4_digits(d, e, f);
 }
 // Splits a staged slice (n elements, a multiple of 128) into its digits, n bytes each.
-__device__ __forceinline__ void i4_split(const uint8_t* raw, bool wide, uint8_t* digits, int n, float f, int lane) {
+__device__ __forceinline__ void i4_split(const uint8_t* raw, bool wide, uint8_t* digits, int n, float f,
+                                         int lane) {
 #pragma unroll 1
   for (int k = lane * 4; k < n; k += 128) {
     uint4 w;  // as FP32
@@ -593,8 +593,8 @@ __device__ __forceinline__ I4Factor i4_factor(int E) {
 }
 
 // B fragments of a warp's K slice (`units` superblocks) of `tokens` tokens, 2 MODE registers a run;
-// row(t): the slice's first element of token t (BF16, or FP32 with wide), or null.  factor[h]: of the token of the lane's result
-// column h.
+// row(t): the slice's first element of token t (BF16, or FP32 with wide), or null.  factor[h]: of the
+// token of the lane's result column h.
 //
 // MODE 1 and 2 split a token at a time with the whole warp, through shared memory: a lane's share of the
 // work is 1/32 of the slice, the code is short, and few registers are held beside the fragments.  At 8
@@ -610,103 +610,104 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
   const int first = MODE == 1 ? 0 : MODE == 2 ? 2 * (c & 1) : 2 * c;  // token of the lane's result column 0
   int E[2] = {0, 0};
   if constexpr (MODE < 3) {
-  const int bytes = n * (wide ? 4 : 2);
-  uint8_t* const digits = raw + bytes;
-  const int token = MODE == 1 ? (g < 6 ? g & 1 : -1) : g & 3;  // of B column g
-  uint4 v[kRowLoads];
-  const void* next = row(0);
-  fetch_row(v, next, bytes, lane);
-#pragma unroll 1
-  for (int t = 0; t < tokens; ++t) {
-    const void* from = next;
-    uint32_t top = 0;
-    if (from != nullptr) {
-      settle_row(v, src, from, bytes, lane);
-      top = stage_row(v, wide, bytes, raw, lane);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    next = t + 1 < tokens ? row(t + 1) : nullptr;
+    const int bytes = n * (wide ? 4 : 2);
+    uint8_t* const digits = raw + bytes;
+    const int token = MODE == 1 ? (g < 6 ? g & 1 : -1) : g & 3;  // of B column g
+    uint4 v[kRowLoads];
+    const void* next = row(0);
     fetch_row(v, next, bytes, lane);
-    const I4Scale s = i4_scale(top);
-    if (from != nullptr) i4_split(raw, wide, digits, n, s.f, lane);
-    __syncwarp();
-    const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
-    E[0] = t == first ? e : E[0];
-    E[1] = t == first + 1 ? e : E[1];
-    const bool mine = token == t && from != nullptr;
-    if (mine || t == 0) {  // the first token also clears the other columns
+#pragma unroll 1
+    for (int t = 0; t < tokens; ++t) {
+      const void* from = next;
+      uint32_t top = 0;
+      if (from != nullptr) {
+        settle_row(v, src, from, bytes, lane);
+        top = stage_row(v, wide, bytes, raw, lane);
+      }
+      __syncwarp();
+      top = __reduce_max_sync(0xffffffffu, top);
+      next = t + 1 < tokens ? row(t + 1) : nullptr;
+      fetch_row(v, next, bytes, lane);
+      const I4Scale s = i4_scale(top);
+      if (from != nullptr) i4_split(raw, wide, digits, n, s.f, lane);
+      __syncwarp();
+      const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
+      E[0] = t == first ? e : E[0];
+      E[1] = t == first + 1 ? e : E[1];
+      const bool mine = token == t && from != nullptr;
+      if (mine || t == 0) {  // the first token also clears the other columns
 #pragma unroll
-      for (int q = 0; q < MODE; ++q) {
-        const int digit = MODE == 1 ? g >> 1 : q == 0 ? g >> 2 : 2;  // of column g in MMA q
-        const bool any = mine && (q == 0 || g < 4);
-        const uint8_t* p = any ? digits + digit * n + c * 8 : zeros;
-        const int step = any ? 32 : 0;
+        for (int q = 0; q < MODE; ++q) {
+          const int digit = MODE == 1 ? g >> 1 : q == 0 ? g >> 2 : 2;  // of column g in MMA q
+          const bool any = mine && (q == 0 || g < 4);
+          const uint8_t* p = any ? digits + digit * n + c * 8 : zeros;
+          const int step = any ? 32 : 0;
 #pragma unroll
-        for (int j = 0; j < kRuns; ++j) {
-          if (j < units * 4) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p + j * step);
-            b[(j * MODE + q) * 2] = w.x;
-            b[(j * MODE + q) * 2 + 1] = w.y;
+          for (int j = 0; j < kRuns; ++j) {
+            if (j < units * 4) {
+              const uint2 w = *reinterpret_cast<const uint2*>(p + j * step);
+              b[(j * MODE + q) * 2] = w.x;
+              b[(j * MODE + q) * 2 + 1] = w.y;
+            }
           }
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     auto convert = [&](auto is_wide) {
-    constexpr bool kWide = decltype(is_wide)::value;
-    // a lane's 8 elements of run j; of FP32 rows the second half comes 16 bytes on
-    const uint4* p = g < tokens ? reinterpret_cast<const uint4*>(row(g)) + c * (kWide ? 2 : 1) : nullptr;
-    auto part = [&](int j, int half) {
-      if (p == nullptr || j >= units * 4) return make_uint4(0u, 0u, 0u, 0u);
-      return __ldcg(p + j * (kWide ? 8 : 4) + half);
-    };
-    uint32_t top = 0;
-    if constexpr (kWide) {  // read twice: 8 words of a run do not fit where its 6 of digits go
+      constexpr bool kWide = decltype(is_wide)::value;
+      // a lane's 8 elements of run j; of FP32 rows the second half comes 16 bytes on
+      const uint4* p = g < tokens ? reinterpret_cast<const uint4*>(row(g)) + c * (kWide ? 2 : 1) : nullptr;
+      auto part = [&](int j, int half) {
+        if (p == nullptr || j >= units * 4) return make_uint4(0u, 0u, 0u, 0u);
+        return __ldcg(p + j * (kWide ? 8 : 4) + half);
+      };
+      uint32_t top = 0;
+      if constexpr (kWide) {  // read twice: 8 words of a run do not fit where its 6 of digits go
 #pragma unroll
-      for (int j = 0; j < kRuns * 2; ++j) {
-        const uint4 v = part(j / 2, j % 2);
-        top = max(top, max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
-        const uint4 v = part(j, 0);
-        b[j * 6] = v.x;
-        b[j * 6 + 1] = v.y;
-        b[j * 6 + 2] = v.z;
-        b[j * 6 + 3] = v.w;
-      }
-      uint32_t w = 0;  // magnitudes, two at a time
-#pragma unroll
-      for (int j = 0; j < kRuns; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w = __vmaxu2(w, b[j * 6 + i] & 0x7fff7fffu);
-      top = max(w << 16, w & 0xffff0000u);
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const I4Scale s = i4_scale(top);
-    const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
-    E[0] = __shfl_sync(0xffffffffu, e, first * 4);
-    E[1] = __shfl_sync(0xffffffffu, e, first * 4 + 4);
-#pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
-      uint32_t lo[3], hi[3];
-      if constexpr (kWide) {
-        i4_digits(lo, part(j, 0), s.f);
-        i4_digits(hi, part(j, 1), s.f);
+        for (int j = 0; j < kRuns * 2; ++j) {
+          const uint4 v = part(j / 2, j % 2);
+          top = max(top, max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu)));
+        }
       } else {
-        i4_digits(lo, b[j * 6], b[j * 6 + 1], s.f);
-        i4_digits(hi, b[j * 6 + 2], b[j * 6 + 3], s.f);
-      }
 #pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        b[j * 6 + q * 2] = lo[q];
-        b[j * 6 + q * 2 + 1] = hi[q];
+        for (int j = 0; j < kRuns; ++j) {  // the elements of a run, where its digits go
+          const uint4 v = part(j, 0);
+          b[j * 6] = v.x;
+          b[j * 6 + 1] = v.y;
+          b[j * 6 + 2] = v.z;
+          b[j * 6 + 3] = v.w;
+        }
+        uint32_t w = 0;  // magnitudes, two at a time
+#pragma unroll
+        for (int j = 0; j < kRuns; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w = __vmaxu2(w, b[j * 6 + i] & 0x7fff7fffu);
+        top = max(w << 16, w & 0xffff0000u);
       }
-    }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const I4Scale s = i4_scale(top);
+      const int e = top >= 0x7f800000u ? kI4NonFinite : s.E;
+      E[0] = __shfl_sync(0xffffffffu, e, first * 4);
+      E[1] = __shfl_sync(0xffffffffu, e, first * 4 + 4);
+#pragma unroll
+      for (int j = 0; j < kRuns; ++j) {
+        uint32_t lo[3], hi[3];
+        if constexpr (kWide) {
+          i4_digits(lo, part(j, 0), s.f);
+          i4_digits(hi, part(j, 1), s.f);
+        } else {
+          i4_digits(lo, b[j * 6], b[j * 6 + 1], s.f);
+          i4_digits(hi, b[j * 6 + 2], b[j * 6 + 3], s.f);
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          b[j * 6 + q * 2] = lo[q];
+          b[j * 6 + q * 2 + 1] = hi[q];
+        }
+      }
     };
     if (wide)
       convert(std::true_type{});

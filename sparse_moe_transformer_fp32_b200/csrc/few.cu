@@ -138,8 +138,8 @@ struct FewShared {
   uint32_t mask[kMaxE];                 // tokens of each expert
   uint8_t chosen[kFewMaxTokens][kMaxTopK];  // chosen experts of each token, ascending
   uint8_t entry_e[kFewMaxSlots];        // expert of each entry
-  uint8_t entry_n[kFewMaxSlots];        // its token columns, 1..8
-  uint8_t entry_slot[kFewMaxSlots][kFewCols];  // their slots, or kNoSlot
+  uint8_t entry_n[kFewMaxSlots];        // its token columns, 1..4
+  uint8_t entry_slot[kFewMaxSlots][kEntryMax];  // their slots, or kNoSlot
   int warp_entries[kFewWarps];
   alignas(16) uint8_t zeros[16];
   int n_entries, abort_flag;
@@ -232,13 +232,12 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, uint8_t* slo
 //   by_token: an entry's column t is token t (kNoSlot where the token has other experts), so that all
 //             entries share the token fragments of gate|up;
 //   else      its columns are its tokens, entry_max at most; one more opens a second entry that reads
-//             the weights again (with 8 to an entry and at most 16 tokens that takes a routing where
-//             more than half of them agree).
+//             the weights again (16 tokens that choose 8 of 64 experts at random: for 3 experts in 100).
 __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewShared& sh, bool by_token) {
   const int e = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kFewWarps * 32 == kMaxE, "a thread to an expert");
   uint32_t m = e < a.E ? sh.mask[e] : 0u;
-  const int shift = 31 - __clz(a.entry_max);  // 2, 4 or 8
+  const int shift = 31 - __clz(a.entry_max);  // 2 or 4 tokens
   const int need = by_token ? m != 0u : (__popc(m) + a.entry_max - 1) >> shift;
   int incl = need;
 #pragma unroll
@@ -283,7 +282,7 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
 // cross the GPU.  GROUP = 0: BF16 weights.  MODE: the arrangement of digits, 1 or 2 (0 for BF16).
 //
 // Bound by HBM, the bytes of the touched experts.  d = 5120, I = 2560, 64 experts, 8 chosen: BF16 1 token
-// 107 us and 16 tokens 680 (6.0 and 6.5 TB/s), 4-bit weights 8 tokens 167.  4-bit, 1 token, 41.6 us: 26 of
+// 109 us and 16 tokens 725 (5.9 and 6.1 TB/s), 4-bit weights 8 tokens 178.  4-bit, 1 token, 42 us: 26 of
 // them the bytes, 6 the selection and the first copies, 4 the exchange of the activations (the ring holds
 // 4 us of weights, and the slowest CTA's last rows take that long to reach everyone), 4 the combine.
 template <int GROUP, int MODE>
@@ -683,8 +682,8 @@ static_assert(sizeof(FewShared) <= 4096, "FewShared must fit beside the ring");
 // calls whose columns are not the tokens may reach into the partial-tile buffers behind: nothing uses
 // those before the selection is done.
 constexpr int kSmallestRing = kFewMaxStages * 2 * i4_unit_bytes(128);
-static_assert(16 * bf16_row_stride(4) >= 4 * i4_unit_bytes(128), "BF16 rings are twice as large at least");
-static_assert(kSlotTable + kEntryMax * kMaxE <= kSmallestRing && 2 * kSmallestRing > kSlotTable + kFewCols * kMaxE, "scores and slots must fit in the ring");
+static_assert(16 * bf16_row_stride(4) >= 2 * i4_unit_bytes(128), "BF16 rings are no smaller");
+static_assert(kSlotTable + kEntryMax * kMaxE <= kSmallestRing, "scores and slots must fit in the ring");
 static_assert(kFewMaxTokens * kMaxE * 9 <= kSmallestRing + kFewRed * kFewWarps * 512,
               "scores and slots must fit in the ring and the partial-tile buffers");
 
@@ -702,9 +701,10 @@ int few_router_tokens(int d) { return (kRtSmemMax - kRtExperts * d * 4) / (d * 2
 
 cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
-  // Tokens of an entry: with 4-bit weights 4 (2 alone, or where the digits of 4 do not fit in a warp's
-  // registers).  8 to an entry read the weights of an expert of 5 to 8 tokens once, but every product
-  // then takes three MMAs instead of two: 16 tokens over 64 experts 267 us, with 4 to an entry 249.
+  // Tokens of an entry: 4, or with 4-bit weights 2 where there are no more or the digits of 4 do not fit in
+  // a warp's registers.  With 8 the weights of an expert of 5 to 8 tokens are read once, but every 4-bit
+  // product then takes three MMAs instead of two (16 tokens over 64 experts 267 us, with 4 to an entry 249),
+  // and with BF16 weights the activations' second pieces have no columns.
   a.entry_max = group && (a.T <= 2 || a.d > 5120 || a.I > 5120) ? 2 : kEntryMax;
   const int step = group ? 2 : 1;  // tiles
   a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
