@@ -414,7 +414,7 @@ BEAM_API size_t beam_moe_few_workspace_size(const beam_moe_shape* shape);
  * where d > 5632): the same arguments and definition, with ws sized by beam_moe_few_workspace_size.  The
  * router's sums run in FP64 and are rounded once to FP32, so topk_idx is the definition's also on near
  * ties.  Activations between an expert's two products and expert outputs stay FP32 (the activations
- * enter the second product as two BF16 pieces) until the combine's sum is rounded to BF16: closer to
+ * enter the second product as three BF16 pieces) until the combine's sum is rounded to BF16: closer to
  * the definition than beam_moe_forward, which rounds both to BF16.  Results do not depend on timing.
  * The second launch is cooperative: it needs every SM for itself and runs when they are free. */
 BEAM_API beam_status beam_moe_forward_few(const beam_moe_shape* shape, const void* hidden,

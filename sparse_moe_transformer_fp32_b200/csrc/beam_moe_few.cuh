@@ -409,94 +409,147 @@ __device__ __forceinline__ uint32_t stage_row(const uint4 (&v)[kRowLoads], bool 
   }
   return top;
 }
-// Stages an FP32 row of n elements as two BF16 pieces (16 bits: off by at most 2^-17; beyond BF16's range
-// the second is zero), the second ones n elements on.
-__device__ __forceinline__ void stage_pieces(const uint4 (&v)[kRowLoads], int n, uint8_t* raw, int lane) {
+// Stages the first two of the three BF16 pieces of an FP32 row of n elements, the second ones n elements on,
+// and keeps the third in v's first two words.  Each piece is the rest's rounding to BF16, 8 bits and a sign,
+// so that the three hold all 24 bits of an element of at least 2^-110 (smaller ones lose what lies below
+// BF16's smallest step, 2^-133); beyond BF16's range the others are zero.
+__device__ __forceinline__ void stage_pieces(uint4 (&v)[kRowLoads], int n, uint8_t* raw, int lane) {
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
     const int k = (i * 32 + lane) * 4;
     if (k < n) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t hi[2], lo[2];
+      uint32_t p[3][2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float x = __uint_as_float(w[j * 2]), y = __uint_as_float(w[j * 2 + 1]);
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        hi[j] = *reinterpret_cast<const uint32_t*>(&h);
-        const float hx = bf16_lo(hi[j]), hy = bf16_hi(hi[j]);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(fabsf(hx) < kInfinity ? x - hx : 0.f,
-                                                       fabsf(hy) < kInfinity ? y - hy : 0.f);
-        lo[j] = *reinterpret_cast<const uint32_t*>(&l);
+        float x = __uint_as_float(w[j * 2]), y = __uint_as_float(w[j * 2 + 1]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+          p[q][j] = *reinterpret_cast<const uint32_t*>(&h);
+          const float hx = bf16_lo(p[q][j]), hy = bf16_hi(p[q][j]);
+          x = fabsf(hx) < kInfinity ? x - hx : 0.f;  // exact
+          y = fabsf(hy) < kInfinity ? y - hy : 0.f;
+        }
       }
-      *reinterpret_cast<uint2*>(raw + k * 2) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(raw + (n + k) * 2) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(raw + k * 2) = make_uint2(p[0][0], p[0][1]);
+      *reinterpret_cast<uint2*>(raw + (n + k) * 2) = make_uint2(p[1][0], p[1][1]);
+      v[i].x = p[2][0];
+      v[i].y = p[2][1];
     }
   }
 }
+__device__ __forceinline__ void stage_third(const uint4 (&v)[kRowLoads], int n, uint8_t* raw, int lane) {
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) {
+    const int k = (i * 32 + lane) * 4;
+    if (k < n) *reinterpret_cast<uint2*>(raw + k * 2) = make_uint2(v[i].x, v[i].y);
+  }
+}
 
-// B fragments of the K slices of BF16 tokens (n elements), 4 registers per 32 elements.  Column t is
-// token t, up to 8; wide: up to 4 FP32 tokens, columns t and 4 + t their two pieces.  row(t): the
-// slice's first element of token t, or null (a column of zeros).
+// B fragments of the K slices of tokens, n elements each, 4 registers per 32 elements and set of 8 columns.
+//   BF16 rows         one set, column t is token t, up to 8
+//   FP32 rows (wide)  column 2 p + t % 2 of set t / 2 is piece p of token t; one set for up to 2 tokens,
+//                     for up to 4 a second one whose registers are those of runs RUNS / 2 and on
+// row(t): the slice's first element of token t, or null (columns of zeros).
 template <int RUNS, int REGS, class Row>
 __device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& src, Row row, bool wide, int tokens,
                                             int n, uint8_t* raw, const uint8_t* zeros, int lane) {
   static_assert(RUNS * 4 <= REGS, "the fragments must fit");
   const int g = lane >> 2, c = lane & 3, bytes = n * (wide ? 4 : 2);
+  const bool two = wide && tokens > 2;
   uint4 v[kRowLoads];
   const void* next = row(0);
   fetch_row(v, next, bytes, lane);
 #pragma unroll 1
   for (int t = 0; t < tokens; ++t) {
     const void* from = next;
-    if (from != nullptr) {
-      settle_row(v, src, from, bytes, lane);
-      if (wide)
-        stage_pieces(v, n, raw, lane);
-      else
-        stage_row(v, false, bytes, raw, lane);
-    }
-    __syncwarp();
-    next = t + 1 < tokens ? row(t + 1) : nullptr;
-    fetch_row(v, next, bytes, lane);
-    const bool mine = (wide ? g & 3 : g) == t && from != nullptr;
-    if (mine || t == 0) {  // the first token also clears the other columns
-      const uint8_t* p = mine ? raw + (wide ? (g >> 2) * n * 2 : 0) + c * 16 : zeros;
-      const int step = mine ? 64 : 0;
+    if (from != nullptr) settle_row(v, src, from, bytes, lane);
+    // FP32: two of the pieces, then in their place the third
+#pragma unroll 1
+    for (int pass = 0; pass < (wide ? 2 : 1); ++pass) {
+      if (from != nullptr) {
+        if (pass)
+          stage_third(v, n, raw, lane);
+        else if (wide)
+          stage_pieces(v, n, raw, lane);
+        else
+          stage_row(v, false, bytes, raw, lane);
+      }
+      __syncwarp();
+      if (pass == (wide ? 1 : 0)) {
+        next = t + 1 < tokens ? row(t + 1) : nullptr;
+        fetch_row(v, next, bytes, lane);
+      }
+      const int piece = g >> 1;
+      const bool mine = from != nullptr && (wide ? (g & 1) == (t & 1) && (pass ? piece == 2 : piece < 2) : g == t);
+      const bool clear = t == 0 && pass == 0;  // the first token also clears the other columns
+      if (mine || clear) {
+        const uint8_t* p = mine ? raw + (wide && !pass ? piece * n * 2 : 0) + c * 16 : zeros;
+        const int step = mine ? 64 : 0;
 #pragma unroll
-      for (int j = 0; j < RUNS; ++j) {
-        if (j * 32 < n) {
-          const uint4 w = *reinterpret_cast<const uint4*>(p + j * step);
-          b[j * 4 + 0] = w.x;
-          b[j * 4 + 1] = w.y;
-          b[j * 4 + 2] = w.z;
-          b[j * 4 + 3] = w.w;
+        for (int half = 0; half < 2; ++half) {  // two sets: half of the registers each
+          const bool other = two && half != t >> 1;  // not the token's set
+          const int left = two ? (!other || clear ? n : 0) : n - half * (RUNS / 2) * 32;
+          const int first = two ? 0 : half * (RUNS / 2) * step, each = other ? 0 : step;
+          const uint8_t* from_half = other ? zeros : p + first;
+#pragma unroll
+          for (int j = 0; j < RUNS / 2; ++j) {
+            if (j * 32 < left) {
+              const uint4 w = *reinterpret_cast<const uint4*>(from_half + j * each);
+              uint32_t* f = b + (half * (RUNS / 2) + j) * 4;
+              f[0] = w.x;
+              f[1] = w.y;
+              f[2] = w.z;
+              f[3] = w.w;
+            }
+          }
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
-// acc += 16 BF16 weight rows (`base`: row 0 of the warp's slice, rows `stride` bytes apart) times
-// the token columns, over `runs` runs of 32 K elements.
-template <int RUNS>
-__device__ __forceinline__ void bf16_slice(float (&acc)[4], const uint32_t (&b)[RUNS * 4],
+// acc[s] += 16 BF16 weight rows (`base`: row 0 of the warp's slice, rows `stride` bytes apart) times
+// set s of token columns, over `runs` runs of 32 K elements.  The registers of set s begin at those of run
+// s RUNS.
+template <int RUNS, int SETS, int REGS>
+__device__ __forceinline__ void bf16_slice(float (&acc)[SETS][4], const uint32_t (&b)[REGS],
                                            uint32_t base, int stride, int runs, int lane) {
+  static_assert(SETS * RUNS * 4 <= REGS, "the fragments must fit");
   const uint32_t lo = base + (lane >> 2) * stride + (lane & 3) * 16;
   const uint32_t hi = lo + 8 * stride;
-  float d0[4] = {}, d1[4] = {};  // two chains of dependent MMAs
+  float d0[SETS][4] = {}, d1[SETS][4] = {};  // chains of dependent MMAs
 #pragma unroll
   for (int j = 0; j < RUNS; ++j) {
     if (j < runs) {
       const uint4 r = lds128(lo + j * 64), s = lds128(hi + j * 64);
-      mma_bf16(d0, r.x, s.x, r.y, s.y, b[j * 4], b[j * 4 + 1]);
-      mma_bf16(d1, r.z, s.z, r.w, s.w, b[j * 4 + 2], b[j * 4 + 3]);
+#pragma unroll
+      for (int q = 0; q < SETS; ++q) {
+        const uint32_t* f = b + (q * RUNS + j) * 4;
+        mma_bf16(d0[q], r.x, s.x, r.y, s.y, f[0], f[1]);
+        mma_bf16(d1[q], r.z, s.z, r.w, s.w, f[2], f[3]);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] += d0[i] + d1[i];
+  for (int q = 0; q < SETS; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[q][i] += d0[q][i] + d1[q][i];
 }
 
+// Sum over the three pieces of each token: on every lane, what columns 0 and 1 of the result hold.  The
+// columns behind the third piece are zero.
+__device__ __forceinline__ float4 sum_pieces(float4 v) {
+  float* o = &v.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);  // third piece to the first, zeros to the second
+    o[i] += __shfl_xor_sync(0xffffffffu, o[i], 1);
+  }
+  return v;
+}
 
 // Products with 4-bit weights run on INT8 MMAs for up to 8 tokens.  A code block of 16 rows x 64
 // columns takes 22 clocks of an SM to arrive (528 bytes at 6.5 TB/s over the GPU), and expanding it

@@ -128,7 +128,7 @@ constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..24
 
 constexpr uint8_t kNoSlot = 255;
 constexpr int kEntryMax = 4;  // tokens of an entry, at most
-static_assert(kEntryMax * 2 == kFewCols, "both BF16 pieces of an entry's activations are columns");
+static_assert(kEntryMax * 3 <= 2 * kFewCols, "the BF16 pieces of an entry's activations are columns of two MMAs");
 constexpr int kSlotTable = kFewMaxTokens * kMaxE * 8;  // offset in the ring, behind the scores
 
 struct FewShared {
@@ -417,7 +417,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           continue;
         }
         len = step_len(last - it, per - tile);
-        float4 part[kStep] = {};  // of each tile: rows g, g of two tokens, then g + 8
+        // of each tile: rows g, g of two tokens, then g + 8; BF16 weights: of each set of columns
+        float4 part[2] = {};
+        static_assert(kStep <= 2, "parts");
+        const bool two_sets = !kI4 && ph > 0 && sh.entry_n[entry] > 2;
         bool red_seen = false;
         if (!kI4) red_seen = mbar_test_wait(smem_u32(&sh.red_empty[rb]), rpar);
         // every warp passes every chunk in order: a phase may only be waited for by who has seen
@@ -447,9 +450,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
 #pragma unroll
               for (int r = 0; r < kStep; ++r) part[r] = i4_result(acc[r], factor, lane);
             } else {
-              float acc[4] = {};
-              bf16_slice<kRuns>(acc, b, base, stride, units, lane);
-              part[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+              if (two_sets) {
+                float acc[2][4] = {};
+                bf16_slice<kRuns / 2>(acc, b, base, stride, units, lane);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) part[r] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+              } else {
+                float acc[1][4] = {};
+                bf16_slice<kRuns>(acc, b, base, stride, units, lane);
+                part[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+              }
             }
           }
           __syncwarp();
@@ -457,6 +467,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           slot = next;
         }
         if (!ok) break;
+        if (!kI4 && ph > 0) {
+          part[0] = sum_pieces(part[0]);
+          // both sets go into one partial tile: lanes c = 0 keep tokens 0 and 1, lanes c = 1 the others
+          if (two_sets) {
+            const float4 other = sum_pieces(part[1]);
+            if (lane & 1) part[0] = other;
+          }
+        }
         ok = mbar_wait_seen(red_seen, smem_u32(&sh.red_empty[rb]), rpar, abort_flag, a.wait_limit_ns, a.status,
                             kWhereFew + 3);
         if (!ok) break;
@@ -589,12 +607,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.red_empty[rb]));
           const int n = sh.entry_n[entry];
-          if (!kI4 && ph > 0) {  // the products of the second pieces are two lanes on
-            v[0].x += __shfl_xor_sync(0xffffffffu, v[0].x, 2);
-            v[0].y += __shfl_xor_sync(0xffffffffu, v[0].y, 2);
-            v[0].z += __shfl_xor_sync(0xffffffffu, v[0].z, 2);
-            v[0].w += __shfl_xor_sync(0xffffffffu, v[0].w, 2);
-          }
 #pragma unroll
           for (int r = 0; r < kStep; ++r) {
             if (r >= len) break;
@@ -701,11 +713,11 @@ int few_router_tokens(int d) { return (kRtSmemMax - kRtExperts * d * 4) / (d * 2
 
 cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s) {
   const int unit = group ? kI4Unit : kBf16Unit, unit_bytes = group ? i4_unit_bytes(group) : 0;
-  // Tokens of an entry: 4, or with 4-bit weights 2 where there are no more or the digits of 4 do not fit in
-  // a warp's registers.  With 8 the weights of an expert of 5 to 8 tokens are read once, but every 4-bit
-  // product then takes three MMAs instead of two (16 tokens over 64 experts 267 us, with 4 to an entry 249),
-  // and with BF16 weights the activations' second pieces have no columns.
-  a.entry_max = group && (a.T <= 2 || a.d > 5120 || a.I > 5120) ? 2 : kEntryMax;
+  // Tokens of an entry: 4, or 2 where the registers of a warp do not hold the fragments of 4 (the three
+  // pieces of FP32 activations; the digits of 4-bit products, and there also where there are no more
+  // tokens).  With 8 the weights of an expert of 5 to 8 tokens are read once, but every 4-bit product then
+  // takes three MMAs instead of two (16 tokens over 64 experts 267 us, with 4 to an entry 249).
+  a.entry_max = (group ? a.T <= 2 || a.d > 5120 || a.I > 5120 : a.I > kFewMaxK / 2) ? 2 : kEntryMax;
   const int step = group ? 2 : 1;  // tiles
   a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);
   a.k2 = make_ksplit(a.I / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);

@@ -363,3 +363,48 @@ def test_beam_layer(group):
         out, idx, w, _ = m.run(h)
         assert T == 1 or int(idx.max()) > 200
         m.check(h, out, idx, w)
+
+
+def pair_layer(T, I, k, E):
+    """Experts whose activations come in nearly equal pairs, with outputs that are their differences.  Gate
+    and up sums hold two terms, exact in FP32, and a pair's differ by 2^-16: what is lost of an activation
+    on its way into the second product shows in the output."""
+    d = 256
+    m = Layer(d, E, 1, 1, k, I, bias=torch.linspace(1, 0, E, device="cuda"))
+    h = torch.zeros(T, d, device="cuda", dtype=torch.bfloat16)
+    h[:, 0] = 1.0 + torch.arange(T, device="cuda") / 64
+    h[:, 1] = 2.0 ** -8
+    for w in (m.gate, m.up, m.down):
+        w.zero_()
+    m.gate[..., 0] = normal(31, E, I // 2, std=0.7).abs().clamp(0.25, 2).repeat_interleave(2, dim=1)
+    m.up[..., 0] = normal(32, E, I // 2).abs().clamp(0.5, 2).repeat_interleave(2, dim=1)
+    m.up[:, 0::2, 1] = 1.0
+    m.up[:, 1::2, 1] = 1.0 + 2.0 ** -7
+    r = torch.arange(d, device="cuda")
+    pair = r * (I // 2) // d
+    m.down[:, r, 2 * pair] = 1.0
+    m.down[:, r, 2 * pair + 1] = -1.0
+    return m, h
+
+
+@pytest.mark.parametrize("T,I,k", [(1, 128, 1), (2, 384, 3), (3, 128, 1), (4, 256, 2), (5, 1280, 1), (16, 128, 2),
+                                   (4, 4096, 1), (3, 4224, 1), (7, 8192, 2)])
+def test_bf16_layer_keeps_every_bit_of_the_activation(T, I, k):
+    m, h = pair_layer(T, I, k, 4)
+    out, idx, w, _ = m.run(h)
+    ridx, rw = R.route_ref(h, m.router_w, m.bias, 1, 1, k)
+    assert torch.equal(idx.cpu().long(), ridx)
+    x = h.double()
+    ref, mag = torch.zeros_like(x), torch.zeros_like(x)
+    for t in range(T):
+        for j in range(k):
+            e, wt = int(ridx[t, j]), rw[t, j].item()
+            g, u = m.gate[e].double() @ x[t], m.up[e].double() @ x[t]
+            a = g * torch.sigmoid(g) * u
+            ref[t] += wt * (m.down[e].double() @ a)
+            mag[t] += wt * (m.down[e].double().abs() @ a.abs())
+    # of each activation: its product's rounding (the SiLU's error is the pair's alike, 8 half steps of the
+    # difference), and one each of the three columns' sums and the two additions of columns; then the
+    # weights' and the combine's roundings, and the output's
+    bound = 8 * R.U32 * mag + 16 * R.U32 * ref.abs() + R.U16 * ref.abs()
+    R.assert_within(out, ref, bound + 1e-37, f"T={T} I={I} k={k}")
