@@ -160,7 +160,7 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, uint8_t* slo
     for (int j = 0; j < P; ++j) {
       const float v = sc[lane * P + jj].y;
       if (++jj == P) jj = 0;
-      n += v - v;  // NaN if a score is NaN (or infinite)
+      n = v != v ? v : n;  // NaN if a score is; infinities (a bias of -inf masks an expert) have their order
       m2 = fmaxf(m2, fminf(m1, v));
       m1 = fmaxf(m1, v);
     }

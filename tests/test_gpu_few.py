@@ -408,3 +408,48 @@ def test_bf16_layer_keeps_every_bit_of_the_activation(T, I, k):
     # weights' and the combine's roundings, and the output's
     bound = 8 * R.U32 * mag + 16 * R.U32 * ref.abs() + R.U16 * ref.abs()
     R.assert_within(out, ref, bound + 1e-37, f"T={T} I={I} k={k}")
+
+
+MASKS = {  # of 32 experts in 4 groups: one expert; all but one of a group; a group; one of each group; all but two of each
+    "one": [5], "all but one of a group": list(range(1, 8)), "a group": list(range(8, 16)),
+    "one of each group": [0, 9, 18, 27], "all but two of each": [e for e in range(32) if e % 8 not in (2, 5)]}
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("T", [1, 3, 6, 16])
+@pytest.mark.parametrize("mask", MASKS)
+def test_a_bias_of_minus_infinity_masks_experts(mask, T, group):
+    bias = normal(2, 32, std=0.05, dtype=torch.float32)
+    bias[MASKS[mask]] = -float("inf")
+    m = Layer(512, 32, 4, 2, 4, 128, group, bias=bias)
+    h = normal(3, T, 512)
+    out, idx, w, _ = m.run(h)
+    assert not torch.isin(idx.cpu(), torch.tensor(MASKS[mask])).any()
+    m.check(h, out, idx, w)
+    # and as in the many-token layer, whose experts' outputs are not looked at here
+    oidx, ow = torch.empty_like(idx), torch.empty_like(w)
+    bm.beam_moe_route(m.shape(T), h, m.router_w, m.bias, oidx, ow)
+    torch.cuda.synchronize()
+    assert torch.equal(idx, oidx)
+
+
+def test_masked_experts_fill_up_where_no_other_is_left():
+    """All groups but one masked and more experts to choose than are left open: the lowest masked ones."""
+    bias = torch.full((32,), -float("inf"), device="cuda")
+    bias[[17, 21]] = 0.0
+    m = Layer(512, 32, 4, 2, 4, 128, bias=bias)
+    h = normal(3, 5, 512)
+    out, idx, w, _ = m.run(h)
+    assert (idx.cpu() == torch.tensor([0, 1, 17, 21])).all()
+    m.check(h, out, idx, w)
+
+
+def test_a_bias_of_plus_infinity_forces_experts():
+    bias = normal(2, 32, std=0.05, dtype=torch.float32)
+    bias[[6, 30]] = float("inf")
+    bias[[1, 2, 3]] = -float("inf")
+    m = Layer(512, 32, 4, 2, 4, 128, bias=bias)
+    h = normal(3, 7, 512)
+    out, idx, w, _ = m.run(h)
+    assert (idx == 6).any(dim=1).all() and (idx == 30).any(dim=1).all()
+    m.check(h, out, idx, w)
