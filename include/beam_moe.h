@@ -398,8 +398,8 @@ BEAM_API size_t beam_dense_int4_workspace_size(const beam_dense_shape* shape);
 
 /* beam_dense_forward with 4-bit weights, T <= BEAM_FEW_MAX_TOKENS, I <= BEAM_INT4_MAX_K: gate_up
  * packed from (w_gate, w_up) [1, I, d], down from w_down [1, d, I], both with group_size.  Two
- * launches.  The activation between the products is FP32 for up to 8 tokens, BF16 beyond (as in
- * beam_dense_forward).  ws holds the activation only: beam_moe_sync_status does not apply to it
+ * launches, three for more than 8 tokens.  The activation between the products stays FP32 (in
+ * beam_dense_forward it is BF16).  ws holds the activation only: beam_moe_sync_status does not apply to it
  * (errors as in beam_int4_linear: NaN outputs). */
 BEAM_API beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int32_t group_size,
                                              const void* hidden, const void* gate_up,

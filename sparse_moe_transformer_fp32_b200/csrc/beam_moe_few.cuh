@@ -114,12 +114,12 @@ struct Int4QuantArgs {
   int group;
 };
 
-enum Int4Out { kI4OutBf16 = 0, kI4OutF32 = 1, kI4OutSwigluBf16 = 2, kI4OutSwigluF32 = 3 };
+enum Int4Out { kI4OutBf16 = 0, kI4OutF32 = 1, kI4OutSwiglu = 2 };
 
 struct Int4LinearArgs {
   const void* x;           // [T, K], BF16, or FP32 with wide
   const uint8_t* w;        // packed [tiles, K / 128, superblock]
-  void* out;               // [T, N] (SwiGLU: [T, N / 2], FP32 or BF16)
+  void* out;               // [T, N] (SwiGLU: FP32 [T, N / 2])
   uint64_t wait_limit_ns;
   int T, N, K, tiles;
   int out_kind;            // Int4Out

@@ -434,16 +434,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
         for (int h = 0; h < 2; ++h) {
           const int t = s * kFewCols + c * 2 + h;
           if (t >= a.T) continue;
-          if (a.out_kind >= kI4OutSwigluBf16) {  // row g: gate, row g + 8: up
+          if (a.out_kind == kI4OutSwiglu) {  // row g: gate, row g + 8: up
             const int n = tile * 8 + g;
-            const size_t o = static_cast<size_t>(t) * (a.N / 2) + n;
-            const float v = swiglu(lo[h], hi[h]);
-            if (n < a.N / 2) {
-              if (a.out_kind == kI4OutSwigluF32)
-                static_cast<float*>(a.out)[o] = v;
-              else
-                static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
-            }
+            if (n < a.N / 2)
+              static_cast<float*>(a.out)[static_cast<size_t>(t) * (a.N / 2) + n] = swiglu(lo[h], hi[h]);
           } else {
             const int n = tile * 16 + g;
             const size_t o = static_cast<size_t>(t) * a.N + n;

@@ -317,3 +317,21 @@ def test_wait_that_runs_out_shows_as_nan_and_the_context_survives(T, N, K):
     assert torch.equal(out[ok], good[ok])  # what is not NaN is right
     bm.beam_int4_linear(sh, x, packed, out)
     assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("T,d,I,group", [(9, 1024, 2816, 64), (12, 1024, 2816, 32), (16, 1024, 2816, 128),
+                                         (16, 2560, 640, 64), (11, 512, 8320, 64)])
+def test_dense_of_9_to_16_tokens_loses_nothing_before_the_output_is_rounded(T, d, I, group):
+    """As for up to 8 tokens: the whole error has the rounding's mean square to within some percent."""
+    h = normal(1, T, d)
+    g, u = (normal(s, 1, I, d, std=d ** -0.5) for s in (2, 3))
+    dn = normal(4, 1, d, I, std=I ** -0.5)
+    flat = torch.full((T + 2, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = flat[1:T + 1]
+    gu, dq = bm.beam_int4_quantize(g, u, group_size=group), bm.beam_int4_quantize(dn, group_size=group)
+    bm.beam_dense_forward_int4(bm.dense_shape(T, d, I), group, h, gu, dq, out)
+    assert (flat[0] == 7).all() and (flat[T + 1] == 7).all()
+    ref, bound = R.dense_ref(h, g[0], u[0], dn[0], group)
+    R.assert_within(out, ref, bound, f"T={T} d={d} I={I} g={group}")
+    rounding = (ref.to(torch.bfloat16).double() - ref).square().mean()
+    assert (out.double() - ref).square().mean() <= 1.1 * rounding
