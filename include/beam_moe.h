@@ -387,8 +387,7 @@ typedef struct {
  * workspace.  out may overlap neither input.
  * With no workspace there is no status word: a device-side wait that ran out (see
  * beam_moe_set_wait_limit_ns), which a healthy GPU never produces, shows as NaN in the outputs it
- * concerns.  The kernel may begin to read `packed` while the previous beam_int4_linear or
- * beam_dense_forward_int4 of the stream still runs; x is read and out written only after it. */
+ * concerns. */
 BEAM_API beam_status beam_int4_linear(const beam_int4_shape* shape, const void* x,
                                       const void* packed, void* out, int32_t out_fp32,
                                       beam_stream stream);

@@ -165,10 +165,12 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
 // 6.6 TB/s).  From 5 tokens on by the consumers: at 8 the three MMAs of a run alone take the time in which
 // its weights arrive (84 us), at 16 the expansion to BF16 and the waits between (133 us).
 //
-// Launched with programmatic stream serialisation: the producer starts on the weights while the
-// previous kernel of the stream drains; tokens are read, and outputs written, after
-// griddepcontrol.wait.  (Weights written by the previous kernel are safe: only kernels of this
-// kind let their successor start early, and they write no weights.)
+// Launched with programmatic stream serialisation, so that barriers are set up while the kernel before
+// drains.  Every warp that reads or writes global memory, the producer too, does so after
+// griddepcontrol.wait: whatever ran before may have let its successor start early and still be writing
+// these weights, and an ended kernel's writes are only sure to be seen after the wait.  (Weights copied
+// ahead of it gained nothing but on a second product of 55 MB, 1.2 us of 33.)  Since every CTA waits, the end
+// of a product is the end of all before it.
 
 // Superblocks per warp at most: 64 to 128 registers of token fragments.
 __host__ __device__ constexpr int lin_units(int mode) { return mode == 4 ? 4 : i4_mode_runs(mode) / 4; }
@@ -329,6 +331,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     int slot = 0;
     uint32_t par = 1, issued = 0;
     bool ok = true;
+    pdl_wait();
     for (int tile = tile0; tile < tile1 && ok; tile += STEP) {
       const int len = tile1 - tile < STEP ? tile1 - tile : STEP;
       const uint8_t* src = a.w + (static_cast<size_t>(tile) * units_all + u0) * kUnitBytes;

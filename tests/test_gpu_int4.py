@@ -335,3 +335,46 @@ def test_dense_of_9_to_16_tokens_loses_nothing_before_the_output_is_rounded(T, d
     R.assert_within(out, ref, bound, f"T={T} d={d} I={I} g={group}")
     rounding = (ref.to(torch.bfloat16).double() - ref).square().mean()
     assert (out.double() - ref).square().mean() <= 1.1 * rounding
+
+
+LATE_COPY = """
+extern "C" __global__ void late_copy(const unsigned* src, unsigned* dst, int n) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the successor may start now
+  for (long long t = clock64(); clock64() - t < 200000;) {}
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) dst[i] = src[i];
+}
+"""
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 1283, 1280), (12, 640, 20480)])
+def test_weights_written_by_a_kernel_that_lets_its_successor_start_early(T, N, K):
+    late = torch.cuda._compile_kernel(LATE_COPY, "late_copy")
+    x, old, new = normal(1, T, K), normal(2, 1, N, K, std=K ** -0.5), normal(3, 1, N, K, std=K ** -0.5)
+    src, packed = bm.beam_int4_quantize(new, group_size=64), bm.beam_int4_quantize(old, group_size=64)
+    out = torch.empty(T, N, device="cuda")
+    torch.cuda.synchronize()
+    late(grid=(32, 1, 1), block=(256, 1, 1), args=[src, packed, src.numel() // 4])
+    bm.beam_int4_linear(bm.int4_shape(T, N, K, 64), x, packed, out)
+    torch.cuda.synchronize()
+    ref, bound = R.linear_ref(x, new[0], 64, True)
+    R.assert_within(out, ref, bound, f"T={T} N={N} K={K}")
+
+
+@pytest.mark.parametrize("T", [3, 12])
+@pytest.mark.parametrize("which", ["gate_up", "down"])
+def test_dense_weights_written_by_a_kernel_that_lets_its_successor_start_early(which, T):
+    late = torch.cuda._compile_kernel(LATE_COPY, "late_copy")
+    d, I = 512, 1280
+    h = normal(1, T, d)
+    g, u = (normal(s, 1, I, d, std=d ** -0.5) for s in (2, 3))
+    dn = normal(4, 1, d, I, std=I ** -0.5)
+    packed = {"gate_up": bm.beam_int4_quantize(g, u, group_size=64), "down": bm.beam_int4_quantize(dn, group_size=64)}
+    src = packed[which].clone()
+    packed[which].zero_()
+    out = torch.empty(T, d, device="cuda", dtype=torch.bfloat16)
+    ws = bm.dense_int4_workspace(bm.dense_shape(T, d, I))
+    torch.cuda.synchronize()
+    late(grid=(32, 1, 1), block=(256, 1, 1), args=[src, packed[which], src.numel() // 4])
+    bm.beam_dense_forward_int4(bm.dense_shape(T, d, I), 64, h, packed["gate_up"], packed["down"], out, ws=ws)
+    torch.cuda.synchronize()
+    R.assert_within(out, *R.dense_ref(h, g[0], u[0], dn[0], 64), which)
