@@ -51,9 +51,9 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
        i += static_cast<int64_t>(gridDim.x) * kRtThreads)
     a.unwritten[i] = make_uint4(kUnwritten32, kUnwritten32, kUnwritten32, kUnwritten32);
   __syncthreads();
-  // a copy that never lands leaves the CTA's scores undefined; the layer kernel's waits do not
-  // depend on them
-  mbar_wait_bounded(smem_u32(&bar), 0, &abort_sh, a.wait_limit_ns ? a.wait_limit_ns : 1000000000ull, nullptr, 0);
+  const bool landed = a.wait_limit_ns == 0
+                          ? mbar_test_wait(smem_u32(&bar), 0)  // gives up at once
+                          : mbar_wait_bounded(smem_u32(&bar), 0, &abort_sh, a.wait_limit_ns, nullptr, 0);
   const float* W = reinterpret_cast<const float*>(rt_smem);
   const __nv_bfloat16* h = reinterpret_cast<const __nv_bfloat16*>(rt_smem + w_bytes);
   // warps: pairs of tokens, and parts of K while there are warps to spare
@@ -96,15 +96,23 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
     if (lane < 2 * kRtExperts)
       part[warp][lane] = lane == 0 ? acc[0][0] : lane == 1 ? acc[0][1] : lane == 2 ? acc[1][0] : acc[1][1];
   }
-  __syncthreads();
+  // After a wait that ran out the scores are marked as unwritten, and the layer kernel, which chooses such
+  // an expert before any other, reports it (the status words are only being cleared).
+  const bool lost = __syncthreads_or(!landed);
   if (threadIdx.x < kRtExperts * a.T) {
     const int j = threadIdx.x % kRtExperts, t = threadIdx.x / kRtExperts;
     double v = 0.0;
     for (int p = 0; p < 1 << log_parts; ++p)
       v += part[((t >> 1) << log_parts) + p][(t & 1) * kRtExperts + j];
     const float logit = static_cast<float>(v);
-    const float s = static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logit))));
-    a.sc[static_cast<size_t>(t) * a.E + e0 + j] = make_float2(s, s + a.bias[e0 + j]);
+    float s = static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logit))));
+    if (s != s) s = __uint_as_float(0x7fffffffu);  // not the mark
+    const float2 nan = make_float2(__uint_as_float(kUnwritten32), __uint_as_float(0x7fffffffu));
+    a.sc[static_cast<size_t>(t) * a.E + e0 + j] = lost ? nan : make_float2(s, s + a.bias[e0 + j]);
+  }
+  if (lost) {  // copies in flight must land before this CTA's shared memory is given up
+    volatile int never = 0;
+    mbar_wait_bounded(smem_u32(&bar), 0, &never, 2000000000ull, nullptr, 0);
   }
 }
 
@@ -124,7 +132,7 @@ __device__ __forceinline__ uint32_t score_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..24
+constexpr int kWhereFew = 20;  // status sites of the layer kernel: 20..26
 
 constexpr uint8_t kNoSlot = 255;
 constexpr int kEntryMax = 4;  // tokens of an entry, at most
@@ -219,6 +227,10 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, uint8_t* slo
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xffffffffu, s, j);
   if (lane < a.k) {
+    if (__float_as_uint(s) == kUnwritten32) {  // a wait of the router ran out: no CTA writes outputs
+      sh.abort_flag = 1;
+      record_status(a.status, kDevTimeout, kWhereFew + 6);
+    }
     const float w = a.norm ? a.scale * s / sum : a.scale * s;
     sh.wts[t * a.k + lane] = w;
     if (blockIdx.x == 0) {

@@ -453,3 +453,33 @@ def test_a_bias_of_plus_infinity_forces_experts():
     out, idx, w, _ = m.run(h)
     assert (idx == 6).any(dim=1).all() and (idx == 30).any(dim=1).all()
     m.check(h, out, idx, w)
+
+
+@pytest.mark.parametrize("T,d,I,group", [(1, 256, 128, 0), (10, 8192, 256, 0), (4, 5120, 2560, 64), (16, 512, 1280, 32)])
+def test_short_wait_limits_give_the_right_output_or_are_reported(T, d, I, group):
+    """Whichever wait runs out, the router's or one of the layer's: never a wrong output with BEAM_OK."""
+    m = Layer(d, 16, 4, 2, 4, I, group)
+    h = normal(5, T, d)
+    out, idx, w, ws = m.run(h)
+    want = out.clone()
+    old = bm.beam_moe_get_wait_limit_ns()
+    seen = set()
+    try:
+        for limit in (0, 0, 1, 500, 2000, 5000, 10_000, 20_000, 50_000, 100_000, 1_000_000):
+            bm.beam_moe_set_wait_limit_ns(limit)
+            out.fill_(7.0)
+            m.call(h, out, ws=ws)
+            status = bm.beam_moe_sync_status(ws)
+            assert status in (bm.BEAM_OK, bm.BEAM_ERR_TIMEOUT)
+            if status == bm.BEAM_OK:
+                assert torch.equal(out, want), limit
+            else:
+                seen.add(bm.last_cuda_error())
+    finally:
+        bm.beam_moe_set_wait_limit_ns(old)
+    assert seen  # a limit of 0 gives up at once
+    if d == 8192:  # 224 KB of copies a CTA are not there at once: the router's wait (site 26)
+        assert any("site 26" in s for s in seen), seen
+    m.call(h, out, ws=ws)
+    assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
+    assert torch.equal(out, want)
