@@ -22,11 +22,21 @@ namespace {
 // The kernel also clears the status words and marks as unwritten what the layer kernel exchanges.
 constexpr int kRtThreads = 256, kRtExperts = 2, kRtWarps = kRtThreads / 32;
 
-// FP32 to FP64: exponent rebiased by 896.  Zero and subnormals become values of at most 2^-126,
-// infinity and NaN values of at least 2^128 (such a token's outputs are NaN whatever its experts).
-__device__ __forceinline__ double widen(uint32_t u) {
-  const int hi = ((static_cast<int>(u) >> 3) & static_cast<int>(0x8fffffffu)) + 0x38000000;
-  return __hiloint2double(hi, static_cast<int>(u << 29));
+// x 2^-896 in FP64, exactly, zero and subnormals too: the exponent field as it is.  Infinity becomes what
+// 2^128 does (as large a logit); NaN, which also becomes a number, is looked for apart.
+constexpr double kUnscale = 0x1p+896;
+__device__ __forceinline__ double widen_scaled(uint32_t u) {
+  return __hiloint2double((static_cast<int>(u) >> 3) & static_cast<int>(0x8fffffffu), static_cast<int>(u << 29));
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterArgs a) {
@@ -62,7 +72,9 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
   const int pair = warp >> log_parts, t0 = pair * 2, t1 = t0 + 1 < a.T ? t0 + 1 : t0;
   const int span = a.d >> log_parts;
   if (pair < pairs) {
-    double acc[2][kRtExperts] = {};
+    double acc[2][kRtExperts] = {};  // of h and W 2^-896
+    uint32_t h_top[2] = {};
+    float w_top[kRtExperts] = {};
     const int k0 = (warp & ((1 << log_parts) - 1)) * span;
 #pragma unroll 1
     for (int k = k0 + lane * 4; k < k0 + span; k += 128) {
@@ -71,21 +83,31 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
       double hd[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        hd[t][0] = widen(x[t].x << 16);
-        hd[t][1] = widen(x[t].x & 0xffff0000u);
-        hd[t][2] = widen(x[t].y << 16);
-        hd[t][3] = widen(x[t].y & 0xffff0000u);
+        hd[t][0] = widen_scaled(x[t].x << 16) * kUnscale;
+        hd[t][1] = widen_scaled(x[t].x & 0xffff0000u) * kUnscale;
+        hd[t][2] = widen_scaled(x[t].y << 16) * kUnscale;
+        hd[t][3] = widen_scaled(x[t].y & 0xffff0000u) * kUnscale;
+        h_top[t] = max_nan_bf16x2(h_top[t], max_nan_bf16x2(x[t].x, x[t].y));
       }
 #pragma unroll
       for (int j = 0; j < kRtExperts; ++j) {
         const uint4 w = *reinterpret_cast<const uint4*>(W + j * a.d + k);
-        const double wd[4] = {widen(w.x), widen(w.y), widen(w.z), widen(w.w)};
+        const double wd[4] = {widen_scaled(w.x), widen_scaled(w.y), widen_scaled(w.z), widen_scaled(w.w)};
+        w_top[j] = max_nan(w_top[j], max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                                             max_nan(__uint_as_float(w.z), __uint_as_float(w.w))));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           acc[0][j] = fma(wd[i], hd[0][i], acc[0][j]);
           acc[1][j] = fma(wd[i], hd[1][i], acc[1][j]);
         }
       }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float top = max_nan(bf16_lo(h_top[t]), bf16_hi(h_top[t]));
+#pragma unroll
+      for (int j = 0; j < kRtExperts; ++j)
+        if (top != top || w_top[j] != w_top[j]) acc[t][j] = CUDART_NAN;
     }
 #pragma unroll 1
     for (int o = 16; o > 0; o >>= 1)
@@ -104,7 +126,7 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
     double v = 0.0;
     for (int p = 0; p < 1 << log_parts; ++p)
       v += part[((t >> 1) << log_parts) + p][(t & 1) * kRtExperts + j];
-    const float logit = static_cast<float>(v);
+    const float logit = static_cast<float>(v * kUnscale);
     float s = static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(logit))));
     if (s != s) s = __uint_as_float(0x7fffffffu);  // not the mark
     const float2 nan = make_float2(__uint_as_float(kUnwritten32), __uint_as_float(0x7fffffffu));

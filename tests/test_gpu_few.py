@@ -483,3 +483,60 @@ def test_short_wait_limits_give_the_right_output_or_are_reported(T, d, I, group)
     m.call(h, out, ws=ws)
     assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 9])
+def test_router_sums_of_zeros_and_huge_values(T):
+    """Zero weights with tokens of 2^120, and zero tokens with weights of 2^125: logits of exactly zero."""
+    m = Layer(256, 16, 4, 2, 4, 128, norm=False)
+    m.bias.zero_()
+    m.router_w.zero_()
+    m.gate.zero_()
+    h = (normal(3, T, 256).abs().double() * 2.0 ** 120).bfloat16()
+    out, idx, w, _ = m.run(h)
+    assert (w == 2.5 * 0.5).all() and (idx.cpu() == torch.arange(4)).all() and (out == 0).all()
+    m.router_w.fill_(2.0 ** 125)
+    out, idx, w, _ = m.run(torch.zeros_like(h))
+    assert (w == 2.5 * 0.5).all() and (idx.cpu() == torch.arange(4)).all() and (out == 0).all()
+    # zeros among others
+    h = normal(4, T, 256)
+    h[:, 1::2] = 0
+    m.router_w.copy_(normal(5, 16, 256, std=0.05, dtype=torch.float32))
+    m.router_w[:, 1::2] = 2.0 ** 125
+    m.gate.copy_(normal(6, 16, 128, 256, std=1 / 16))
+    out, idx, w, _ = m.run(h)
+    m.check(h, out, idx, w)
+
+
+def test_router_subnormals_count():
+    """Subnormal weights against tokens of 2^126: logits of 2^-5 for one expert, 2^-6 for the next."""
+    m = Layer(256, 4, 1, 1, 2, 128, norm=False)
+    m.bias.zero_()
+    m.router_w.zero_()
+    m.router_w[2, 9], m.router_w[1, 9] = 2.0 ** -131, 2.0 ** -132
+    m.gate.zero_()
+    h = torch.zeros(3, 256, device="cuda", dtype=torch.bfloat16)
+    h[:, 9] = 2.0 ** 126
+    out, idx, w, _ = m.run(h)
+    assert (idx.cpu() == torch.tensor([1, 2])).all()
+    want = 2.5 * torch.sigmoid(torch.tensor([2.0 ** -6, 2.0 ** -5], dtype=torch.float64))
+    assert ((w.cpu().double() - want).abs() <= 4 * R.U32 * want).all()
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_a_nan_router_row_is_not_hidden(group):
+    m = Layer(512, 16, 4, 2, 4, 128, group)
+    m.router_w[11, 100] = float("nan")
+    h = normal(3, 5, 512)
+    out, idx, w, _ = m.run(h)
+    assert (idx == 11).any(dim=1).all()
+    assert torch.isnan(out).all() and torch.isnan(w).all()
+
+
+def test_infinite_router_weights_decide():
+    m = Layer(512, 16, 4, 2, 4, 128)
+    m.router_w[11, 100], m.router_w[3, 200] = float("inf"), -float("inf")
+    h = normal(3, 8, 512)
+    assert (h[:, [100, 200]] != 0).all()
+    out, idx, w, _ = m.run(h)
+    m.check(h, out, idx, w)
