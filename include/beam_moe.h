@@ -355,7 +355,8 @@ BEAM_API beam_status beam_moe_bias_update(const beam_moe_shape* shape, const voi
  * In a code block, byte i (0..3) of 32-bit word v (0..3) of the 16 bytes at 16 (4g + c) (g 0..7,
  * c 0..3) holds the codes, in two's complement, of column 32 (v / 2) + 8c + 4 (v % 2) + i: row g in
  * the high four bits, row g + 8 in the low four.
- * Rows past the last are zero codes with zero scales.  Weights must be finite. */
+ * Rows past the last are zero codes with zero scales.  Weights must be finite and below 2^100 in
+ * magnitude (larger ones may overflow a product's intermediate sums). */
 #define BEAM_FEW_MAX_TOKENS 16
 #define BEAM_INT4_MAX_K 32768
 

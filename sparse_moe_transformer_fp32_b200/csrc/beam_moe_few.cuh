@@ -889,12 +889,14 @@ __device__ __forceinline__ float4 i4_result(const I4Acc<MODE>& acc, const I4Fact
 // ---- 9 to 16 tokens: BF16 MMAs, two sets of 8 columns (six INT8 MMAs of 4 clocks a run are slower:
 // 16 x 40960 x 5120 in 55 us, with these 42)
 
-// Two codes (two's complement, bits 0..3 and 16..19 of v) as exact BF16: with the sign bit inverted
-// a code is q + 8, 0x4300 | (q + 8) is the BF16 value 136 + q.
+// Two codes (two's complement, bits 0..3 and 16..19 of v) as exact BF16, q 2^-10: with the sign bit
+// inverted a code is q + 8, 0x3e00 | (q + 8) is the BF16 value (136 + q) 2^-10.  At 2^-10 a group's unscaled
+// sum (128 products with |q| <= 8) is no larger than the largest token element and cannot overflow.
+constexpr float kI4PairUnscale = 1024.f;
 __device__ __forceinline__ uint32_t i4_pair(uint32_t v) {
   uint32_t u, d;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(u) : "r"(v), "r"(0x000f000fu), "r"(0x43084308u));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(u), "r"(0x43084308u));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(u) : "r"(v), "r"(0x000f000fu), "r"(0x3e083e08u));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(u), "r"(0x3e083e08u));
   return d;
 }
 

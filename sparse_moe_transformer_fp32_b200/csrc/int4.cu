@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
 #pragma unroll
             for (int i = 0; i < STEP * 2; ++i) {
               const float* v = acc[i / 2][i % 2];
-              part[i] = make_float4(v[0], v[1], v[2], v[3]);
+              part[i] = make_float4(v[0] * kI4PairUnscale, v[1] * kI4PairUnscale, v[2] * kI4PairUnscale,
+                                    v[3] * kI4PairUnscale);
             }
           } else {
             I4Acc<MODE> acc[STEP] = {};

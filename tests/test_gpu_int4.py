@@ -378,3 +378,18 @@ def test_dense_weights_written_by_a_kernel_that_lets_its_successor_start_early(w
     bm.beam_dense_forward_int4(bm.dense_shape(T, d, I), 64, h, packed["gate_up"], packed["down"], out, ws=ws)
     torch.cuda.synchronize()
     R.assert_within(out, *R.dense_ref(h, g[0], u[0], dn[0], 64), which)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("T", [4, 8, 9, 16])
+def test_linear_of_tokens_whose_unscaled_sums_would_overflow(T, group):
+    """Elements up to 1e38 against weights of 0.04: the codes alone, up to 7, would take the sums of a group
+    beyond FP32; the outputs are 2^123 at most."""
+    x = normal(1, T, 512)
+    x[2, 200] = 1e38
+    x[3] = (normal(2, 512).double() * 2.0 ** 118).bfloat16()
+    x[0] = (normal(3, 512).double() * 2.0 ** -100).bfloat16()
+    x, w, _, out = run_linear(T, 80, 512, group, True, x=x)
+    ref, bound = R.linear_ref(x, w[0], group, True)
+    assert ref.abs().max() < 2.0 ** 124
+    R.assert_within(out, ref, bound)
