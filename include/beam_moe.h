@@ -323,8 +323,8 @@ BEAM_API beam_status beam_dense_forward_nvfp4(const beam_dense_shape* shape, con
                                               const float* down_scales, void* out, void* ws,
                                               size_t ws_bytes, beam_stream stream);
 
-/* Selection-bias update from the expert loads of the last beam_moe_forward / beam_moe_block
- * call made with `ws` (same shape):  bias[e] += gamma * sign(mean_load - load[e]), sign(0) = 0,
+/* Selection-bias update from the expert loads of the last beam_moe_forward / beam_moe_block call of any
+ * form (few-token ones included) made with `ws` (same shape):  bias[e] += gamma * sign(mean_load - load[e]), sign(0) = 0,
  * mean_load = T * top_k / E.  Under-loaded experts gain bias, over-loaded ones lose it; the
  * caller supplies gamma from its (e.g. cosine-decayed) schedule.
  * Cites: archdb "Beam-1.0-501B-A23B", load-balancing entry (auxiliary-loss-free bias with
@@ -528,7 +528,8 @@ BEAM_API const char* beam_status_string(beam_status status);
 /* Text of the last CUDA error seen by this library on the calling thread, or "". */
 BEAM_API const char* beam_moe_last_cuda_error(void);
 
-/* Per-expert token counts of the last forward/block call that used `ws` (synchronises
+/* Per-expert token counts of the last forward/block call that used `ws`, few-token forwards included
+ * (not beam_dense_forward_*, whose workspaces hold none; synchronises
  * `stream` and copies E int32 values to the HOST buffer counts_host). */
 BEAM_API beam_status beam_moe_expert_counts(const beam_moe_shape* shape, const void* ws,
                                    int32_t* counts_host, beam_stream stream);
@@ -537,7 +538,8 @@ BEAM_API beam_status beam_moe_expert_counts(const beam_moe_shape* shape, const v
  * call that used `ws` (synchronises `stream` and copies T * top_k int32 values, slot order as
  * topk_idx, to the HOST buffer rows_host).  Expert e owns rows off[e] .. off[e+1]-1, where
  * off is the exclusive prefix sum of the per-expert counts over ascending e, and inside them
- * its tokens sit in ascending token order: the layout is a function of the routing alone. */
+ * its tokens sit in ascending token order: the layout is a function of the routing alone.
+ * beam_moe_forward_few and _few_int4 have no such buffers: BEAM_ERR_WORKSPACE after one of them. */
 BEAM_API beam_status beam_moe_slot_rows(const beam_moe_shape* shape, const void* ws,
                                         int32_t* rows_host, beam_stream stream);
 

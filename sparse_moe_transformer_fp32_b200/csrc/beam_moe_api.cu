@@ -1222,7 +1222,7 @@ beam_status check_dense_int4(const beam_dense_shape* s, int32_t group_size) {
 }
 
 struct FewLayout {
-  size_t status, sc, act, y, total;
+  size_t status, cnt, sc, act, y, total;
 };
 
 beam_status check_few_shape(const beam_moe_shape* s) {
@@ -1233,7 +1233,7 @@ beam_status check_few_shape(const beam_moe_shape* s) {
   return BEAM_OK;
 }
 
-// Status words first, as in every workspace.
+// Status words first and the experts' counts behind them, as in every workspace of the layer.
 FewLayout plan_few(const beam_moe_shape& s) {
   FewLayout L{};
   size_t o = 0;
@@ -1244,6 +1244,7 @@ FewLayout plan_few(const beam_moe_shape& s) {
   };
   const size_t R = static_cast<size_t>(s.T) * s.top_k;
   L.status = take(256);
+  L.cnt = take(sizeof(int32_t) * s.E);
   L.sc = take(sizeof(float2) * s.T * s.E);
   L.act = take(sizeof(float) * R * s.I);
   L.y = take(sizeof(float) * R * s.d);
@@ -1298,6 +1299,7 @@ beam_status few_impl(const beam_moe_shape* shape, int32_t group_size, const void
   la.out = static_cast<__nv_bfloat16*>(out);
   la.idx = topk_idx;
   la.wts = topk_w;
+  la.cnt = at<int32_t>(ws, L.cnt);
   la.status = ra.status;
   la.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   la.T = shape->T;
@@ -1724,6 +1726,15 @@ beam_status beam_moe_slot_rows(const beam_moe_shape* shape, const void* ws, int3
   const Layout L = plan(*shape);
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
+  uint32_t mark = 0;
+  e = cudaMemcpy(&mark, at<uint32_t>(const_cast<void*>(ws), L.status) + kFewMarkWord, sizeof mark,
+                 cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (mark == kFewMark) {
+    std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error,
+                  "the last forward on this workspace was a few-token one, which has no slot rows");
+    return BEAM_ERR_WORKSPACE;
+  }
   e = cudaMemcpy(rows_host, static_cast<const char*>(ws) + L.rowmap,
                  sizeof(int32_t) * static_cast<size_t>(L.R), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e);

@@ -130,12 +130,17 @@ struct Int4LinearArgs {
   int stages, slot_bytes, stage_bytes;  // the last: of a warp's token buffer
 };
 
+// In the status region of a workspace whose last forward was a few-token one: it has the experts' counts
+// where every workspace does, and no slot rows.  (Other forwards clear the region.)
+constexpr int kFewMarkWord = 8;
+constexpr uint32_t kFewMark = 0x77656600u;
+
 struct FewRouterArgs {
   const __nv_bfloat16* h;  // [T, d]
   const float* W;          // [E, d]
   const float* bias;       // [E]
   float2* sc;              // [T, E] out: score, biased score
-  uint32_t* status;        // cleared (4 words)
+  uint32_t* status;        // cleared (4 words), and marked
   uint4* unwritten;        // what the layer kernel exchanges, set to all ones
   int64_t unwritten_n;     // in 16-byte units
   uint64_t wait_limit_ns;
@@ -153,6 +158,7 @@ struct FewLayerArgs {
   __nv_bfloat16* out;      // [T, d]
   int32_t* idx;            // [T, k] out, or null
   float* wts;              // [T, k] out, or null
+  int32_t* cnt;            // [E] out, tokens of each expert
   uint32_t* status;
   uint64_t wait_limit_ns;
   KSplit k1, k2;           // gate/up and down K slices

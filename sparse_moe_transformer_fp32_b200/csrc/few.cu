@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kRtThreads) few_router_kernel(const FewRouterA
     bulk_load(smem_u32(rt_smem) + w_bytes, a.h, h_bytes, smem_u32(&bar));
   }
   if (blockIdx.x == 0 && threadIdx.x < 4) a.status[threadIdx.x] = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 4) a.status[kFewMarkWord] = kFewMark;
   for (int64_t i = blockIdx.x * kRtThreads + threadIdx.x; i < a.unwritten_n;
        i += static_cast<int64_t>(gridDim.x) * kRtThreads)
     a.unwritten[i] = make_uint4(kUnwritten32, kUnwritten32, kUnwritten32, kUnwritten32);
@@ -271,6 +272,7 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
   const int e = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kFewWarps * 32 == kMaxE, "a thread to an expert");
   uint32_t m = e < a.E ? sh.mask[e] : 0u;
+  if (blockIdx.x == 0 && e < a.E) a.cnt[e] = __popc(m);
   const int shift = 31 - __clz(a.entry_max);  // 2 or 4 tokens
   const int need = by_token ? m != 0u : (__popc(m) + a.entry_max - 1) >> shift;
   int incl = need;

@@ -540,3 +540,34 @@ def test_infinite_router_weights_decide():
     assert (h[:, [100, 200]] != 0).all()
     out, idx, w, _ = m.run(h)
     m.check(h, out, idx, w)
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("T", [1, 4, 11, 16])
+def test_loads_and_the_bias_update_from_a_few_token_workspace(T, group):
+    m = Layer(512, 32, 4, 2, 4, 128, group)
+    out, idx, w, ws = m.run(normal(3, T, 512))
+    loads = torch.bincount(idx.flatten().cpu().long(), minlength=32)
+    assert torch.equal(bm.beam_moe_expert_counts(m.shape(T), ws).long(), loads)
+    want = m.bias.cpu() + 0.25 * torch.sign(T * 4 / 32 - loads.double()).float()
+    bm.beam_moe_bias_update(m.shape(T), ws, m.bias, 0.25)
+    torch.cuda.synchronize()
+    assert torch.equal(m.bias.cpu(), want)
+
+
+def test_slot_rows_are_refused_after_a_few_token_forward():
+    m = Layer(512, 32, 4, 2, 4, 128)
+    h = normal(3, 11, 512)
+    ws = bm.workspace(m.shape(11))  # larger than a few-token one
+    out, idx = torch.empty_like(h), torch.empty(11, 4, dtype=torch.int32, device="cuda")
+
+    def many():
+        bm.beam_moe_forward(m.shape(11), h, m.router_w, m.bias, m.gate, m.up, m.down, out, idx, ws=ws)
+        return bm.beam_moe_slot_rows(m.shape(11), ws)
+
+    rows = many()
+    m.call(h, out, ws=ws)
+    with pytest.raises(bm.BeamError) as e:
+        bm.beam_moe_slot_rows(m.shape(11), ws)
+    assert e.value.status == bm.BEAM_ERR_WORKSPACE and "few-token" in bm.last_cuda_error()
+    assert torch.equal(many(), rows)
