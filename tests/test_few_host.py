@@ -182,3 +182,34 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
     assert bm._one_device(5, _FakeTensor(0), None, _FakeTensor(0)) == 5
     with pytest.raises(ValueError, match="cuda:1"):
         bm._one_device(5, _FakeTensor(0), _FakeTensor(1))
+
+
+def test_workspaces_hold_fp32_activations(L):
+    s = bm.dense_shape(4, 512, 640)
+    assert int(L.beam_dense_int4_workspace_size(ctypes.byref(s))) >= 4 * 640 * 4
+    for T in (1, 8, 16):
+        n = int(L.beam_moe_few_workspace_size(ctypes.byref(beam(T))))
+        assert n >= T * 8 * (2560 + 5120) * 4 + T * 256 * 8 + 256 * 4
+
+
+class _OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on CUDA device `index`."""
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", self.index))
+
+    def get_device(self):
+        return self.index
+
+
+def test_launch_refuses_tensors_of_another_device(monkeypatch):
+    def entry(index):
+        t = torch.zeros(4).as_subclass(_OnDevice)
+        t.index = index
+        return t, torch.float32, "t", (4,)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    st, ptrs = bm._launch(5, entry(0), (None, torch.float32, "none", (4,), True), entry(0))
+    assert st == 5 and ptrs[1] is None and len(ptrs) == 3
+    for devices in ((1,), (1, 1), (0, 1), (1, 0)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            bm._launch(5, *(entry(d) for d in devices))

@@ -571,3 +571,34 @@ def test_slot_rows_are_refused_after_a_few_token_forward():
         bm.beam_moe_slot_rows(m.shape(11), ws)
     assert e.value.status == bm.BEAM_ERR_WORKSPACE and "few-token" in bm.last_cuda_error()
     assert torch.equal(many(), rows)
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("T,d", [(16, 5888), (11, 8192), (16, 8192)])
+def test_router_of_wide_layers_in_one_and_two_launches(T, d, group):
+    """16 token rows of 5888 do not fit beside the router's weights in shared memory, nor 11 of 8192."""
+    m = Layer(d, 16, 4, 2, 4, 128, group)
+    h = normal(9, T, d)
+    before = bm.beam_moe_launch_count()
+    out, idx, w, ws = m.run(h)
+    assert bm.beam_moe_launch_count() - before == 3
+    m.check(h, out, idx, w)
+    assert bm.beam_moe_expert_counts(m.shape(T), ws).sum() == T * 4
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("T,d,I", [(4, 512, 256), (5, 512, 256), (8, 512, 256), (9, 512, 256), (2, 5376, 256),
+                                   (3, 5376, 256), (5, 5376, 256), (2, 256, 4224), (3, 256, 4224), (5, 256, 4224)])
+def test_entries_of_the_same_experts_at_their_limits(T, d, I, group):
+    """An entry holds 4 tokens, 2 in wide layers; one more token of an expert opens another."""
+    bias = torch.zeros(8, device="cuda")
+    bias[[2, 7]] = 5.0
+    m = Layer(d, 8, 2, 2, 2, I, group, bias=bias)
+    h = normal(3, T, d)
+    out, idx, w, _ = m.run(h)
+    assert (idx.cpu() == torch.tensor([2, 7])).all()
+    m.check(h, out, idx, w)
+    one = torch.empty_like(out[:1])
+    for t in range(T):
+        m.call(h[t:t + 1].clone(), one)
+        assert torch.equal(one[0], out[t])
