@@ -7,6 +7,7 @@ library is missing this module raises instead of computing anything itself.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -441,6 +442,14 @@ def _launch(stream, *specs):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream), ptrs
 
 
+def _allocating_on(stream):
+    """Context for what a call allocates itself: memory freed on the current stream may still be written by
+    work queued there, so a call on another stream takes its own from that stream's pool."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
 def int4_shape(T, N, K, group_size=128) -> beam_int4_shape:
     return beam_int4_shape(T, N, K, group_size)
 
@@ -459,7 +468,9 @@ def beam_int4_quantize(a, b=None, group_size=128, out=None, stream=None):
     if n == 0:
         raise BeamError(BEAM_ERR_UNSUPPORTED, "beam_int4_packed_size")
     if out is None:
-        out = torch.empty((groups, n), dtype=torch.uint8, device=a.device)
+        _ptr(a, torch.bfloat16, "a")
+        with _allocating_on(stream):
+            out = torch.empty((groups, n), dtype=torch.uint8, device=a.device)
     st, (pa, pb, po) = _launch(stream, (a, torch.bfloat16, "a", a.shape),
                                (b, torch.bfloat16, "b", a.shape, True),
                                (out, torch.uint8, "out", (groups, n)))
@@ -500,7 +511,8 @@ def beam_dense_forward_int4(shape, group_size, hidden, gate_up, down, out, ws=No
     T, d, I = shape.T, shape.d, shape.I
     if ws is None:
         _ptr(hidden, torch.bfloat16, "hidden", (T, d))
-        ws = dense_int4_workspace(shape, hidden.device)
+        with _allocating_on(stream):
+            ws = dense_int4_workspace(shape, hidden.device)
     st, ptrs = _launch(stream, (hidden, torch.bfloat16, "hidden", (T, d)),
                        _packed(gate_up, "gate_up", 1, 2 * I, d, group_size),
                        _packed(down, "down", 1, d, I, group_size),
@@ -524,7 +536,8 @@ def beam_moe_forward_few(shape, hidden, router_w, bias, w_gate, w_up, w_down, ou
     T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
     if ws is None:
         _ptr(hidden, torch.bfloat16, "hidden", (T, d))
-        ws = few_workspace(shape, hidden.device)
+        with _allocating_on(stream):
+            ws = few_workspace(shape, hidden.device)
     st, ptrs = _launch(stream, (hidden, torch.bfloat16, "hidden", (T, d)),
                        (router_w, torch.float32, "router_w", (E, d)),
                        (bias, torch.float32, "bias", (E,)),
@@ -546,7 +559,8 @@ def beam_moe_forward_few_int4(shape, group_size, hidden, router_w, bias, gate_up
     T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
     if ws is None:
         _ptr(hidden, torch.bfloat16, "hidden", (T, d))
-        ws = few_workspace(shape, hidden.device)
+        with _allocating_on(stream):
+            ws = few_workspace(shape, hidden.device)
     st, ptrs = _launch(stream, (hidden, torch.bfloat16, "hidden", (T, d)),
                        (router_w, torch.float32, "router_w", (E, d)),
                        (bias, torch.float32, "bias", (E,)),

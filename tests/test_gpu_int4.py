@@ -393,3 +393,48 @@ def test_linear_of_tokens_whose_unscaled_sums_would_overflow(T, group):
     ref, bound = R.linear_ref(x, w[0], group, True)
     assert ref.abs().max() < 2.0 ** 124
     R.assert_within(out, ref, bound)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_quantize_on_another_stream_does_not_take_memory_that_is_still_written(as_handle):
+    """Memory freed on the current stream while a write to it is queued there."""
+    a = normal(1, 4, 512, 512)
+    want = bm.beam_int4_quantize(a, group_size=64)
+    side = torch.cuda.Stream()
+    old = torch.empty_like(want)
+    old.fill_(3)  # loads the kernel
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # 50 ms
+    old.fill_(3)
+    del old
+    got = bm.beam_int4_quantize(a, group_size=64, stream=side.cuda_stream if as_handle else side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_workspaces_of_calls_on_another_stream_come_from_its_pool():
+    T, d, I = 3, 512, 1280
+    h = normal(1, T, d)
+    g, u = (normal(s, 1, I, d, std=d ** -0.5) for s in (2, 3))
+    dn = normal(4, 1, d, I, std=I ** -0.5)
+    gu, dq = bm.beam_int4_quantize(g, u, group_size=64), bm.beam_int4_quantize(dn, group_size=64)
+    sh = bm.dense_shape(T, d, I)
+    layer = bm.make_shape(T, d, 4, 1, 1, 1, I)
+    router_w, bias = normal(5, 4, d, std=0.02, dtype=torch.float32), torch.zeros(4, device="cuda")
+    gu4, dq4 = gu.expand(4, -1).contiguous(), dq.expand(4, -1).contiguous()
+    w = [t.expand(4, -1, -1).contiguous() for t in (g, u, dn)]
+    out, side = torch.empty_like(h), torch.cuda.Stream()
+    calls = [
+        (lambda: bm.dense_int4_workspace(sh), lambda: bm.beam_dense_forward_int4(sh, 64, h, gu, dq, out, stream=side)),
+        (lambda: bm.few_workspace(layer),
+         lambda: bm.beam_moe_forward_few(layer, h, router_w, bias, *w, out, stream=side)),
+        (lambda: bm.few_workspace(layer),
+         lambda: bm.beam_moe_forward_few_int4(layer, 64, h, router_w, bias, gu4, dq4, out, stream=side))]
+    torch.cuda.synchronize()
+    for allocate, call in calls:
+        free = [allocate() for _ in range(4)]  # what the current stream's pool would hand out
+        at = [t.data_ptr() for t in free]
+        del free
+        ws = call()
+        torch.cuda.synchronize()
+        assert ws.data_ptr() not in at
