@@ -1190,6 +1190,7 @@ beam_status check_int4_linear(const beam_int4_shape* s) {
     return unsupported("4-bit weights: group_size must be 32, 64 or 128 and K a multiple of 128");
   if (s->T > kFewMaxTokens) return unsupported("4-bit products: at most 16 tokens");
   if (s->K > BEAM_INT4_MAX_K) return unsupported("4-bit products: K above BEAM_INT4_MAX_K");
+  if (s->N > INT32_MAX - 31) return unsupported("4-bit products: N above 2^31 - 32");  // whole tiles of rows
   return BEAM_OK;
 }
 
@@ -1321,7 +1322,9 @@ extern "C" {
 
 size_t beam_int4_packed_size(int64_t groups, int32_t rows, int32_t cols, int32_t group_size) {
   if (groups < 0 || rows <= 0 || !int4_group_ok(group_size, cols)) return 0;
-  return static_cast<size_t>(groups) * int4_bytes(rows, cols, group_size);
+  const size_t each = int4_bytes(rows, cols, group_size);
+  if (static_cast<size_t>(groups) > SIZE_MAX / each) return 0;
+  return static_cast<size_t>(groups) * each;
 }
 
 beam_status beam_int4_quantize(const void* a, const void* b, int64_t groups, int32_t rows,
@@ -1334,9 +1337,13 @@ beam_status beam_int4_quantize(const void* a, const void* b, int64_t groups, int
     return unsupported("4-bit weights: interleaving needs rows to be a multiple of 8");
   if (b && rows > (1 << 30)) return BEAM_ERR_UNSUPPORTED;
   if (groups == 0) return BEAM_OK;
+  const int32_t out_rows = b ? 2 * rows : rows;
+  const int64_t tiles = ceil_div(out_rows, 16), sbs = cols / kI4Unit;
+  // a warp to a superblock, 8 to a block; what is within the grid's limit is also within 64 bits below
+  if (groups > 8 * int64_t(0x7fffffff) / (tiles * sbs))
+    return unsupported("4-bit weights: more than 2^34 superblocks of 16 x 128 in one call");
   if (any_misaligned({a, packed}) || (b && !aligned16(b))) return BEAM_ERR_INVALID_ARG;
   const uint64_t in_bytes = static_cast<uint64_t>(groups) * rows * cols * 2;
-  const int32_t out_rows = b ? 2 * rows : rows;
   const uint64_t out_bytes = static_cast<uint64_t>(groups) * int4_bytes(out_rows, cols, group_size);
   if (ranges_overlap(packed, out_bytes, a, in_bytes) || ranges_overlap(packed, out_bytes, b, in_bytes))
     return BEAM_ERR_INVALID_ARG;
@@ -1346,10 +1353,9 @@ beam_status beam_int4_quantize(const void* a, const void* b, int64_t groups, int
   qa.packed = static_cast<uint8_t*>(packed);
   qa.rows = rows;
   qa.cols = cols;
-  qa.tiles = static_cast<int>(ceil_div(out_rows, 16));
-  qa.units = groups * qa.tiles * (cols / kI4Unit);
+  qa.tiles = static_cast<int>(tiles);
+  qa.units = groups * tiles * sbs;
   qa.group = group_size;
-  if (ceil_div(qa.units, 8) > 0x7fffffff) return BEAM_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   BEAM_LAUNCH(kKQuantizeInt4, st, launch_int4_quantize(qa, st));
   return BEAM_OK;

@@ -213,3 +213,21 @@ def test_launch_refuses_tensors_of_another_device(monkeypatch):
     for devices in ((1,), (1, 1), (0, 1), (1, 0)):
         with pytest.raises(ValueError, match="cuda:1"):
             bm._launch(5, *(entry(d) for d in devices))
+
+
+def test_sizes_beyond_64_bits_are_refused(L):
+    big = 1 << 31
+    assert bm.beam_int4_packed_size(1 << 62, 16, 128, 64) == 0
+    assert bm.beam_int4_packed_size(1 << 40, big - 1, big - 128, 64) == 0
+    assert bm.beam_int4_packed_size(1, big - 1, big - 128, 64) == (1 << 27) * ((1 << 24) - 1) * 1088
+    f = L.beam_int4_quantize
+    for groups, rows, cols in ((1 << 62, 16, 128), (1 << 40, big - 1, big - 128), (1 << 24, 1 << 15, 128),
+                               ((1 << 63) - 1, 1, 128)):
+        for b in (None, q(A + (1 << 30))):
+            if b and (rows % 8 or rows > 1 << 30):
+                continue
+            assert f(q(A), b, groups, rows, cols, 64, q(A + (1 << 46)), None) == bm.BEAM_ERR_UNSUPPORTED
+    s = bm.int4_shape(1, big - 16, 128, 64)
+    assert L.beam_int4_linear(ctypes.byref(s), q(A), q(A + (1 << 44)), q(A + (1 << 45)), 0,
+                              None) == bm.BEAM_ERR_UNSUPPORTED
+    assert "2^31" in bm.last_cuda_error()
