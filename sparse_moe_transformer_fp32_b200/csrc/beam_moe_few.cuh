@@ -927,66 +927,52 @@ __device__ __forceinline__ void i4_load_tokens16(uint32_t (&b)[RUNS * 8], Row ro
   }
 }
 
-template <int GROUP, int UNITS, int R, int REGS>
-__device__ __forceinline__ void i4_slice16_of(float (&acc)[R][2][4], const uint32_t (&b)[REGS], uint32_t base,
-                                              uint32_t apart, int lane) {
+template <int GROUP, int UNITS, int REGS>
+__device__ __forceinline__ void i4_slice16_of(float (&acc)[2][4], const uint32_t (&b)[REGS], uint32_t base, int lane) {
   constexpr int kUnitBytes = i4_unit_bytes(GROUP);
-  uint32_t codes[R], scales[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    codes[r] = base + r * apart + lane * 16;
-    scales[r] = base + r * apart + 1024 + (lane >> 2) * 4;
-  }
-  float d[R][2][4];
-  uint4 q[R];
+  const uint32_t codes = base + lane * 16, scales = base + 1024 + (lane >> 2) * 4;
+  float d[2][4];
+  uint4 q;
 #pragma unroll
   for (int j = 0; j < UNITS * 4; ++j) {  // runs of 32
     const int u = j / 4, run = j % 4;
     constexpr int kRunsPerGroup = GROUP / 32;
     const bool first = j % kRunsPerGroup == 0, last = j % kRunsPerGroup == kRunsPerGroup - 1;
-    if (run % 2 == 0) {
+    if (run % 2 == 0) q = lds128(codes + u * kUnitBytes + (run / 2) * 512);
 #pragma unroll
-      for (int r = 0; r < R; ++r) q[r] = lds128(codes[r] + u * kUnitBytes + (run / 2) * 512);
-    }
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = run % 2 ? (h ? q.w : q.z) : (h ? q.y : q.x);
+      const uint32_t a0 = i4_pair(w >> 4), a1 = i4_pair(w), a2 = i4_pair(w >> 12), a3 = i4_pair(w >> 8);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w = run % 2 ? (h ? q[r].w : q[r].z) : (h ? q[r].y : q[r].x);
-        const uint32_t a0 = i4_pair(w >> 4), a1 = i4_pair(w), a2 = i4_pair(w >> 12), a3 = i4_pair(w >> 8);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint32_t b0 = b[(j * 2 + nt) * 4 + h * 2], b1 = b[(j * 2 + nt) * 4 + h * 2 + 1];
-          if (first && h == 0)
-            mma_bf16_first(d[r][nt], a0, a1, a2, a3, b0, b1);
-          else
-            mma_bf16(d[r][nt], a0, a1, a2, a3, b0, b1);
-        }
+      for (int nt = 0; nt < 2; ++nt) {
+        const uint32_t b0 = b[(j * 2 + nt) * 4 + h * 2], b1 = b[(j * 2 + nt) * 4 + h * 2 + 1];
+        if (first && h == 0)
+          mma_bf16_first(d[nt], a0, a1, a2, a3, b0, b1);
+        else
+          mma_bf16(d[nt], a0, a1, a2, a3, b0, b1);
       }
     }
     if (last) {
+      const uint32_t s = lds32(scales + u * kUnitBytes + (run / kRunsPerGroup) * 32);
+      const float sc[2] = {bf16_lo(s), bf16_hi(s)};
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint32_t s = lds32(scales[r] + u * kUnitBytes + (run / kRunsPerGroup) * 32);
-        const float sc[2] = {bf16_lo(s), bf16_hi(s)};
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][nt][i] = fmaf(sc[i >> 1], d[r][nt][i], acc[r][nt][i]);
-      }
+        for (int i = 0; i < 4; ++i) acc[nt][i] = fmaf(sc[i >> 1], d[nt][i], acc[nt][i]);
     }
   }
 }
 
-template <int GROUP, int R, int REGS>
-__device__ __forceinline__ void i4_slice16(float (&acc)[R][2][4], const uint32_t (&b)[REGS], uint32_t base,
-                                           uint32_t apart, int units, int lane) {
+// acc[s] += one tile times set s of 8 token columns, in units of 2^-10.
+template <int GROUP, int REGS>
+__device__ __forceinline__ void i4_slice16(float (&acc)[2][4], const uint32_t (&b)[REGS], uint32_t base, int units,
+                                           int lane) {
   static_assert(REGS == 128, "four superblocks");
   switch (units) {
-    case 1: i4_slice16_of<GROUP, 1>(acc, b, base, apart, lane); break;
-    case 2: i4_slice16_of<GROUP, 2>(acc, b, base, apart, lane); break;
-    case 3: i4_slice16_of<GROUP, 3>(acc, b, base, apart, lane); break;
-    case 4: i4_slice16_of<GROUP, 4>(acc, b, base, apart, lane); break;
+    case 1: i4_slice16_of<GROUP, 1>(acc, b, base, lane); break;
+    case 2: i4_slice16_of<GROUP, 2>(acc, b, base, lane); break;
+    case 3: i4_slice16_of<GROUP, 3>(acc, b, base, lane); break;
+    case 4: i4_slice16_of<GROUP, 4>(acc, b, base, lane); break;
     default: break;
   }
 }

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
     const int units = ks.count(warp), mine = warp / ks.cw, chunks = ks.chunks();
     const int cstart = ks.start(mine * ks.cw);
     const uint32_t off = (ks.start(warp) - cstart) * kUnitBytes;
-    const uint32_t apart = (ks.start((mine + 1) * ks.cw) - cstart) * kUnitBytes;  // tiles in a slot
+    [[maybe_unused]] const uint32_t apart = (ks.start((mine + 1) * ks.cw) - cstart) * kUnitBytes;  // tiles in a slot
     uint32_t b[kUnits * 8 * MODE];
     [[maybe_unused]] I4Factor factor[2];
     pdl_wait();
@@ -287,12 +287,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) int4_linear_kernel(const Int4L
           // what the slot held before, and their sums are not stored.
           const uint32_t base = ring + slot * a.slot_bytes + off;
           if constexpr (MODE == 4) {
-            float acc[STEP][2][4] = {};
-            i4_slice16<GROUP>(acc, b, base, apart, units, lane);
-            if (STEP > 1) test();
+            static_assert(MODE < 4 || STEP == 1, "one tile to a step");
+            float acc[2][4] = {};
+            i4_slice16<GROUP>(acc, b, base, units, lane);
 #pragma unroll
-            for (int i = 0; i < STEP * 2; ++i) {
-              const float* v = acc[i / 2][i % 2];
+            for (int i = 0; i < 2; ++i) {
+              const float* v = acc[i];
               part[i] = make_float4(v[0] * kI4PairUnscale, v[1] * kI4PairUnscale, v[2] * kI4PairUnscale,
                                     v[3] * kI4PairUnscale);
             }
