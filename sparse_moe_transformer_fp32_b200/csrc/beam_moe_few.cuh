@@ -166,6 +166,7 @@ struct FewLayerArgs {
   float scale;
   int norm;
   int entry_max;           // tokens of an entry at most
+  int room;                // a warp's buffer holds all BF16 pieces of an activation row
   int stages, slot_bytes, stage_bytes;  // the last: of a warp's token buffer
 };
 
@@ -415,13 +416,14 @@ __device__ __forceinline__ uint32_t stage_row(const uint4 (&v)[kRowLoads], bool 
   }
   return top;
 }
-// Stages the first two of the three BF16 pieces of an FP32 row of n elements, the second ones n elements on,
-// and keeps the third in v's first two words.  Each piece is the rest's rounding to BF16, 8 bits and a sign,
+// Stages the three BF16 pieces of an FP32 row of n elements, each n elements behind the one before; without
+// room for the third, keeps it in v's first two words.  Each piece is the rest's rounding to BF16, 8 bits and a sign,
 // so that the three hold all 24 bits of an element of at least 2^-110 (smaller ones lose what lies below
 // BF16's smallest step, 2^-133); beyond BF16's range the others are zero.
-__device__ __forceinline__ void stage_pieces(uint4 (&v)[kRowLoads], int n, uint8_t* raw, int lane) {
+__device__ __forceinline__ void stage_pieces(uint4 (&v)[kRowLoads], int n, bool room, uint8_t* raw, int lane) {
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
+    if (i * 128 >= n) break;
     const int k = (i * 32 + lane) * 4;
     if (k < n) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -440,6 +442,7 @@ __device__ __forceinline__ void stage_pieces(uint4 (&v)[kRowLoads], int n, uint8
       }
       *reinterpret_cast<uint2*>(raw + k * 2) = make_uint2(p[0][0], p[0][1]);
       *reinterpret_cast<uint2*>(raw + (n + k) * 2) = make_uint2(p[1][0], p[1][1]);
+      if (room) *reinterpret_cast<uint2*>(raw + (2 * n + k) * 2) = make_uint2(p[2][0], p[2][1]);
       v[i].x = p[2][0];
       v[i].y = p[2][1];
     }
@@ -448,6 +451,7 @@ __device__ __forceinline__ void stage_pieces(uint4 (&v)[kRowLoads], int n, uint8
 __device__ __forceinline__ void stage_third(const uint4 (&v)[kRowLoads], int n, uint8_t* raw, int lane) {
 #pragma unroll
   for (int i = 0; i < kRowLoads; ++i) {
+    if (i * 128 >= n) break;
     const int k = (i * 32 + lane) * 4;
     if (k < n) *reinterpret_cast<uint2*>(raw + k * 2) = make_uint2(v[i].x, v[i].y);
   }
@@ -457,13 +461,15 @@ __device__ __forceinline__ void stage_third(const uint4 (&v)[kRowLoads], int n, 
 //   BF16 rows         one set, column t is token t, up to 8
 //   FP32 rows (wide)  column 2 p + t % 2 of set t / 2 is piece p of token t; one set for up to 2 tokens,
 //                     for up to 4 a second one whose registers are those of runs RUNS / 2 and on
-// row(t): the slice's first element of token t, or null (columns of zeros).
+// row(t): the slice's first element of token t, or null (columns of zeros).  room: whether the buffer holds
+// all pieces of a row.
 template <int RUNS, int REGS, class Row>
-__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& src, Row row, bool wide, int tokens,
-                                            int n, uint8_t* raw, const uint8_t* zeros, int lane) {
+__device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& src, Row row, bool wide, bool room,
+                                            int tokens, int n, uint8_t* raw, const uint8_t* zeros, int lane) {
   static_assert(RUNS * 4 <= REGS, "the fragments must fit");
   const int g = lane >> 2, c = lane & 3, bytes = n * (wide ? 4 : 2);
   const bool two = wide && tokens > 2;
+  const int passes = wide && !room ? 2 : 1;
   uint4 v[kRowLoads];
   const void* next = row(0);
   fetch_row(v, next, bytes, lane);
@@ -471,24 +477,24 @@ __device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& sr
   for (int t = 0; t < tokens; ++t) {
     const void* from = next;
     if (from != nullptr) settle_row(v, src, from, bytes, lane);
-    // FP32: two of the pieces, then in their place the third
+    // without room two of the pieces, then in their place the third
 #pragma unroll 1
-    for (int pass = 0; pass < (wide ? 2 : 1); ++pass) {
+    for (int pass = 0; pass < passes; ++pass) {
       if (from != nullptr) {
         if (pass)
           stage_third(v, n, raw, lane);
         else if (wide)
-          stage_pieces(v, n, raw, lane);
+          stage_pieces(v, n, room, raw, lane);
         else
           stage_row(v, false, bytes, raw, lane);
       }
       __syncwarp();
-      if (pass == (wide ? 1 : 0)) {
+      if (pass + 1 == passes) {
         next = t + 1 < tokens ? row(t + 1) : nullptr;
         fetch_row(v, next, bytes, lane);
       }
       const int piece = g >> 1;
-      const bool mine = from != nullptr && (wide ? (g & 1) == (t & 1) && (pass ? piece == 2 : piece < 2) : g == t);
+      const bool mine = from != nullptr && (wide ? (g & 1) == (t & 1) && (pass ? piece == 2 : piece < 4 - passes) : g == t);
       const bool clear = t == 0 && pass == 0;  // the first token also clears the other columns
       if (mine || clear) {
         const uint8_t* p = mine ? raw + (wide && !pass ? piece * n * 2 : 0) + c * 16 : zeros;
@@ -501,14 +507,13 @@ __device__ __forceinline__ void load_tokens(uint32_t (&b)[REGS], TokenSource& sr
           const uint8_t* from_half = other ? zeros : p + first;
 #pragma unroll
           for (int j = 0; j < RUNS / 2; ++j) {
-            if (j * 32 < left) {
-              const uint4 w = *reinterpret_cast<const uint4*>(from_half + j * each);
-              uint32_t* f = b + (half * (RUNS / 2) + j) * 4;
-              f[0] = w.x;
-              f[1] = w.y;
-              f[2] = w.z;
-              f[3] = w.w;
-            }
+            if (j * 32 >= left) break;
+            const uint4 w = *reinterpret_cast<const uint4*>(from_half + j * each);
+            uint32_t* f = b + (half * (RUNS / 2) + j) * 4;
+            f[0] = w.x;
+            f[1] = w.y;
+            f[2] = w.z;
+            f[3] = w.w;
           }
         }
       }

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewLaye
       if constexpr (kI4)
         i4_load_tokens<(kI4 ? MODE : 1)>(b, factor, src, row, ph > 0, n, units, raw, sh.zeros, lane);
       else
-        load_tokens<kRuns>(b, src, row, ph > 0, n, units * kUnit, raw, sh.zeros, lane);
+        load_tokens<kRuns>(b, src, row, ph > 0, a.room, n, units * kUnit, raw, sh.zeros, lane);
       return __all_sync(0xffffffffu, src.ok) != 0;
     };
     int slot = 0, rb = 0;
@@ -761,11 +761,20 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   a.slot_bytes = c1 > c2 ? c1 : c2;
   const int b1 = stage_bytes((a.d / unit + kFewWarps - 1) / kFewWarps * unit, group != 0, false);
   const int b2 = stage_bytes((a.I / unit + kFewWarps - 1) / kFewWarps * unit, group != 0, true);
-  a.stage_bytes = b1 > b2 ? b1 : b2;
-  const size_t red = static_cast<size_t>(kFewRed) * kFewWarps * step * 512 +
-                     static_cast<size_t>(kFewWarps) * a.stage_bytes;
-  a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);
-  if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
+  size_t red = 0;
+  auto plan_stages = [&](int bytes) {
+    a.stage_bytes = bytes;
+    red = static_cast<size_t>(kFewRed) * kFewWarps * step * 512 + static_cast<size_t>(kFewWarps) * bytes;
+    a.stages = static_cast<int>((kFewDynamicSmem - red) / a.slot_bytes);
+    if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
+    return a.stages;
+  };
+  const int without = plan_stages(b1 > b2 ? b1 : b2);
+  if (!group) {  // room for all three BF16 pieces of a row, unless it costs a ring slot (as at I = 2560)
+    const int pieces = b2 / 2 * 3;
+    a.room = plan_stages(b1 > pieces ? b1 : pieces) == without;
+    if (!a.room) plan_stages(b1 > b2 ? b1 : b2);
+  }
   // no more CTAs than gate|up items can exist
   const int64_t items = static_cast<int64_t>(a.T) * a.k * (a.I / 8);
   const int grid = items < sms ? static_cast<int>(items) : sms;
