@@ -602,3 +602,90 @@ def test_entries_of_the_same_experts_at_their_limits(T, d, I, group):
     for t in range(T):
         m.call(h[t:t + 1].clone(), one)
         assert torch.equal(one[0], out[t])
+
+
+def test_a_captured_step_that_forks_and_joins():
+    """Products on two streams that join before the layer, which forks again into two heads."""
+    T, d, V = 3, 512, 1001
+    m = Layer(d, 32, 4, 2, 4, 384, 64)
+    h = normal(1, T, d)
+    ws_ = [normal(s, 1, n, d, std=d ** -0.5) for s, n in ((2, d), (3, d), (4, V), (5, V))]
+    qs = [bm.beam_int4_quantize(w, group_size=64) for w in ws_]
+    a, b, x = torch.empty_like(h), torch.empty_like(h), torch.empty_like(h)
+    idx = torch.empty(T, 4, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, 4, device="cuda")
+    l1, l2 = torch.empty(T, V, device="cuda"), torch.empty(T, V, device="cuda")
+    ws = bm.few_workspace(m.shape(T))
+    square, head = bm.int4_shape(T, d, d, 64), bm.int4_shape(T, V, d, 64)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        bm.beam_int4_linear(square, h, qs[0], a)
+        with torch.cuda.stream(side):
+            bm.beam_int4_linear(square, h, qs[1], b)
+        main.wait_stream(side)
+        bm.beam_int4_linear(square, b, qs[0], x)   # behind both
+        m.call(x, a, idx, w, ws=ws)
+        side.wait_stream(main)
+        bm.beam_int4_linear(head, a, qs[2], l1)
+        with torch.cuda.stream(side):
+            bm.beam_int4_linear(head, a, qs[3], l2)
+        main.wait_stream(side)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        step()
+    for seed in (11, 12):
+        h.copy_(normal(seed, T, d))
+        for t in (a, b, x, l1, l2):
+            t.fill_(9.0)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bm.beam_moe_sync_status(ws) == bm.BEAM_OK
+        R.assert_within(b, *R.linear_ref(h, ws_[1][0], 64, False), "second branch")
+        R.assert_within(x, *R.linear_ref(b, ws_[0][0], 64, False), "after the join")
+        m.check(x, a, idx, w)
+        R.assert_within(l1, *R.linear_ref(a, ws_[2][0], 64, True), "head")
+        R.assert_within(l2, *R.linear_ref(a, ws_[3][0], 64, True), "other head")
+
+
+def test_two_host_threads_at_once():
+    import threading
+    ms = [Layer(1280, 32, 4, 2, 4, 640, 0, seed=1), Layer(1280, 32, 4, 2, 4, 640, 64, seed=2)]
+    hs = [normal(5, 4, 1280), normal(6, 7, 1280)]
+    want = [m.run(h)[0].clone() for m, h in zip(ms, hs)]
+    lw = normal(7, 1, 999, 1280, std=0.03)
+    lq = bm.beam_int4_quantize(lw, group_size=64)
+    logits = []
+    for o, h in zip(want, hs):
+        logits.append(torch.empty(h.shape[0], 999, device="cuda"))
+        bm.beam_int4_linear(bm.int4_shape(h.shape[0], 999, 1280, 64), o, lq, logits[-1])
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(m, h, o, l):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            ws, out = bm.few_workspace(m.shape(h.shape[0])), torch.empty_like(h)
+            got = torch.empty_like(l)
+            for _ in range(40):
+                m.call(h, out, ws=ws)
+                bm.beam_int4_linear(bm.int4_shape(h.shape[0], 999, 1280, 64), out, lq, got)
+                stream.synchronize()
+                if not (torch.equal(out, o) and torch.equal(got, l)):
+                    bad.append(m.group)
+            if bm.beam_moe_sync_status(ws) != bm.BEAM_OK:
+                bad.append("status")
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(ms, hs, want, logits)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
