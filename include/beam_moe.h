@@ -347,7 +347,8 @@ BEAM_API beam_status beam_moe_bias_update(const beam_moe_shape* shape, const voi
  * FP32.  (For up to 8 tokens, and in the MoE layer for any number, the activations enter as 23-bit integers with a common
  * power of two per token and K slice: exactly their BF16 values, unless an element is below 2^-14 of
  * the slice's largest, when it is off by at most 2^-22 of that.  There a token with a non-finite
- * element has NaN outputs.)
+ * element has NaN outputs; in beam_int4_linear of 9 to 16 tokens, and in the first product of the MLP,
+ * an infinite one has what the arithmetic gives, infinities of either sign or NaN.)
  *
  * Packed storage (what the kernels stream): tiles of 16 rows; in a tile, superblocks of 128
  * columns in order; a superblock is two 512-byte code blocks of 64 columns, then for each of its
@@ -410,12 +411,17 @@ BEAM_API beam_status beam_dense_forward_int4(const beam_dense_shape* shape, int3
  * shape: T <= BEAM_FEW_MAX_TOKENS and I <= 8192 besides the layer's shape rules). */
 BEAM_API size_t beam_moe_few_workspace_size(const beam_moe_shape* shape);
 
-/* beam_moe_forward for 1 to BEAM_FEW_MAX_TOKENS tokens in two launches (three for more than 10 tokens
- * where d > 5632): the same arguments and definition, with ws sized by beam_moe_few_workspace_size.  The
+/* beam_moe_forward for 1 to BEAM_FEW_MAX_TOKENS tokens in two launches (three where the token rows and
+ * two router rows, T * 2d + 8d bytes, exceed 231424: for 16 tokens from d = 5888 on, for 11 at d = 8192): the
+ * same arguments and definition, with ws sized by beam_moe_few_workspace_size.  An expert's weights are read
+ * once for each 4 of its tokens (each 2 where I > 4096; with 4-bit weights where d or I > 5120).  The
  * router's sums run in FP64 and are rounded once to FP32, so topk_idx is the definition's also on near
  * ties.  Activations between an expert's two products and expert outputs stay FP32 (the activations
  * enter the second product as three BF16 pieces) until the combine's sum is rounded to BF16: closer to
  * the definition than beam_moe_forward, which rounds both to BF16.  Results do not depend on timing.
+ * A bias of -inf masks its expert.  For few tokens it is the faster call, by 65 us at Beam's sizes and one
+ * token; layers of a few MB are faster through beam_moe_forward from 4 to 8 tokens on, and large ones
+ * where many of 12 to 16 tokens share experts.
  * The second launch is cooperative: it needs every SM for itself and runs when they are free. */
 BEAM_API beam_status beam_moe_forward_few(const beam_moe_shape* shape, const void* hidden,
                                           const float* router_w, const float* bias,
@@ -545,9 +551,9 @@ BEAM_API beam_status beam_moe_slot_rows(const beam_moe_shape* shape, const void*
 
 /* ---- diagnostics (process-wide settings) ---- */
 
-/* Limit, in nanoseconds, of every device-side wait in the expert GEMM kernels; after it
- * the kernel records BEAM_ERR_TIMEOUT, drains its own copies, frees its tensor memory and
- * returns.  Default 4e9 (4 s).  Applies to launches made after the call. */
+/* Limit, in nanoseconds, of every device-side wait in the expert GEMM kernels and the few-token kernels;
+ * after it the kernel records BEAM_ERR_TIMEOUT (beam_int4_linear and beam_dense_forward_int4: NaN
+ * outputs), drains its own copies, frees its tensor memory and returns.  Default 4e9 (4 s).  Applies to launches made after the call. */
 BEAM_API void beam_moe_set_wait_limit_ns(uint64_t ns);
 BEAM_API uint64_t beam_moe_get_wait_limit_ns(void);
 

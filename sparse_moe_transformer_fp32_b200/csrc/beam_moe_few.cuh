@@ -7,10 +7,10 @@
 // arithmetic intensity at which the tensor cores bound anything, so the design is about streaming
 // weights without a pause:
 //
-//  - one persistent CTA per SM: a producer warp moves weights into a shared-memory ring of
-//    about 190 KB with bulk copies (4 us of one SM's share of the HBM bandwidth in flight, so
-//    synchronisation between phases does not stop the stream), 8 consumer warps multiply, three
-//    finish outputs;
+//  - one persistent CTA per SM: a producer warp moves weights into a shared-memory ring (at Beam's
+//    sizes 169 KB with 4-bit weights in groups of 128, 210 KB with BF16) with bulk copies (4 us of one
+//    SM's share of the HBM bandwidth in flight, so synchronisation between phases does not stop the
+//    stream), 8 consumer warps multiply, three finish outputs;
 //  - a tile is 16 weight rows by the whole K range of the CTA; the 8 consumer warps split K.
 //    Each keeps its K slice of the token rows in registers, as B fragments of mma.sync (weights are
 //    the 16-row A operand, tokens the 8 columns), for as long as the CTA stays with the same
@@ -572,8 +572,9 @@ __device__ __forceinline__ float4 sum_pieces(float4 v) {
 // The token is a 23-bit integer per element, in three signed 8-bit digits:
 //   x = 2^(E - 21) (65536 d0 + 256 d1 + d2),  2^E <= largest of the warp's K slice < 2^(E + 1)
 // which is x exactly for every element within 2^-14 of the slice's largest, and off by at most
-// 2^-22 of the largest otherwise -- a quarter step of FP32 in the sum that holds it.  The digits of a
-// token are columns of their own, in one of three arrangements by the number of tokens (MODE = MMAs
+// 2^-22 of the largest otherwise -- a quarter step of FP32 in the sum that holds it.  (FP32 activations
+// lose up to two bits by it: of a layer's BF16 outputs 7 in 10,000 then differ from the correctly rounded
+// ones, with exact activations 3, and the error to three digits does not.)  The digits of a token are columns of their own, in one of three arrangements by the number of tokens (MODE = MMAs
 // per run of 32):
 //   MODE 1, up to 2 tokens: column 2 p + t holds digit p of token t
 //   MODE 2, up to 4: of the first MMA column 4 p + t, p = 0, 1; of the second column t digit 2
@@ -783,7 +784,8 @@ __device__ __forceinline__ void i4_load_tokens(uint32_t (&b)[REGS], I4Factor (&f
 }
 
 // Sums of i4_slice, per MMA of a run.  Digits are kept apart to the end, so that a token's result has
-// the same bits in every arrangement.
+// the same bits in every arrangement (as long as K is cut alike: the linear product of more than 5120
+// columns may take fewer CTAs to a tile for up to 2 tokens).
 template <int MODE>
 struct I4Acc {
   float v[MODE][4] = {};

@@ -267,7 +267,7 @@ __device__ void few_select(const FewLayerArgs& a, const float2* sc, uint8_t* slo
 //   by_token: an entry's column t is token t (kNoSlot where the token has other experts), so that all
 //             entries share the token fragments of gate|up;
 //   else      its columns are its tokens, entry_max at most; one more opens a second entry that reads
-//             the weights again (16 tokens that choose 8 of 64 experts at random: for 3 experts in 100).
+//             the weights again (16 tokens that choose 8 of 64 experts at random: for 4 experts in 100).
 __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewShared& sh, bool by_token) {
   const int e = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kFewWarps * 32 == kMaxE, "a thread to an expert");
@@ -318,7 +318,7 @@ __device__ void few_entries(const FewLayerArgs& a, const uint8_t* slot_of, FewSh
 // cross the GPU.  GROUP = 0: BF16 weights.  MODE: the arrangement of digits, 1 or 2 (0 for BF16).
 //
 // Bound by HBM, the bytes of the touched experts.  d = 5120, I = 2560, 64 experts, 8 chosen: BF16 1 token
-// 109 us and 16 tokens 725 (5.9 and 6.1 TB/s), 4-bit weights 8 tokens 178.  4-bit, 1 token, 42 us: 26 of
+// 114 us and 16 tokens 745 (5.5 and 6 TB/s), 4-bit weights 8 tokens 180.  4-bit, 1 token, 42 us: 26 of
 // them the bytes, 6 the selection and the first copies, 4 the exchange of the activations (the ring holds
 // 4 us of weights, and the slowest CTA's last rows take that long to reach everyone), 4 the combine.
 template <int GROUP, int MODE>
@@ -752,7 +752,8 @@ cudaError_t launch_few_layer(FewLayerArgs a, int group, int sms, cudaStream_t s)
   // Tokens of an entry: 4, or 2 where the registers of a warp do not hold the fragments of 4 (the three
   // pieces of FP32 activations; the digits of 4-bit products, and there also where there are no more
   // tokens).  With 8 the weights of an expert of 5 to 8 tokens are read once, but every 4-bit product then
-  // takes three MMAs instead of two (16 tokens over 64 experts 267 us, with 4 to an entry 249).
+  // takes three MMAs instead of two (16 tokens over 64 experts, BF16 activations: 267 us, with 4 to an entry
+  // 249).
   a.entry_max = (group ? a.T <= 2 || a.d > 5120 || a.I > 5120 : a.I > kFewMaxK / 2) ? 2 : kEntryMax;
   const int step = group ? 2 : 1;  // tiles
   a.k1 = make_ksplit(a.d / unit, group ? kI4SlotBytes : kBf16SlotBytes, step * unit_bytes);

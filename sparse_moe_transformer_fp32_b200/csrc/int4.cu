@@ -161,9 +161,9 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
 // exchange's 1.5 us.  C > 1 is for matrices with few tiles (the spread over 148 SMs would be uneven) and
 // for K ranges whose token fragments do not fit in registers.
 //
-// Bound by HBM, N K (1/2 + 2 / group) bytes, for up to 4 tokens (1 x 151936 x 5120, groups of 128: 61 us,
-// 6.6 TB/s).  From 5 tokens on by the consumers: at 8 the three MMAs of a run alone take the time in which
-// its weights arrive (84 us), at 16 the expansion to BF16 and the waits between (133 us).
+// Bound by HBM, N K (1/2 + 2 / group) bytes, for up to 4 tokens (1 x 151936 x 5120, groups of 128: 62 us,
+// 6.5 TB/s).  From 5 tokens on by the consumers: at 8 the three MMAs of a run alone take the time in which
+// its weights arrive (86 us), at 16 the expansion to BF16 and the waits between (139 us).
 //
 // Launched with programmatic stream serialisation, so that barriers are set up while the kernel before
 // drains.  Every warp that reads or writes global memory, the producer too, does so after
@@ -180,8 +180,8 @@ __host__ __device__ constexpr int lin_sets(int mode) { return mode == 4 ? 2 : 1;
 // later tile's, when it waits; three of them in turn, so that the tile before is two steps back at most.
 __host__ __device__ constexpr int lin_red(int step) { return 4 / step; }
 // Tiles of a CTA from which on a step is two tiles, for up to 4 tokens: half the waits, but twice the code
-// to fetch for a first tile (1 x 1280 x 2560 with one tile to a CTA: 3.4 us, with steps of two 3.7; 1 x 40960
-// x 5120 with 18: 20.3 and 20.0; 4 x 40960 x 5120: 25.1 and 23.8).  Beyond 4 tokens the products of a tile
+// to fetch for a first tile (1 x 1280 x 2560 with one tile to a CTA: 3.5 us, with steps of two 4.0; 1 x 40960
+// x 5120 with 18: 21.3 and 20.2; 4 x 40960 x 5120: 27.8 and 25.7).  Beyond 4 tokens the products of a tile
 // take longer than the waits, and two at a time nothing off.
 constexpr int kLinStepTiles = 4;
 
