@@ -532,7 +532,7 @@ def few_workspace(shape: beam_moe_shape, device="cuda") -> torch.Tensor:
 
 def beam_moe_forward_few(shape, hidden, router_w, bias, w_gate, w_up, w_down, out, topk_idx=None,
                          topk_w=None, ws=None, stream=None):
-    """beam_moe_forward for at most 16 tokens, in two launches."""
+    """beam_moe_forward for at most 16 tokens, in two launches (three for wide rows)."""
     T, d, E, k, I = shape.T, shape.d, shape.E, shape.top_k, shape.I
     if ws is None:
         _ptr(hidden, torch.bfloat16, "hidden", (T, d))
